@@ -40,4 +40,14 @@ from ._binding import (  # noqa: F401
     load_library,
     selected_kernel,
 )
+from .paged import (  # noqa: F401,E402
+    decode_paged_workspace_bytes,
+    ffpa_decode_paged,
+    ffpa_kv_append,
+    ffpa_page_plan,
+    ffpa_qk_norm_rope,
+    ffpa_qk_norm_rope_bwd,
+    qk_norm_rope_bwd_workspace_bytes,
+    rope_inv_freq,
+)
 from .torch_ops import ffpa_attn_func, ffpa_attn_varlen_func  # noqa: F401,E402

@@ -27,7 +27,9 @@ EXPORTED = ("ffpa_fwd", "ffpa_fwd_ex", "ffpa_fwd_varlen", "ffpa_fwd_varlen_ex", 
             "ffpa_last_device_error", "ffpa_selected_kernel", "ffpa_bwd_noalloc",
             "ffpa_fwd_fp8", "ffpa_fwd_fp8_ex", "ffpa_fwd_fp8_workspace_bytes", "ffpa_bwd_ws",
             "ffpa_bwd_ws_ex", "ffpa_bwd_workspace_bytes", "ffpa_bwd_varlen_ws", "ffpa_bwd_varlen_ws_ex",
-            "ffpa_bwd_varlen_workspace_bytes")
+            "ffpa_bwd_varlen_workspace_bytes", "ffpa_decode_paged", "ffpa_decode_paged_workspace_bytes",
+            "ffpa_qk_norm_rope", "ffpa_qk_norm_rope_bwd", "ffpa_qk_norm_rope_bwd_workspace_bytes",
+            "ffpa_kv_append", "ffpa_page_plan")
 
 KERNEL_VARIANTS = {"auto": 0, "single": 1, "pair": 2, "split": 3, "dual": 4}
 
@@ -38,6 +40,15 @@ class Options(ctypes.Structure):
     """ffpa_options of include/ffpa.h (one call's status word, wait limit, kernel, test hook)."""
     _fields_ = [("status", ctypes.c_void_p), ("wait_timeout_ns", ctypes.c_uint64),
                 ("kernel", ctypes.c_int), ("test_drop_first_copy", ctypes.c_int)]
+
+
+class Rope(ctypes.Structure):
+    """ffpa_rope of include/ffpa.h (norm weights, positions and frequencies of one call)."""
+    _fields_ = [("positions", ctypes.c_void_p), ("position_str", ctypes.c_int64 * 2),
+                ("position_bits", ctypes.c_int), ("rot_dim", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
+                ("interleaved", ctypes.c_int), ("rope_scale", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_f32", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 class FFPAError(RuntimeError):
@@ -118,6 +129,21 @@ def load_library(path: str | Path | None = None) -> ctypes.CDLL:
     # ffpa_bwd without the delta argument
     lib.ffpa_bwd_noalloc.argtypes = sigs["ffpa_bwd"][:9] + sigs["ffpa_bwd"][10:]
     lib.ffpa_bwd_noalloc.restype = I
+    L, Z, R = ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(Rope)
+    paged = {
+        "ffpa_decode_paged": [P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P, L, P, P, I, P, Z, P, O],
+        "ffpa_qk_norm_rope": [P, P, P, P, I, I, I, I, I, I, P, P, P, P, R, P],
+        "ffpa_qk_norm_rope_bwd": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, P, P, R, P, Z, P],
+        "ffpa_kv_append": [P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P, P, P, P, R, P, O],
+        "ffpa_page_plan": [P, L, I, I, P, P, P, I, P, I, I, P, P, P, P, P, P, O],
+    }
+    for name, args in paged.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = I
+    lib.ffpa_decode_paged_workspace_bytes.argtypes = [I, I, I]
+    lib.ffpa_decode_paged_workspace_bytes.restype = Z
+    lib.ffpa_qk_norm_rope_bwd_workspace_bytes.argtypes = [I]
+    lib.ffpa_qk_norm_rope_bwd_workspace_bytes.restype = Z
     lib.ffpa_status_string.argtypes = [I]
     lib.ffpa_status_string.restype = ctypes.c_char_p
     lib.ffpa_last_device_error.argtypes = [P]

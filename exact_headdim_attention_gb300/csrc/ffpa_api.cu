@@ -10,7 +10,7 @@
 #include <cstdint>
 #include <mutex>
 
-#include "ffpa_common.cuh"
+#include "ffpa_paged.cuh"
 
 // =====================================================================
 // Host side: validation, planning, tensor maps, launch.
@@ -574,6 +574,17 @@ DeviceScope::DeviceScope(int dev) {
 
 DeviceScope::~DeviceScope() {
   if (restore_) ctx_fns().set(saved_);
+}
+
+ffpa_status call_device(std::initializer_list<const void*> ptrs, int* dev) { return check_devices(ptrs, dev); }
+
+ffpa_status call_status(int dev, const ffpa_options* options, int** err, int* sms) {
+  CallOpts o;
+  if (read_opts(options, &o) != FFPA_OK) return FFPA_ERR_INVALID;
+  const ffpa_status st = device_status_word(dev, o, err);
+  if (st != FFPA_OK) return st;
+  *sms = device_facts(dev).sms;
+  return *sms > 0 ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
 // Kernels whose shared-memory limit was raised, per device (set-once facts).

@@ -1,0 +1,161 @@
+#pragma once
+// RMS norm of query and key heads with the rotation by position: what the
+// forward, the cache append and the backward share.
+//
+//   y = x * rsqrt(mean(x^2) + eps) * w           (x when there is no weight)
+//   pair i of the first rot columns, angle t = position * inv_freq[i]:
+//     (a, b) -> rope_scale * (a cos t - b sin t, b cos t + a sin t)
+//   pairs (i, rot/2 + i), or (2i, 2i+1) when interleaved; later columns stay.
+//
+// A row (one head of one token) belongs to LPR lanes.  A lane holds ITER
+// chunks of 2 VEC values: the two VEC-wide vectors that hold VEC whole pairs,
+// so that a rotation never leaves its lane, or 2 VEC columns behind the
+// rotated ones.
+//
+// Angles are taken in turns, as 64-bit fixed-point fractions: position times
+// frequency wraps there as the angle does, so that far positions need neither
+// a table nor 64-bit floating point per angle (off by 2^-32 turns, and by the
+// rounding of the frequency itself to a double, 2^-52 of the angle).
+#include "ffpa_paged.cuh"
+
+namespace ffpa {
+
+struct RopeTensor {
+  const char* x;       // input rows
+  char* y;             // output rows
+  int64_t xs[3], ys[3];   // byte strides (b, h, n)
+  const void* w;       // norm weight [D], or NULL
+  int H;
+};
+
+struct RopeParams {
+  RopeTensor t[2];     // queries, keys
+  const char* pos;
+  int64_t pos_s[2];    // byte strides (b, n)
+  const double* inv_freq;
+  int pos64, rot, w32, B, N, D;
+  float eps, rope_scale;
+  int heads_per[2];    // heads of one work item
+  int64_t items[2];    // work items of queries and of keys
+  int chunks[2];       // head chunks of a token
+  // append (keys go to pages, values are copied): slots == NULL otherwise
+  const int64_t* slots;
+  int64_t n_slots, slot_page;
+  char *kc, *vc;
+  const char* v;
+  int64_t vs[2], kcs[3], vcs[3];   // byte strides (h, n); (page, slot, h)
+  int64_t items_v;
+  int* err;
+  // backward
+  const char* g[2];    // gradients of the outputs
+  int64_t gs[2][3];
+  float* part[2];      // per-block weight gradients
+  void* dw[2];
+  int blocks[2];
+};
+
+// The vector width that the pairs' halves and the row's end allow.
+inline int rope_vec(int D, int rot) { return D % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
+
+template <int VEC>
+struct RopeChunk {
+  int a, b;      // columns of the two vectors
+  bool pair;     // rotated
+  bool live;
+};
+
+template <int VEC, bool INTER>
+__device__ __forceinline__ RopeChunk<VEC> rope_chunk(int j, int D, int rot) {
+  RopeChunk<VEC> c;
+  const int np = rot / (2 * VEC);
+  c.live = j < D / (2 * VEC);
+  c.pair = j < np;
+  if (c.pair) {
+    c.a = INTER ? 2 * j * VEC : j * VEC;
+    c.b = INTER ? c.a + VEC : rot / 2 + j * VEC;
+  } else {
+    c.a = rot + (j - np) * 2 * VEC;
+    c.b = c.a + VEC;
+  }
+  return c;
+}
+
+template <int VEC>
+struct alignas(VEC * 2) Raw {
+  uint32_t u[VEC / 2];
+};
+
+template <bool F16, int VEC>
+__device__ __forceinline__ void widen(const Raw<VEC>& r, float* x) {
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    const float2 f = unpack2<F16>(r.u[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <bool F16, int VEC>
+__device__ __forceinline__ Raw<VEC> narrow(const float* x) {
+  Raw<VEC> r;
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) r.u[i] = pack2<F16>(x[2 * i], x[2 * i + 1]);
+  return r;
+}
+
+template <bool F16, int VEC>
+__device__ __forceinline__ void load_weight(const void* w, int w32, int col, float* x) {
+  if (w32) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = static_cast<const float*>(w)[col + i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const uint16_t h = static_cast<const uint16_t*>(w)[col + i];
+      x[i] = unpack2<F16>(h).x;
+    }
+  }
+}
+
+// A frequency in turns per position, as a fraction of 2^64 (whole turns drop out).
+__device__ __forceinline__ long long freq_turns(double inv_freq) {
+  double f = inv_freq * 0.15915494309189534561;   // 1 / (2 pi)
+  f -= rint(f);
+  return __double2ll_rn(f * 18446744073709551616.0);
+}
+__device__ __forceinline__ void turn(long long pos, long long freq, float scale, float& c, float& s) {
+  const unsigned long long t = static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(freq);
+  const int hi = static_cast<int>(static_cast<unsigned>(t >> 32));   // turns in [-1/2, 1/2), times 2^32
+  sincospif(static_cast<float>(hi) * 4.656612873077393e-10f, &s, &c);   // 2 hi / 2^32
+  c *= scale;
+  s *= scale;
+}
+
+__device__ __forceinline__ long long position_of(const RopeParams& P, int b, int n) {
+  const char* p = P.pos + b * P.pos_s[0] + n * P.pos_s[1];
+  return P.pos64 ? *reinterpret_cast<const long long*>(p) : *reinterpret_cast<const int*>(p);
+}
+
+// (a, b) of a chunk rotated by +t or, BACK, by -t; the vectors hold pairs
+// (a[i], b[i]), or interleaved ones in the order a then b.
+template <int VEC, bool INTER, bool BACK>
+__device__ __forceinline__ void rotate(float* x, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : VEC + i;
+    const float a = x[ia], b = x[ib], sn = BACK ? -s[i] : s[i];
+    x[ia] = a * c[i] - b * sn;
+    x[ib] = b * c[i] + a * sn;
+  }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int d = LPR / 2; d > 0; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+  return x;
+}
+
+// Host: the checks of ffpa_rope and the parameters that the passes share.
+ffpa_status rope_params(const ffpa_rope* r, ffpa_dtype dt, int B, int Hq, int Hkv, int N, int D, RopeParams* P);
+
+}  // namespace ffpa

@@ -1,0 +1,288 @@
+// Backward of the head norm with rotation.  With g the gradient of a row's
+// output, g' = g rotated by the opposite angle (times rope_scale), xn = x r,
+// r = rsqrt(mean(x^2) + eps):
+//
+//   dw += g' xn (over all rows),   dx = r (w g' - xn mean(w g' xn)),
+//
+// or dx = g' where there is no weight.  x is read again and r recomputed (a
+// row sum in registers) instead of being stored by the forward.  Each row is
+// read twice (x, g) and written once: the memory's bandwidth is the bound.
+//
+// dw is summed in fp32 in a fixed order (no atomics): each lane keeps its
+// columns' sums over its rows in registers, a block adds its lanes and writes
+// one row of partial sums, a second launch adds the blocks.
+#include "ffpa_rope.cuh"
+
+namespace ffpa {
+namespace {
+
+constexpr int RB_THREADS = 256;
+constexpr int RB_BLOCKS_MAX = 512;   // blocks of queries and keys together
+
+template <bool F16, int VEC, int LPR, int ITER, bool INTER>
+__global__ void __launch_bounds__(RB_THREADS) rope_bwd_kernel(const RopeParams P) {
+  constexpr int GROUPS = RB_THREADS / LPR, COLS = LPR * 2 * VEC * ITER;
+  __shared__ float sums[GROUPS][COLS];
+  const int lane = threadIdx.x % LPR, row = threadIdx.x / LPR;
+  const int wt = blockIdx.x < P.blocks[0] ? 0 : 1;
+  const int block = blockIdx.x - (wt ? P.blocks[0] : 0);
+  const RopeTensor& t = P.t[wt];
+  RopeChunk<VEC> ch[ITER];
+  long long freq[ITER][VEC];
+  float w[ITER][2 * VEC], dw[ITER][2 * VEC];
+#pragma unroll
+  for (int k = 0; k < ITER; ++k) {
+    ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      freq[k][i] = ch[k].live && ch[k].pair ? freq_turns(P.inv_freq[(lane + k * LPR) * VEC + i]) : 0;
+#pragma unroll
+    for (int i = 0; i < 2 * VEC; ++i) dw[k][i] = 0.0f;
+    if (ch[k].live && t.w) {
+      load_weight<F16, VEC>(t.w, P.w32, ch[k].a, w[k]);
+      load_weight<F16, VEC>(t.w, P.w32, ch[k].b, w[k] + VEC);
+    }
+  }
+  const int64_t stride = (int64_t)P.blocks[wt] * GROUPS;
+  // Whole warps stay in the loop: the lanes of a row talk through shuffles.
+  for (int64_t first = (int64_t)block * GROUPS + (threadIdx.x / 32) * (32 / LPR); first < P.items[wt]; first += stride) {
+    const int64_t item = first + (threadIdx.x % 32) / LPR;
+    const bool in = item < P.items[wt];
+    const int64_t token = in ? item / P.chunks[wt] : 0;
+    const int h0 = in ? (int)(item % P.chunks[wt]) * P.heads_per[wt] : 0;
+    const int h1 = in ? min(t.H, h0 + P.heads_per[wt]) : h0;
+    const int b = (int)(token / P.N), n = (int)(token % P.N);
+    float cs[ITER][VEC], sn[ITER][VEC];
+    const long long pos = P.rot ? position_of(P, b, n) : 0;
+#pragma unroll
+    for (int k = 0; k < ITER; ++k) {
+      if (!ch[k].live || !ch[k].pair) continue;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) turn(pos, freq[k][i], P.rope_scale, cs[k][i], sn[k][i]);
+    }
+    for (int i = 0; i < P.heads_per[wt]; ++i) {
+      const int h = h0 + i;
+      const bool on = h < h1;
+      float g[ITER][2 * VEC], x[ITER][2 * VEC];
+      float sq = 0.0f, dot = 0.0f;
+      if (on) {
+        const char* gp = P.g[wt] + b * P.gs[wt][0] + h * P.gs[wt][1] + n * P.gs[wt][2];
+        const char* xp = t.x + b * t.xs[0] + h * t.xs[1] + n * t.xs[2];
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+          if (!ch[k].live) continue;
+          widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(gp + ch[k].a * 2), g[k]);
+          widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(gp + ch[k].b * 2), g[k] + VEC);
+          if (ch[k].pair) rotate<VEC, INTER, true>(g[k], cs[k], sn[k]);
+          if (t.w) {
+            widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(xp + ch[k].a * 2), x[k]);
+            widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(xp + ch[k].b * 2), x[k] + VEC);
+#pragma unroll
+            for (int j = 0; j < 2 * VEC; ++j) {
+              sq += x[k][j] * x[k][j];
+              dot += w[k][j] * g[k][j] * x[k][j];
+            }
+          }
+        }
+      }
+      if (t.w) {
+        sq = row_sum<LPR>(sq);
+        dot = row_sum<LPR>(dot);
+      }
+      if (!on) continue;
+      const float r = rsqrtf(sq / P.D + P.eps);
+      const float back = r * r * dot / P.D;      // r mean(w g' xn)
+      char* dst = t.y + b * t.ys[0] + h * t.ys[1] + n * t.ys[2];
+#pragma unroll
+      for (int k = 0; k < ITER; ++k) {
+        if (!ch[k].live) continue;
+        if (t.w) {
+#pragma unroll
+          for (int j = 0; j < 2 * VEC; ++j) {
+            dw[k][j] += g[k][j] * (x[k][j] * r);
+            g[k][j] = r * (w[k][j] * g[k][j] - x[k][j] * back);
+          }
+        }
+        *reinterpret_cast<Raw<VEC>*>(dst + ch[k].a * 2) = narrow<F16, VEC>(g[k]);
+        *reinterpret_cast<Raw<VEC>*>(dst + ch[k].b * 2) = narrow<F16, VEC>(g[k] + VEC);
+      }
+    }
+  }
+  if (!t.w) return;
+#pragma unroll
+  for (int k = 0; k < ITER; ++k) {
+    if (!ch[k].live) continue;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      sums[row][ch[k].a + i] = dw[k][i];
+      sums[row][ch[k].b + i] = dw[k][VEC + i];
+    }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < P.D; d += RB_THREADS) {
+    float s = 0.0f;
+    for (int i = 0; i < GROUPS; ++i) s += sums[i][d];
+    P.part[wt][(int64_t)block * P.D + d] = s;
+  }
+}
+
+// dw[wt][d] = sum of the blocks' partial rows: 32 columns a block, 32 threads a column.
+template <bool F16>
+__global__ void __launch_bounds__(1024) weight_sum_kernel(const RopeParams P) {
+  const int wt = blockIdx.y;
+  if (!P.dw[wt]) return;
+  const int col = threadIdx.x % 32, row = threadIdx.x / 32, d = blockIdx.x * 32 + col;
+  __shared__ float sums[32][33];
+  float s = 0.0f;
+  if (d < P.D)
+    for (int i = row; i < P.blocks[wt]; i += 32) s += P.part[wt][(int64_t)i * P.D + d];
+  sums[row][col] = s;
+  __syncthreads();
+  // A warp now takes one column's 32 sums.
+  s = sums[col][row];
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
+  const int out = blockIdx.x * 32 + row;
+  if (col == 0 && out < P.D) {
+    if (P.w32)
+      static_cast<float*>(P.dw[wt])[out] = s;
+    else
+      store16<F16>(static_cast<char*>(P.dw[wt]) + out * 2, s);
+  }
+}
+
+template <bool F16, int VEC, int LPR, int ITER>
+ffpa_status launch_bwd_as(RopeParams& P, bool inter, int sms, cudaStream_t stream) {
+  const int64_t groups = RB_THREADS / LPR;
+  // Blocks in proportion to the rows, some two per SM in all.
+  const int64_t all = P.items[0] + P.items[1];
+  const int64_t most = sms * 2 < RB_BLOCKS_MAX - 2 ? sms * 2 : RB_BLOCKS_MAX - 2;
+  for (int i = 0; i < 2; ++i) {
+    int64_t n = (P.items[i] + groups - 1) / groups;
+    const int64_t share = (most * P.items[i] + all - 1) / all;
+    if (n > share) n = share;
+    P.blocks[i] = (int)(n < 1 ? 1 : n);
+  }
+  P.part[1] = P.part[0] + (int64_t)P.blocks[0] * P.D;
+  const int grid = P.blocks[0] + P.blocks[1];
+  if (inter)
+    rope_bwd_kernel<F16, VEC, LPR, ITER, true><<<grid, RB_THREADS, 0, stream>>>(P);
+  else
+    rope_bwd_kernel<F16, VEC, LPR, ITER, false><<<grid, RB_THREADS, 0, stream>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
+  if (P.dw[0] || P.dw[1]) {
+    weight_sum_kernel<F16><<<dim3((P.D + 31) / 32, 2), 1024, 0, stream>>>(P);
+    if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
+  }
+  return FFPA_OK;
+}
+
+template <bool F16>
+ffpa_status launch_bwd_rope(RopeParams& P, bool inter, int sms, cudaStream_t stream) {
+  const int64_t tokens = (int64_t)P.B * P.N;
+  for (int i = 0; i < 2; ++i) {
+    int per = 8;
+    while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
+    P.heads_per[i] = per;
+    P.chunks[i] = (P.t[i].H + per - 1) / per;
+    P.items[i] = tokens * P.chunks[i];
+  }
+  if (rope_vec(P.D, P.rot) == 8) {
+    const int n = P.D / 16;
+    if (n <= 4) return launch_bwd_as<F16, 8, 4, 1>(P, inter, sms, stream);
+    if (n <= 8) return launch_bwd_as<F16, 8, 8, 1>(P, inter, sms, stream);
+    if (n <= 16) return launch_bwd_as<F16, 8, 16, 1>(P, inter, sms, stream);
+    if (n <= 32) return launch_bwd_as<F16, 8, 32, 1>(P, inter, sms, stream);
+    return launch_bwd_as<F16, 8, 32, 2>(P, inter, sms, stream);
+  }
+  const int n = P.D / 8;
+  if (n <= 16) return launch_bwd_as<F16, 4, 16, 1>(P, inter, sms, stream);
+  if (n <= 32) return launch_bwd_as<F16, 4, 32, 1>(P, inter, sms, stream);
+  if (n <= 64) return launch_bwd_as<F16, 4, 32, 2>(P, inter, sms, stream);
+  return launch_bwd_as<F16, 4, 32, 4>(P, inter, sms, stream);
+}
+
+}  // namespace
+}  // namespace ffpa
+
+extern "C" {
+
+size_t ffpa_qk_norm_rope_bwd_workspace_bytes(int D) {
+  return D < 64 || D > 1024 || D % 8 != 0 ? 0 : (size_t)ffpa::RB_BLOCKS_MAX * D * 4;
+}
+
+ffpa_status ffpa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq,
+                                  void* dk, void* dq_weight, void* dk_weight, ffpa_dtype dt, int B, int Hq, int Hkv,
+                                  int N, int D, const int64_t dqo_str[4], const int64_t dko_str[4],
+                                  const int64_t q_str[4], const int64_t k_str[4], const int64_t dq_str[4],
+                                  const int64_t dk_str[4], const ffpa_rope* rope, void* workspace,
+                                  size_t workspace_bytes, ffpa_stream_t stream) {
+  using namespace ffpa;
+  RopeParams P{};
+  ffpa_status st = rope_params(rope, dt, B, Hq, Hkv, N, D, &P);
+  if (st != FFPA_OK) return st;
+  const void* w[2] = {rope->q_weight, rope->k_weight};
+  void* dw[2] = {dq_weight, dk_weight};
+  const bool sums = w[0] || w[1];
+  for (int i = 0; i < 2; ++i)
+    if ((w[i] != nullptr) != (dw[i] != nullptr) || !on_boundary(dw[i], rope->weight_f32 ? 4 : 2)) return FFPA_ERR_INVALID;
+  const bool rows = B > 0 && N > 0;
+  if (!rows && !sums) return FFPA_OK;
+  if (rows && (!dq_out || !dk_out || !q || !k || !dq || !dk || !dqo_str || !dko_str || !q_str || !k_str || !dq_str ||
+               !dk_str))
+    return FFPA_ERR_INVALID;
+  if (rows && (!rows_ok(dqo_str, {B, Hq, N, D}) || !rows_ok(q_str, {B, Hq, N, D}) || !rows_ok(dq_str, {B, Hq, N, D}) ||
+               !rows_ok(dko_str, {B, Hkv, N, D}) || !rows_ok(k_str, {B, Hkv, N, D}) ||
+               !rows_ok(dk_str, {B, Hkv, N, D})))
+    return FFPA_ERR_INVALID;
+  if (rows && (!on_boundary(dq_out, 16) || !on_boundary(dk_out, 16) || !on_boundary(q, 16) || !on_boundary(k, 16) ||
+               !on_boundary(dq, 16) || !on_boundary(dk, 16)))
+    return FFPA_ERR_INVALID;
+  if (sums && rows &&
+      (!workspace || !on_boundary(workspace, 16) || workspace_bytes < ffpa_qk_norm_rope_bwd_workspace_bytes(D)))
+    return FFPA_ERR_INVALID;
+  int dev = 0;
+  const bool turns = rows && rope->rot_dim > 0;
+  auto part = [&](const void* p) { return rows ? p : nullptr; };
+  st = call_device({part(dq_out), part(dk_out), part(q), part(k), part(dq), part(dk), dw[0], dw[1], w[0], w[1],
+                    turns ? rope->positions : nullptr, turns ? rope->inv_freq : nullptr,
+                    rows && sums ? workspace : nullptr},
+                   &dev);
+  if (st != FFPA_OK) return st;
+  DeviceScope scope(dev);
+  if (!scope.ok()) return FFPA_ERR_CUDA;
+  int sms = 0;
+  if ((st = call_status(dev, nullptr, &P.err, &sms)) != FFPA_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!rows) {
+    // No row: the weights' gradients are sums over nothing.
+    for (int i = 0; i < 2; ++i)
+      if (dw[i] && cudaMemsetAsync(dw[i], 0, (size_t)D * (rope->weight_f32 ? 4 : 2), s) != cudaSuccess) {
+        cudaGetLastError();
+        return FFPA_ERR_CUDA;
+      }
+    return FFPA_OK;
+  }
+  const void* x[2] = {q, k};
+  const void* g[2] = {dq_out, dk_out};
+  void* y[2] = {dq, dk};
+  const int64_t* xs[2] = {q_str, k_str};
+  const int64_t* gs[2] = {dqo_str, dko_str};
+  const int64_t* ys[2] = {dq_str, dk_str};
+  for (int i = 0; i < 2; ++i) {
+    P.t[i].x = static_cast<const char*>(x[i]);
+    P.t[i].y = static_cast<char*>(y[i]);
+    P.g[i] = static_cast<const char*>(g[i]);
+    P.dw[i] = dw[i];
+    for (int j = 0; j < 3; ++j) {
+      P.t[i].xs[j] = xs[i][j] * 2;
+      P.t[i].ys[j] = ys[i][j] * 2;
+      P.gs[i][j] = gs[i][j] * 2;
+    }
+  }
+  P.part[0] = static_cast<float*>(workspace);
+  return dt == FFPA_FP16 ? launch_bwd_rope<true>(P, rope->interleaved != 0, sms, s)
+                         : launch_bwd_rope<false>(P, rope->interleaved != 0, sms, s);
+}
+
+}  // extern "C"

@@ -469,6 +469,172 @@ ffpa_status ffpa_bwd_noalloc(const void* q, const void* k, const void* v, const 
                              const float* scale, int is_causal, int enable_gqa,
                              ffpa_stream_t stream);
 
+/*
+ * Generation over a paged key/value cache: one step plans the pages of the new
+ * tokens (ffpa_page_plan), stores their keys and values (ffpa_kv_append) and
+ * attends (ffpa_decode_paged).  The cache is two tensors k_cache, v_cache
+ * [num_pages, page_size, Hkv, D] with any element strides (page, slot, head,
+ * d) that follow the rules above; a slot is page * page_size + index in page.
+ * page_size is any positive number.
+ *
+ * Page numbers, slots and lengths live on the device and cannot be checked by
+ * the host.  The kernels check them: one that is out of range is never used
+ * as an address, and the call's status word (ffpa_options.status, or the
+ * device's fallback word) records FFPA_ERR_INVALID.  The other options have
+ * no effect on these entry points.
+ */
+
+/*
+ * Attention of one new token per request over the paged cache:
+ *
+ *     o[b,h] = sum_n softmax_n(scale * q[b,h] . K[n]) V[n],  0 <= n < seq_lens[b]
+ *
+ * with key n of request b in slot n % page_size of page
+ * block_table[b][n / page_size] and query head h reading key head
+ * h / (Hq / Hkv).
+ *
+ *   q, o [B, Hq, D] (strides b, h, d); lse [B, Hq] fp32 contiguous or NULL.
+ *   block_table: int32 [B, max_pages], rows table_str elements apart.
+ *     Entries at and behind ceil(seq_lens[b] / page_size) are not read.
+ *   seq_lens: int32 [B].  A request of length 0 gets o = 0 and lse = -inf.
+ *     A negative length counts as 0, one above max_pages * page_size as that;
+ *     both are reported (see above).  A key whose page is not in
+ *     [0, num_pages) is reported and counts as a key and value of zeros.
+ *   workspace: device memory of q's device, 256-byte aligned, of at least
+ *     ffpa_decode_paged_workspace_bytes(Hq, Hkv, D) bytes, whatever the batch
+ *     and the lengths; its contents do not matter before and after.  Calls
+ *     that may overlap on the GPU need one each.
+ *
+ * D a multiple of 8 from 64 to 1024 (else FFPA_ERR_UNSUPPORTED); max_pages *
+ * page_size at most 0x7fff0000.  Other checks and error codes as for
+ * ffpa_fwd.  The result does not depend on the order in which the GPU runs
+ * the blocks.  Two launches on `stream`; no allocation, no synchronisation.
+ */
+size_t ffpa_decode_paged_workspace_bytes(int Hq, int Hkv, int D);
+ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                              ffpa_dtype dt, int B, int Hq, int Hkv, int D, int num_pages, int page_size,
+                              int max_pages, const int64_t q_str[3], const int64_t k_str[4],
+                              const int64_t v_str[4], const int64_t o_str[3], const int32_t* block_table,
+                              int64_t table_str, const int32_t* seq_lens, const float* scale, int enable_gqa,
+                              void* workspace, size_t workspace_bytes, ffpa_stream_t stream,
+                              const ffpa_options* options);
+
+/*
+ * RMS norm of every query and key head and the rotation by position, in one
+ * pass.  For a row x (one head of one token) at position p:
+ *
+ *   y = x * w / sqrt(mean(x^2) + eps)                 (y = x without a weight)
+ *   pair i < rot_dim / 2, t = p * inv_freq[i]:
+ *     (y_a, y_b) -> rope_scale * (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ *
+ * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved;
+ * columns from rot_dim on are not rotated.  fp32 arithmetic, rounded once;
+ * an angle is off by at most 2^-31 turns and 2^-52 of its size, so positions
+ * of millions lose nothing.  Scaled frequencies for long contexts come in through inv_freq and
+ * rope_scale.
+ */
+typedef struct ffpa_rope {
+  const void* positions;    /* device int32 or int64 [B, N], element strides position_str */
+  int64_t position_str[2];
+  int position_bits;        /* 32 or 64 */
+  int rot_dim;              /* rotated columns: 0 (no rotation; positions and inv_freq unused) .. D, a multiple of 8 */
+  const double* inv_freq;   /* device, [rot_dim / 2] contiguous: radians per position */
+  int interleaved;
+  float rope_scale;         /* factor on the rotated columns (1 for none) */
+  const void* q_weight;     /* device [D] contiguous, or NULL: queries are not normed */
+  const void* k_weight;     /* device [D] contiguous, or NULL: keys are not normed */
+  int weight_f32;           /* the weights are fp32 (else of the rows' type) */
+  float eps;
+} ffpa_rope;
+
+/*
+ *   q, q_out [B, Hq, N, D]; k, k_out [B, Hkv, N, D] with strides (b, h, n, d).
+ *     An output may be its own input (same pointer and strides); otherwise
+ *     outputs must not overlap inputs.
+ *
+ * Packed [T, H, D] rows are B = 1, N = T with their strides in this order.
+ * Checks as for ffpa_fwd (D % 8 == 0); rot_dim, eps and rope_scale outside
+ * the ranges above: FFPA_ERR_INVALID.  One launch on `stream`.
+ */
+ffpa_status ffpa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, ffpa_dtype dt, int B, int Hq,
+                              int Hkv, int N, int D, const int64_t q_str[4], const int64_t k_str[4],
+                              const int64_t qo_str[4], const int64_t ko_str[4], const ffpa_rope* rope,
+                              ffpa_stream_t stream);
+
+/*
+ * Its backward: the gradients of sum(q_out * dq_out) + sum(k_out * dk_out)
+ * with respect to q, k and the norm weights.
+ *
+ *   dq_out, q, dq [B, Hq, N, D]; dk_out, k, dk [B, Hkv, N, D].
+ *   dq_weight, dk_weight: [D] contiguous, of the weights' type; NULL exactly
+ *     where the weight is.  Sums over all rows in fp32, in a fixed order.
+ *   workspace: as for ffpa_decode_paged, 16-byte aligned, of at least
+ *     ffpa_qk_norm_rope_bwd_workspace_bytes(D) bytes; not used (NULL is taken)
+ *     without weights.
+ *
+ * Outputs must not overlap inputs.  B * N == 0 writes zero weight gradients.
+ * One launch, or two with weights.
+ */
+size_t ffpa_qk_norm_rope_bwd_workspace_bytes(int D);
+ffpa_status ffpa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq,
+                                  void* dk, void* dq_weight, void* dk_weight, ffpa_dtype dt, int B, int Hq, int Hkv,
+                                  int N, int D, const int64_t dqo_str[4], const int64_t dko_str[4],
+                                  const int64_t q_str[4], const int64_t k_str[4], const int64_t dq_str[4],
+                                  const int64_t dk_str[4], const ffpa_rope* rope, void* workspace,
+                                  size_t workspace_bytes, ffpa_stream_t stream);
+
+/*
+ * ffpa_qk_norm_rope for a step that serves: token t's keys (normed and
+ * rotated) and values go to slot slots[t] of the cache, its queries to q_out.
+ *
+ *   q, q_out [T, Hq, D] (q NULL: there are no queries), k, v [T, Hkv, D],
+ *     strides (t, h, d); k_cache, v_cache as above.  rope as above, with
+ *     positions [1, T]; rot_dim = 0 and no weights store k as it is.
+ *   slots: int64 [T] contiguous.  A negative slot is padding: nothing is
+ *     stored for that token (its queries are computed all the same).  One at or beyond
+ *     num_pages * page_size is reported and not stored.  Slots are distinct:
+ *     of two tokens with one slot, which is stored is not defined.
+ *
+ * q_out may be q.  One launch on `stream`.
+ */
+ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                           ffpa_dtype dt, int T, int Hq, int Hkv, int D, int num_pages, int page_size,
+                           const int64_t q_str[3], const int64_t k_str[3], const int64_t v_str[3],
+                           const int64_t qo_str[3], const int64_t kc_str[4], const int64_t vc_str[4],
+                           const int64_t* slots, const ffpa_rope* rope, ffpa_stream_t stream,
+                           const ffpa_options* options);
+
+/*
+ * The page plan of one step.  Request b holds seq_lens[b] tokens, in the first
+ * ceil(seq_lens[b] / page_size) pages of row b of block_table, and gets
+ * new_lens[b] more (0: it waits).  Pages for them come off the end of the free
+ * list free_pages[0 .. free_count[0]), in the order of the requests and then
+ * of their pages, and are entered in the table.
+ *
+ *   block_table: int32 [B, max_pages], rows table_str apart; only the entries
+ *     of new pages are written.
+ *   seq_lens, new_lens: int32 [B]; free_pages: int32 [n_free]; free_count:
+ *     int32 [1].  These are not written: a call with the same inputs writes
+ *     the same results.
+ *   slots (int64), positions (int32) [tokens]: the new tokens of request 0,
+ *     then 1, ...; behind the last one -1 and 0.
+ *   cu_seqlens: int32 [B + 1], cumulative new lengths.
+ *   seq_lens_out: int32 [B], lengths with the new tokens; free_count_out:
+ *     int32 [1].  Neither may be an input's buffer.
+ *
+ * When the free list runs out, or a request outgrows its row of the table,
+ * the tokens without a page get slot -1 (and new table entries -1),
+ * seq_lens_out counts the tokens that have one, and the call is reported.  So
+ * are more than `tokens` new tokens (those beyond are not written and
+ * cu_seqlens stops there), negative lengths (taken as 0) and a free_count
+ * outside [0, n_free].  One launch on `stream`.
+ */
+ffpa_status ffpa_page_plan(int32_t* block_table, int64_t table_str, int B, int max_pages, const int32_t* seq_lens,
+                           const int32_t* new_lens, const int32_t* free_pages, int n_free, const int32_t* free_count,
+                           int page_size, int tokens, int64_t* slots, int32_t* positions, int32_t* cu_seqlens,
+                           int32_t* seq_lens_out, int32_t* free_count_out, ffpa_stream_t stream,
+                           const ffpa_options* options);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* ffpa_status_string(ffpa_status status);
 
