@@ -587,6 +587,12 @@ ffpa_status call_status(int dev, const ffpa_options* options, int** err, int* sm
   return *sms > 0 ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
+ffpa_status encode_rows(CUtensorMap* map, ffpa_dtype dt, int rank, const void* base, const uint64_t* dims,
+                        const uint64_t* stride_bytes, const uint32_t* box) {
+  return encode_map(map, dt == FFPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                    base, dims, stride_bytes, box);
+}
+
 // Kernels whose shared-memory limit was raised, per device (set-once facts).
 ffpa_status set_smem_attr_once(const void* fn, int device, int bytes) {
   struct Entry {

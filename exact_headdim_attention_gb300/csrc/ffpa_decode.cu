@@ -13,27 +13,40 @@
 //    host needs no lengths.  A pair that ends inside its CTA is written at
 //    once; a pair cut between CTAs leaves fp32 partial sums with their maximum
 //    and sum, which the second launch joins in the order of the CTAs.
-//  - K and V tiles (T keys of D columns, about 33 KB) alternate in a ring of
-//    shared-memory slots filled by 16-byte asynchronous copies: a row may lie in any page, so
-//    page sizes, strides and tails need no special path.  Rows are 16 bytes
-//    longer than D so that the matrix loads meet no bank conflict.
-//  - The products run with keys (then columns of V) as the 16 rows of
-//    mma.m16n8k16 and the heads as its 8 columns: K and V are the operands
-//    read once, and 8 heads cost one instruction per 256 elements of K.  A warp
-//    owns 64 columns of D in both products (WD warps; WK groups of them share
-//    the keys when D is small), the scores are summed over the warps in shared
-//    memory, and one pass keeps the running maximum and sum in fp32.
-//    P is rounded to the input type, as in the forward kernels; the sum is
-//    taken over the unrounded values.
+//  - Two rings of shared-memory tiles, one of K and one of V (some 200 KB, all
+//    but the tiles in work in flight), are kept full by warps of their own.
+//    Where pages hold a multiple of 8 keys a tile arrives as tensor boxes of
+//    up to T rows of one page, with the 128-byte swizzle that the matrix
+//    loads want; other page sizes take 16-byte asynchronous copies into the same
+//    layout.  (One bulk copy per row was slower: an SM starts one every 45 to 64
+//    cycles, 1.65 TB/s with the 256-byte rows of D = 128.)
+//  - Keys (then columns of V) are the 16 rows of mma.m16n8k16 and the heads its
+//    8 columns: K and V are the operands read once, and up to 8 heads cost one
+//    instruction per 256 elements.  Eight warps make a team.  For the scores a
+//    warp takes 16 keys and a part of D; for the output it takes 32 keys and a
+//    share of the columns.  Between them lies the only barrier of a tile: each
+//    warp reads the scores of its keys from shared memory, adds the parts and
+//    forms its own P operand in registers (the warps that share keys repeat
+//    the 8 exponentials a lane, which costs less than a second barrier).
+//  - A tile is a chain of dependent steps that leaves most issue slots empty,
+//    so two teams take the tiles in turn where the registers allow it.
+//  - Maximum and sum are kept in fp32 by each group of warps that has keys of
+//    its own and joined at the pair's end in a fixed tree.  P is rounded to
+//    the input type, as in the forward kernels; the sum is of the unrounded values.
+//
+// Every wait on a copy has a time limit, after which the call's status word
+// receives FFPA_ERR_DEVICE_TIMEOUT and the CTA runs out without waiting.
 #include "ffpa_paged.cuh"
 
 namespace ffpa {
 namespace {
 
-constexpr int DEC_SLOTS_MAX = 8;
-constexpr size_t DEC_SLOT_TARGET = 38 * 1024;
+constexpr int DEC_TEAM = 8;           // warps of a team
+constexpr int DEC_COPY_WARPS = 4;     // two for K, two for V
+constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
 
 struct DecodeParams {
+  CUtensorMap map_k, map_v;
   const char *q, *k, *v;
   char* o;
   float* lse;
@@ -46,49 +59,62 @@ struct DecodeParams {
   int64_t q_sb, q_sh, o_sb, o_sh;       // bytes
   int64_t k_sp, k_ss, k_sh, v_sp, v_ss, v_sh;
   int64_t table_str;
+  unsigned long long timeout_ns;
   int B, Hq, Hkv, group, D, head_tiles;
   int num_pages, page_size, max_pages;
-  int wd, wk, tile, pitch, slots;
+  int chunks;       // 64-column chunks of a row
+  int boxed;        // tiles arrive as tensor boxes
+  int box_rows;     // rows of a box (all T where not boxed), a power of two >= 8
+  int box_chunks;   // chunks of a box: all, or 1 when D ends inside a chunk
+  int ring_k, ring_v, drop;
   float scale_log2;
 };
 
+// Sizes of one call.  A tile has T = 16 keys for D > 512 and twice as many each
+// time D halves (at most 32 KB).
 struct DecodePlan {
-  int nt, wd, wk, tile, pitch, slots, head_tiles;
+  int nt, teams, tile, chunks, ring_k, ring_v, head_tiles;
   size_t smem;
 };
 
-// Heads of one pass: 8 NT, as many as the accumulators have registers for
-// (more than 8 warps leave 128 registers a thread).  A larger group is split
-// over pairs that read the same keys (the second from L2).
+// Heads of one pass: 8 NT, as many as the accumulators have registers for.  A
+// larger group is split over pairs that read the same keys (the second from L2).
 int decode_nt(int group, int D) { return group <= 8 ? 1 : group <= 16 || D > 512 ? 2 : 4; }
-
-size_t decode_fixed_smem(const DecodePlan& p) {
-  const size_t heads = 8 * (size_t)p.nt;
-  size_t s = p.wd * heads * (p.tile + 4) * 4;             // partial scores
-  const size_t join = p.wk > 1 ? heads * (p.wd * 64 + 4) * 4 : 0;   // or the key groups' outputs
-  if (join > s) s = join;
-  s += heads * (p.tile + 8) * 2;                          // P
-  s = (s + 15) & ~size_t(15);
-  s += 2 * (size_t)p.tile * 16;                           // row offsets of two tiles
-  s += heads * 12;                                        // maximum, sum, factor
-  return (s + 127) & ~size_t(127);
+// Two teams leave 96 registers a thread.
+__host__ __device__ constexpr int decode_teams(int nt) { return nt == 1 ? 2 : 1; }
+// Parts of D in the first product, and groups of warps with keys of their own in the second.
+__host__ __device__ constexpr int decode_parts(int tile) { return tile >= 128 ? 1 : 128 / tile; }
+__host__ __device__ constexpr int decode_groups(int tile) { return tile >= 32 ? tile / 32 : 1; }
+// Scores of two tiles a team (one where a warp reads no other's); at a pair's
+// end half of the groups' outputs, 64 columns of a warp at a time.
+__host__ __device__ constexpr bool decode_own_keys(int tile) { return tile / 16 > DEC_TEAM; }
+__host__ __device__ constexpr size_t decode_score_bytes(int nt, int tile) {
+  const int teams = decode_teams(nt);
+  const size_t scores = (size_t)teams * (decode_own_keys(tile) ? 1 : 2) * decode_parts(tile) * 8 * nt * (tile + 8) * 4;
+  const int groups = teams * decode_groups(tile);
+  const size_t join = groups > 1 ? (size_t)(groups / 2) * 8 * nt * (DEC_TEAM / decode_groups(tile) * 64 + 4) * 4 : 0;
+  return ((scores > join ? scores : join) + 1023) / 1024 * 1024;
 }
 
 DecodePlan decode_plan(int D, int group) {
   DecodePlan p;
   p.nt = decode_nt(group, D);
+  p.teams = decode_teams(p.nt);
   p.head_tiles = (group + 8 * p.nt - 1) / (8 * p.nt);
-  p.wd = (D + 63) / 64;
-  p.wk = p.wd < 8 ? 8 / p.wd : 1;
-  p.pitch = p.wd * 128 + 16;
-  const int step = 16 * p.wk;
-  p.tile = step;
-  // At least one lane in two of the softmax step has a key from 32 keys on.
-  while ((size_t)(p.tile + step) * p.pitch <= DEC_SLOT_TARGET && (p.tile + step) <= 32 * p.wd * p.wk) p.tile += step;
-  const size_t budget = SMEM_LIMIT - 1024 - decode_fixed_smem(p);
-  p.slots = static_cast<int>(budget / ((size_t)p.tile * p.pitch));
-  if (p.slots > DEC_SLOTS_MAX) p.slots = DEC_SLOTS_MAX;
-  p.smem = decode_fixed_smem(p) + (size_t)p.slots * p.tile * p.pitch;
+  p.tile = D > 512 ? 16 : D > 256 ? 32 : D > 128 ? 64 : D > 64 ? 128 : 256;
+  p.chunks = (D + 63) / 64;
+  const size_t fixed = decode_score_bytes(p.nt, p.tile);
+  const size_t stage = (size_t)p.tile * p.chunks * 128;
+  // 4 KB stay for static shared memory and the alignment of the boxes.
+  int n = static_cast<int>((SMEM_LIMIT - 4096 - fixed) / stage);
+  if (n > 2 * DEC_RING_MAX) n = 2 * DEC_RING_MAX;
+  // A slot belongs to one team (rings of an even length with two of them): the
+  // parity of its barrier tells a tile from the slot's previous one only while
+  // one reader takes the slot's tiles in order.
+  p.ring_v = p.teams == 2 ? n / 4 * 2 : n / 2;
+  p.ring_k = p.teams == 2 ? (n - p.ring_v) / 2 * 2 : n - p.ring_v;
+  if (p.ring_k > DEC_RING_MAX) p.ring_k = DEC_RING_MAX;
+  p.smem = 1024 + fixed + (size_t)(p.ring_k + p.ring_v) * stage;
   return p;
 }
 
@@ -103,7 +129,7 @@ __device__ __forceinline__ int clamped_len(const DecodeParams& P, int b) {
   return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
 
-__device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place& p) {
+__device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place& p, int T) {
   if (++p.t < p.tiles) return;
   p.t = 0;
   if (++p.u < pairs) return;
@@ -117,24 +143,173 @@ __device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place&
     }
     p.len = clamped_len(P, p.b);
   } while (p.len == 0);
-  p.tiles = (p.len + P.tile - 1) / P.tile;
+  p.tiles = (p.len + T - 1) / T;
 }
 
-template <bool F16, int NT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const DecodeParams P) {
-  constexpr int HEADS = 8 * NT;
-  extern __shared__ __align__(128) char smem[];
-  const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int T = P.tile, pitch = P.pitch, slots = P.slots;
+// A whole warp's bounded wait; false for all its lanes when the limit expired for one.
+__device__ __forceinline__ bool all_waited(uint32_t bar, uint32_t parity, const DecodeParams& P, volatile int* abort_flag) {
+  return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag, P.timeout_ns, P.err));
+}
+
+// K (or V) tiles of the run as tensor boxes, a box a lane, its page looked up
+// one tile ahead.  A page that does not exist, and rows that belong to no key,
+// have a coordinate behind the last page: the copy writes zeros there.
+__device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, bool is_v, Place at, int n_tiles, uint32_t ring,
+                                              int slots, uint64_t* full, uint64_t* empty, volatile int* abort_flag) {
+  const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles;
+  const CUtensorMap* map = is_v ? &P.map_v : &P.map_k;
+  const int per_row = P.chunks / P.box_chunks;          // boxes side by side (at most 32 boxes a tile)
+  const int row = lane / per_row * P.box_rows, chunk = lane % per_row;
+  const bool mine = row < T;
+  const uint32_t box_bytes = P.box_rows * P.box_chunks * 128, stage = T * P.chunks * 128;
+  const uint32_t to = row * P.chunks * 128 + chunk * box_bytes;
+  int page = -1, in_page = 0;
+  bool keyed = false;
+  auto look_up = [&](const Place& p) {
+    const int key = p.t * T + row;
+    keyed = mine && key < p.len;
+    page = -1;
+    if (keyed) {
+      const int j = key / P.page_size;
+      in_page = key - j * P.page_size;
+      page = P.table[p.b * P.table_str + j];
+    }
+  };
+  look_up(at);
+  int slot = 0, i = 0;
+  uint32_t lap = 0;
+  for (; i < n_tiles; ++i) {
+    const int head = at.u / P.head_tiles;
+    const bool good = page >= 0 && page < P.num_pages;
+    if (keyed && !good) report_invalid(P.err);
+    const int y = good ? in_page : 0, z = good ? page : P.num_pages;
+    advance(P, pairs, at, T);
+    if (i + 1 < n_tiles) look_up(at);
+    if (!all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) || P.drop) break;
+    const uint32_t bar = smem_u32(full + slot);
+    if (lane == 0) mbar_arrive_expect_tx(bar, stage);
+    __syncwarp();
+    if (mine) {
+      const uint32_t dst = ring + slot * stage + to;
+      if (P.box_chunks == 1)
+        tma_load_4d(dst, map, bar, chunk * 64, y, head, z);
+      else
+        tma_load_5d(dst, map, bar, 0, y, 0, head, z);
+    }
+    if (++slot == slots) {
+      slot = 0;
+      lap ^= 1u;
+    }
+  }
+  // Copies still in flight land before the CTA ends (the teams wait for them,
+  // unless they gave up).
+  for (int j = i < slots ? i : slots; j > 0; --j) {
+    if (slot == 0) {
+      slot = slots;
+      lap ^= 1u;
+    }
+    --slot;
+    wait_drain(smem_u32(full + slot), lap, P.timeout_ns, P.err);
+  }
+}
+
+// The same tile for any page size: a warp looks half of its rows up lane by
+// lane, one tile ahead, and copies them in pieces of 16 bytes, a power of two of
+// lanes to a row.  A row without a key, or of a page that does not exist,
+// becomes zeros.
+__device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, bool is_v, int half, Place at, int n_tiles,
+                                               uint32_t ring, int slots, uint64_t* full, uint64_t* empty,
+                                               volatile int* abort_flag) {
+  const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles;
+  const int cpr = P.D / 8;                         // pieces of a row
+  int wide = 8;                                    // lanes of a row
+  while (wide < cpr && wide < 32) wide *= 2;
+  const int c0 = lane % wide, r0 = lane / wide, step = 32 / wide;
+  const int mine = T / 2, first = half * mine;     // rows of this warp
+  const char* base = is_v ? P.v : P.k;
+  const int64_t sp = is_v ? P.v_sp : P.k_sp, ss = is_v ? P.v_ss : P.k_ss, sh = is_v ? P.v_sh : P.k_sh;
+  const uint32_t stage = T * P.chunks * 128;
+  int page[4];
+  auto look_up = [&](const Place& p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (32 * j >= mine) break;
+      const int r = lane + 32 * j, key = p.t * T + first + r;
+      page[j] = r < mine && key < p.len ? P.table[p.b * P.table_str + key / P.page_size] : -1;
+    }
+  };
+  look_up(at);
+  int slot = 0;
+  uint32_t lap = 0;
+  for (int i = 0; i < n_tiles; ++i) {
+    // Offsets of this tile's rows (-1: zeros), then the pages of the next.
+    const char* head = base + (at.u / P.head_tiles) * sh;
+    int64_t from[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      from[j] = -1;
+      if (32 * j >= mine) break;
+      const int r = lane + 32 * j, key = at.t * T + first + r;
+      if (r < mine && key < at.len) {
+        if (page[j] >= 0 && page[j] < P.num_pages)
+          from[j] = page[j] * sp + key % P.page_size * ss;
+        else
+          report_invalid(P.err);
+      }
+    }
+    advance(P, pairs, at, T);
+    if (i + 1 < n_tiles) look_up(at);
+    if (!all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) || P.drop) break;
+    const uint32_t tile = ring + slot * stage;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (32 * j >= mine) break;
+      const int end = min(32, mine - 32 * j);
+#pragma unroll 2
+      for (int r = 0; r < end; r += step) {
+        const int64_t at_row = __shfl_sync(~0u, from[j], r + r0);
+        if (r + r0 >= end) continue;
+        const int row = first + 32 * j + r + r0;
+        for (int c = c0; c < cpr; c += wide)
+          copy16_async(tile + (c >> 3) * (T * 128) + row * 128 + ((c ^ row) & 7) * 16,
+                       at_row >= 0 ? head + at_row + c * 16 : base, at_row >= 0 ? 16 : 0);
+      }
+    }
+    copy_arrive(smem_u32(full + slot));
+    if (++slot == slots) {
+      slot = 0;
+      lap ^= 1u;
+    }
+  }
+  copy_wait_all();
+}
+
+template <bool F16, int NT, int T>
+__global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS) * 32, 1)
+    decode_kernel(const __grid_constant__ DecodeParams P) {
+  constexpr int HEADS = 8 * NT, TEAMS = decode_teams(NT), THREADS = (TEAMS * DEC_TEAM + DEC_COPY_WARPS) * 32;
+  constexpr int PARTS = decode_parts(T), WK = decode_groups(T), MT = T / 16, GROUPS = TEAMS * WK;
+  constexpr int KSTEPS = T < 32 ? 1 : 2;      // of 16 keys, of a warp in the second product
+  constexpr int DT = T < 32 ? 8 : 4;          // column tiles of a warp there
+  constexpr int WDS = DEC_TEAM / WK;          // warps that share keys there
+  constexpr int SPITCH = T + 8, SBUF = PARTS * HEADS * SPITCH;
+  constexpr bool OWN = decode_own_keys(T);    // a warp's scores are those of its own keys
+  extern __shared__ char smem_raw[];
+  __shared__ uint64_t full_k[DEC_RING_MAX], full_v[DEC_RING_MAX], empty_k[DEC_RING_MAX], empty_v[DEC_RING_MAX];
+  __shared__ float2 ml_s[GROUPS][HEADS];
+  __shared__ long long scan_s[25];
+  __shared__ int start_s;
+  __shared__ int abort_flag;
+  char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = P.Hkv * P.head_tiles;
+  const uint32_t stage = T * P.chunks * 128;
 
   // ---- this CTA's run of tiles
-  __shared__ long long scan_s[17];
-  __shared__ int start_s[2];
   long long total, lo, hi;
   Place cur;
   {
-    const int per = (P.B + nthreads - 1) / nthreads;
+    const int per = (P.B + THREADS - 1) / THREADS;
     const int b0 = tid * per, b1 = min(P.B, b0 + per);
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
@@ -150,10 +325,22 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const DecodeParam
       if (lane >= d) incl += x;
     }
     if (lane == 31) scan_s[warp] = incl;
+    if (tid == 0) {
+      abort_flag = 0;
+      const int arrivals = P.boxed ? 1 : 64;
+      for (int i = 0; i < DEC_RING_MAX; ++i) {
+        mbar_init(smem_u32(full_k + i), arrivals);
+        mbar_init(smem_u32(full_v + i), arrivals);
+        mbar_init(smem_u32(empty_k + i), DEC_TEAM);
+        mbar_init(smem_u32(empty_v + i), DEC_TEAM);
+      }
+      fence_mbar_init();
+      P.meta[blockIdx.x] = make_int2(-1, 0);
+    }
     __syncthreads();
     long long before = 0;
     total = 0;
-    for (int w = 0; w < nthreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) before += scan_s[w];
       total += scan_s[w];
     }
@@ -165,374 +352,350 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const DecodeParam
     hi = c < runs ? (c + 1) * total / runs : 0;
     if (c < runs && lo >= at && lo < at + mine * pairs) {
       int b = b0;
-      long long tiles = 0;
       for (; b < b1; ++b) {
-        tiles = (clamped_len(P, b) + T - 1) / T;
+        const long long tiles = (clamped_len(P, b) + T - 1) / T;
         if (lo < at + tiles * pairs) break;
         at += tiles * pairs;
       }
-      start_s[0] = b;
-      scan_s[16] = lo - at;
-    }
-    if (tid == 0) P.meta[blockIdx.x] = make_int2(-1, 0);
-    __syncthreads();
-    if (c < runs) {
-      cur.b = start_s[0];
-      cur.len = clamped_len(P, cur.b);
-      cur.tiles = (cur.len + T - 1) / T;
-      const long long r = scan_s[16];
-      cur.u = (int)(r / cur.tiles);
-      cur.t = (int)(r % cur.tiles);
+      start_s = b;
+      scan_s[24] = lo - at;
     }
     // Requests without keys have no tile: their rows are written here.
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
       if (clamped_len(P, b) != 0) continue;
-      for (int i = tid; i < P.Hq * (P.D / 8); i += nthreads) {
+      for (int i = tid; i < P.Hq * (P.D / 8); i += THREADS) {
         const int h = i / (P.D / 8), d = i % (P.D / 8);
         *reinterpret_cast<uint4*>(P.o + b * P.o_sb + h * P.o_sh + d * 16) = make_uint4(0, 0, 0, 0);
       }
       if (P.lse)
-        for (int h = tid; h < P.Hq; h += nthreads) P.lse[(int64_t)b * P.Hq + h] = -INFINITY;
+        for (int h = tid; h < P.Hq; h += THREADS) P.lse[(int64_t)b * P.Hq + h] = -INFINITY;
     }
     if (c >= runs) return;
+    // Columns behind D meet zeros of Q and must be finite (boxes bring zeros).
+    if (!P.boxed && P.D % 16 != 0) {
+      char* ring = smem + decode_score_bytes(NT, T);
+      const int c16 = P.D / 8;
+      for (int i = tid; i < (P.ring_k + P.ring_v) * T; i += THREADS)
+        *reinterpret_cast<uint4*>(ring + (size_t)(i / T) * stage + (c16 >> 3) * (T * 128) + (i % T) * 128 +
+                                  ((c16 ^ i) & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    cur.b = start_s;
+    cur.len = clamped_len(P, cur.b);
+    cur.tiles = (cur.len + T - 1) / T;
+    const long long r = scan_s[24];
+    cur.u = (int)(r / cur.tiles);
+    cur.t = (int)(r % cur.tiles);
   }
-  const long long runs = total < gridDim.x ? total : gridDim.x;
   const int n_tiles = (int)(hi - lo);
+  float* scores = reinterpret_cast<float*>(smem);                  // [TEAMS][2, or 1 when OWN][PARTS][HEADS][SPITCH]
+  const uint32_t ring_k = smem_u32(smem + decode_score_bytes(NT, T));
+  const uint32_t ring_v = ring_k + P.ring_k * stage;
 
-  // ---- shared memory
-  float* part_s = reinterpret_cast<float*>(smem);                  // [wd][HEADS][T + 4]
-  const int spitch = T + 4;
-  size_t off = (size_t)P.wd * HEADS * spitch * 4;
-  if (P.wk > 1) {
-    const size_t join = (size_t)HEADS * (P.wd * 64 + 4) * 4;
-    if (join > off) off = join;
-  }
-  char* p_s = smem + off;                                          // [HEADS][T + 8] 16-bit
-  const int ppitch = (T + 8) * 2;
-  off += (size_t)HEADS * ppitch;
-  off = (off + 15) & ~size_t(15);
-  longlong2* rows_s = reinterpret_cast<longlong2*>(smem + off);    // [2][T] byte offsets of K and V rows, or -1
-  off += 2 * (size_t)T * 16;
-  float* max_s = reinterpret_cast<float*>(smem + off);
-  float* sum_s = max_s + HEADS;
-  float* fac_s = sum_s + HEADS;
-  off += HEADS * 12;
-  off = (off + 127) & ~size_t(127);
-  char* ring = smem + off;
-  const int slot_bytes = T * pitch;
-
-  for (int i = tid; i < HEADS * ppitch / 4; i += nthreads) reinterpret_cast<uint32_t*>(p_s)[i] = 0;
-  for (int i = tid; i < HEADS; i += nthreads) fac_s[i] = 1.0f;
-  // Columns past D are read by the matrix loads: zero once, never written again.
-  if (P.D % 64 != 0) {
-    const int pad = P.wd * 8 - P.D / 8;   // 16-byte pieces
-    for (int i = tid; i < slots * T * pad; i += nthreads)
-      *reinterpret_cast<uint4*>(ring + (i / pad) * pitch + P.D * 2 + (i % pad) * 16) = make_uint4(0, 0, 0, 0);
+  if (warp >= TEAMS * DEC_TEAM) {
+    const int w = warp - TEAMS * DEC_TEAM;
+    const bool is_v = w >= 2;
+    uint64_t *full = is_v ? full_v : full_k, *empty = is_v ? empty_v : empty_k;
+    const uint32_t ring = is_v ? ring_v : ring_k;
+    const int slots = is_v ? P.ring_v : P.ring_k;
+    if (!P.boxed)
+      produce_pieces(P, T, is_v, w & 1, cur, n_tiles, ring, slots, full, empty, &abort_flag);
+    else if ((w & 1) == 0)
+      produce_boxes(P, T, is_v, cur, n_tiles, ring, slots, full, empty, &abort_flag);
+    return;
   }
 
-  // ---- producer side: every thread copies its share of each half (K or V tile)
-  const int cpr = P.D / 8;                         // 16-byte pieces of a row
-  const int r0 = tid / cpr, c0 = tid % cpr, dr = nthreads / cpr, dc = nthreads % cpr;
-  Place ahead = cur;        // tile whose rows are looked up next
-  int looked = 0;           // tiles looked up
-  int issued = 0;           // halves issued
-  int page_next = -1;       // page of this thread's row in tile `ahead`
-  bool row_next = false;
-  int u_of[2] = {0, 0};     // pair of the two tiles in rows_s
+  // ---- the teams
+  const int team = warp / DEC_TEAM, tw = warp % DEC_TEAM;
+  const long long runs = total < gridDim.x ? total : gridDim.x;
+  const int ksteps = (P.D + 15) / 16;
+  // Shares of D are whole chunks, so that a chunk's swizzle is a constant of the code.
+  const int part = tw / MT;                        // in the first product (0 when a warp has two key tiles)
+  const int kper = (P.chunks + PARTS - 1) / PARTS * 4;
+  const int k0 = part * kper, kn = max(0, min(kper, ksteps - k0));
+  const int wkey = tw / WDS, wd = tw % WDS, group = team * WK + wkey;
+  const int dper = (P.chunks + WDS - 1) / WDS * 4;
+  const int d0 = wd * dper, dn = max(0, min(dper, ksteps - d0));
+  const int c2 = (lane % 4) * 2, hq = lane / 4;
+  const uint32_t chunk_bytes = P.box_rows * 128;
+  // Row r of a tile: boxes of box_rows rows, in each chunk after chunk.
+  auto row_at = [&](int r) { return r / P.box_rows * (P.chunks * chunk_bytes) + r % P.box_rows * 128; };
+  const int key0 = OWN ? tw * 32 : tw % MT * 16;   // first key of the first product
+  const int kr = key0 + (lane & 15), vr = wkey * 32 + (lane >> 4) * 8 + (lane & 7);
+  const uint32_t k_at = ring_k + row_at(kr) + (k0 >> 2) * chunk_bytes + (((lane >> 4) ^ (lane & 7)) << 4);
+  const uint32_t k_at2 = OWN ? k_at - row_at(kr) + row_at(kr + 16) : 0;
+  const uint32_t v_x = (d0 >> 2) * chunk_bytes + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+  const uint32_t v_at = ring_v + row_at(vr) + v_x, v_at2 = ring_v + row_at(vr + 16) + v_x;
+  uint32_t qf[8][NT][2];
+  float acc[DT][NT][4];
+  float top[NT], sum[NT];                          // of head 8 n + lane / 4
+  int slot_k = team, slot_v = team;                // team < 2 <= ring
+  uint32_t lap_k = 0, lap_v = 0;
+  bool alive = true;
+  int buf = 0;
 
-  auto load_page = [&] {
-    row_next = false;
-    if (looked < n_tiles && tid < T) {
-      const int key = ahead.t * T + tid;
-      if (key < ahead.len) {
-        row_next = true;
-        page_next = P.table[ahead.b * P.table_str + key / P.page_size];
-      }
-    }
-  };
-  // Row offsets of tile `looked` into buffer looked & 1; then the pages of the next one are requested.
-  auto look_up = [&] {
-    if (looked < n_tiles) {
-      if (tid < T) {
-        longlong2 x = make_longlong2(-1, -1);
-        if (row_next) {
-          if (page_next >= 0 && page_next < P.num_pages) {
-            const int in = (ahead.t * T + tid) % P.page_size;
-            x.x = page_next * P.k_sp + in * P.k_ss;
-            x.y = page_next * P.v_sp + in * P.v_ss;
-          } else {
-            report_invalid(P.err);
-          }
-        }
-        rows_s[(looked & 1) * T + tid] = x;
-      }
-      u_of[looked & 1] = ahead.u;
-      ++looked;
-      advance(P, pairs, ahead);
-      load_page();
-    }
-  };
-  // The next half into its slot of the ring; past the run's end an empty group keeps the count.
-  auto issue = [&] {
-    const int tile = issued >> 1;
-    if (tile < n_tiles) {
-      const bool is_v = issued & 1;
-      const uint32_t dst = smem_u32(ring + (issued % slots) * slot_bytes);
-      const int hk = u_of[tile & 1] / P.head_tiles;
-      const char* base = is_v ? P.v + hk * P.v_sh : P.k + hk * P.k_sh;
-      const longlong2* rows = rows_s + (tile & 1) * T;
-      int r = r0, c = c0;
-      while (r < T) {
-        const long long at = is_v ? rows[r].y : rows[r].x;
-        copy16_async(dst + r * pitch + c * 16, at >= 0 ? base + at + c * 16 : base, at >= 0 ? 16 : 0);
-        r += dr;
-        c += dc;
-        if (c >= cpr) {
-          c -= cpr;
-          ++r;
-        }
-      }
-    }
-    copy_commit();
-    ++issued;
-  };
-
-  load_page();
-  look_up();
-  __syncthreads();
-  for (int i = 0; i < slots; ++i) {
-    issue();
-    if ((issued & 1) == 0) {
-      look_up();
-      __syncthreads();
-    }
-  }
-
-  // ---- consumer side
-  const int wd = warp % P.wd, wkey = warp / P.wd;
-  const int keys = T / P.wk, key0 = wkey * keys;         // this warp's keys of a tile
-  uint32_t qf[4][NT][2];
-  float acc[4][NT][4];
-  int rows = 0, hq0 = 0, t0 = 0;
-
-  // wait until at most `left` groups are in flight
-  auto wait = [&](int left) {
-    switch (left) {
-      case 0: copy_wait<0>(); break;
-      case 1: copy_wait<1>(); break;
-      case 2: copy_wait<2>(); break;
-      case 3: copy_wait<3>(); break;
-      case 4: copy_wait<4>(); break;
-      case 5: copy_wait<5>(); break;
-      case 6: copy_wait<6>(); break;
-      default: copy_wait<7>(); break;
-    }
-  };
-
-  for (int i = 0; i < n_tiles; ++i) {
-    if (i == 0 || cur.t == 0) {
-      // A new pair: its queries into registers, sums cleared.
-      const int hk = cur.u / P.head_tiles, ht = cur.u % P.head_tiles;
-      hq0 = hk * P.group + ht * HEADS;
-      rows = min(HEADS, P.group - ht * HEADS);
-      t0 = cur.t;
+  for (int i0 = 0; i0 < n_tiles;) {
+    // ---- one pair's tiles of this run: [i0, i1)
+    const int i1 = min(n_tiles, i0 + cur.tiles - cur.t);
+    const int hk = cur.u / P.head_tiles, ht = cur.u % P.head_tiles;
+    const int hq0 = hk * P.group + ht * HEADS;
+    const int rows = min(HEADS, P.group - ht * HEADS);
+    int i = i0 + ((i0 ^ team) & (TEAMS - 1));      // the team's first tile
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+    for (int n = 0; n < NT; ++n) {
+      const int head = n * 8 + hq;
+      const char* src = P.q + cur.b * P.q_sb + (int64_t)(hq0 + head) * P.q_sh;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int head = n * 8 + lane / 4;
-          const char* src = P.q + cur.b * P.q_sb + (int64_t)(hq0 + head) * P.q_sh;
+      for (int s = 0; s < 8; ++s)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int d = wd * 64 + s * 16 + j * 8 + (lane % 4) * 2;
-            qf[s][n][j] = head < rows && d < P.D ? *reinterpret_cast<const uint32_t*>(src + d * 2) : 0u;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[s][n][j] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+          const int d = (k0 + s) * 16 + j * 8 + c2;
+          qf[s][n][j] = head < rows && s < kn && d < P.D && i < i1 ? *reinterpret_cast<const uint32_t*>(src + d * 2) : 0u;
         }
-      for (int h = warp; h < HEADS; h += nthreads / 32)
-        if (lane == 0) {
-          max_s[h] = -INFINITY;
-          sum_s[h] = 0.0f;
-        }
+#pragma unroll
+      for (int s = 0; s < DT; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[s][n][j] = 0.0f;
+      top[n] = -INFINITY;
+      sum[n] = 0.0f;
     }
-    const int half = 2 * i;
-    wait(slots - 2);
-    __syncthreads();           // K tile i has landed; every warp is done with V tile i - 1
-    if (i > 0) {
-      issue();
-      if ((issued & 1) == 0) look_up();
-    }
-    {
-      const uint32_t ks = smem_u32(ring + (half % slots) * slot_bytes);
-      for (int g = 0; g < keys; g += 16) {
+    int left = cur.len - (cur.t + (i - i0)) * T - wkey * 32;    // keys from this warp's first one on
+    for (; i < i1; i += TEAMS, left -= TEAMS * T) {
+      float* sc = scores + (OWN ? team : team * 2 + buf) * SBUF;
+      buf ^= 1;
+      if (OWN) __syncwarp();
+
+      // ---- scores of 16 keys over this warp's part of D
+      if (alive) alive = all_waited(smem_u32(full_k + slot_k), lap_k, P, &abort_flag);
+#pragma unroll
+      for (int y = 0; y < (OWN ? 2 : 1); ++y) {
+        const uint32_t a0 = (y ? k_at2 : k_at) + slot_k * stage;
         float s[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
-        const uint32_t a0 = ks + (key0 + g + ((lane >> 3) & 1) * 8 + (lane & 7)) * pitch + wd * 128 + (lane >> 4) * 16;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 8; ++x) {
+          if (x >= kn) break;
           uint32_t a[4];
-          ldm_x4(a0 + x * 32, a);
+          ldm_x4((a0 + (x >> 2) * chunk_bytes) ^ ((x & 3) << 5), a);
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16<F16>(s[n], a, qf[x][n]);
         }
-        float* dst = part_s + (wd * HEADS + (lane % 4) * 2) * spitch + key0 + g + lane / 4;
+        float* dst = sc + (part * HEADS + c2) * SPITCH + key0 + y * 16 + hq;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          dst[n * 8 * spitch] = s[n][0];
-          dst[(n * 8 + 1) * spitch] = s[n][1];
-          dst[n * 8 * spitch + 8] = s[n][2];
-          dst[(n * 8 + 1) * spitch + 8] = s[n][3];
+          dst[n * 8 * SPITCH] = s[n][0];
+          dst[(n * 8 + 1) * SPITCH] = s[n][1];
+          dst[n * 8 * SPITCH + 8] = s[n][2];
+          dst[(n * 8 + 1) * SPITCH + 8] = s[n][3];
         }
       }
-    }
-    __syncthreads();           // the partial scores are complete; K tile i is free
-    issue();
-    if ((issued & 1) == 0) look_up();
-    for (int h = warp; h < rows; h += nthreads / 32) {
-      const int left = cur.len - cur.t * T;      // keys of this tile and beyond
-      float x[8], top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = lane + 32 * j;
-        x[j] = -INFINITY;
-        if (key < T && key < left) {
-          float sum = 0.0f;
-          for (int w = 0; w < P.wd; ++w) sum += part_s[(w * HEADS + h) * spitch + key];
-          x[j] = sum * P.scale_log2;
-        }
-        top = fmaxf(top, x[j]);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      const float old = max_s[h];
-      const float now = fmaxf(old, top);
-      const float base = now == -INFINITY ? 0.0f : now;
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = lane + 32 * j;
-        if (key < T) {
-          const float e = ex2_approx(x[j] - base);
-          sum += e;
-          store16<F16>(p_s + h * ppitch + key * 2, e);
-        }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
       __syncwarp();
-      if (lane == 0) {
-        const float f = ex2_approx(old - base);
-        max_s[h] = now;
-        sum_s[h] = sum_s[h] * f + sum;
-        fac_s[h] = f;
+      if (lane == 0) mbar_arrive(smem_u32(empty_k + slot_k));
+      if ((slot_k += TEAMS) >= P.ring_k) {
+        slot_k -= P.ring_k;
+        lap_k ^= 1u;
       }
-    }
-    wait(slots - 1);
-    __syncthreads();           // P is complete; V tile i has landed
-    {
-      const uint32_t vs = smem_u32(ring + ((half + 1) % slots) * slot_bytes);
-      const uint32_t ps = smem_u32(p_s);
+      // The scores are complete (the next tile writes the other buffer).
+      if (!OWN) named_bar_sync(1 + team, DEC_TEAM * 32);
+
+      // ---- P of this warp's keys, as the operand of the second product
+      uint32_t pf[KSTEPS][NT][2];
+      float fac[NT];
+      bool moved = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float f0 = fac_s[n * 8 + (lane % 4) * 2], f1 = fac_s[n * 8 + (lane % 4) * 2 + 1];
+        float2 x[2 * KSTEPS];
+        float most = -INFINITY;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          acc[s][n][0] *= f0;
-          acc[s][n][1] *= f1;
-          acc[s][n][2] *= f0;
-          acc[s][n][3] *= f1;
+        for (int j = 0; j < 2 * KSTEPS; ++j) {
+          const float* src = sc + (n * 8 + hq) * SPITCH + wkey * 32 + j * 8 + c2;
+          x[j] = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+          for (int p = 1; p < PARTS; ++p) {
+            const float2 w = *reinterpret_cast<const float2*>(src + p * HEADS * SPITCH);
+            x[j].x += w.x;
+            x[j].y += w.y;
+          }
+          x[j].x *= P.scale_log2;
+          x[j].y *= P.scale_log2;
+        }
+        if (left < 16 * KSTEPS) {
+#pragma unroll
+          for (int j = 0; j < 2 * KSTEPS; ++j) {
+            if (j * 8 + c2 >= left) x[j].x = -INFINITY;
+            if (j * 8 + c2 + 1 >= left) x[j].y = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * KSTEPS; ++j) most = fmax3(most, x[j].x, x[j].y);
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+        const float now = fmaxf(top[n], most);
+        const float base = now == -INFINITY ? 0.0f : now;
+        fac[n] = ex2_approx(top[n] - base);
+        moved |= now != top[n];
+        top[n] = now;
+        float add = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2 * KSTEPS; ++j) {
+          x[j].x = ex2_approx(x[j].x - base);
+          x[j].y = ex2_approx(x[j].y - base);
+          add += x[j].x + x[j].y;
+          pf[j >> 1][n][j & 1] = pack2<F16>(x[j].x, x[j].y);
+        }
+        sum[n] = sum[n] * fac[n] + add;
+      }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float f0 = __shfl_sync(~0u, fac[n], c2 * 4), f1 = __shfl_sync(~0u, fac[n], c2 * 4 + 4);
+#pragma unroll
+          for (int s = 0; s < DT; ++s) {
+            acc[s][n][0] *= f0;
+            acc[s][n][1] *= f1;
+            acc[s][n][2] *= f0;
+            acc[s][n][3] *= f1;
+          }
         }
       }
-      for (int g = key0; g < key0 + keys; g += 16) {
-        uint32_t b[NT][2];
+
+      // ---- this warp's columns += V^T P
+      if (alive) alive = all_waited(smem_u32(full_v + slot_v), lap_v, P, &abort_flag);
+      const bool tail = left < 16 * KSTEPS;        // rows behind the last key hold anything: zeros, not 0 * NaN
 #pragma unroll
-        for (int n = 0; n < NT; ++n) ldm_x2(ps + (n * 8 + (lane & 7)) * ppitch + g * 2 + ((lane >> 3) & 1) * 16, b[n]);
-        const uint32_t a0 = vs + (g + (lane >> 4) * 8 + (lane & 7)) * pitch + wd * 128 + ((lane >> 3) & 1) * 16;
+      for (int s = 0; s < DT; ++s) {
+        if (s >= dn) break;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int g = 0; g < KSTEPS; ++g) {
           uint32_t a[4];
-          ldm_x4_trans(a0 + s * 32, a);
+          ldm_x4_trans(((g ? v_at2 : v_at) + slot_v * stage + (s >> 2) * chunk_bytes) ^ ((s & 3) << 5), a);
+          if (tail) {
+            const int k = g * 16 + c2;
+            const uint32_t m0 = (k < left ? 0xffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
+            const uint32_t m1 = (k + 8 < left ? 0xffffu : 0u) | (k + 9 < left ? 0xffff0000u : 0u);
+            a[0] &= m0;
+            a[1] &= m0;
+            a[2] &= m1;
+            a[3] &= m1;
+          }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16<F16>(acc[s][n], a, b[n]);
+          for (int n = 0; n < NT; ++n) mma16<F16>(acc[s][n], a, pf[g][n]);
         }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(empty_v + slot_v));
+      if ((slot_v += TEAMS) >= P.ring_v) {
+        slot_v -= P.ring_v;
+        lap_v ^= 1u;
       }
     }
-    const bool done = cur.t == cur.tiles - 1;
-    if (done || i == n_tiles - 1) {
-      // ---- the pair's sums, whole or cut
-      const bool whole = done && t0 == 0;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0 ? 1 : 0);
-      float* part = P.part + slot * HEADS * P.D;
-      if (P.wk > 1) {
-        // The key groups' outputs are added in their order (over the scores: PV does not read them).
-        const int jpitch = P.wd * 64 + 4;
-        for (int w = 0; w < P.wk; ++w) {
-          if (wkey == w) {
+
+    // ---- the pair's sums, joined over the groups of warps in a fixed tree
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      sum[n] += __shfl_xor_sync(~0u, sum[n], 1);
+      sum[n] += __shfl_xor_sync(~0u, sum[n], 2);
+    }
+    constexpr int N = TEAMS * DEC_TEAM * 32;
+    constexpr int JPITCH = WDS * 64 + 4;
+    if (GROUPS > 1) named_bar_sync(3, N);          // the scores are read, their place is free
+#pragma unroll 1
+    for (int half = GROUPS / 2; half > 0; half /= 2) {
+      float f[NT][4];                              // factors of this group's columns and of the other's
+#pragma unroll
+      for (int s0 = 0; s0 < DT; s0 += 4) {
+        float* at = scores + ((group & (half - 1)) * HEADS + c2) * JPITCH + wd * 64 + hq;
+        if (group >= half && group < 2 * half) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (s0 == 0 && wd == 0 && lane % 4 == 0) ml_s[group][n * 8 + hq] = make_float2(top[n], sum[n]);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  float* dst = part_s + (n * 8 + (lane % 4) * 2 + (j & 1)) * jpitch + wd * 64 + s * 16 + lane / 4 + (j >> 1) * 8;
-                  acc[s][n][j] = w == 0 ? acc[s][n][j] : *dst + acc[s][n][j];
-                  if (w < P.wk - 1) *dst = acc[s][n][j];
-                }
+              for (int j = 0; j < 4; ++j) at[(n * 8 + (j & 1)) * JPITCH + s * 16 + (j >> 1) * 8] = acc[s0 + s][n][j];
           }
-          __syncthreads();
         }
-      }
-      if (wkey == P.wk - 1) {
+        named_bar_sync(3, N);
+        if (group < half) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int head = n * 8 + (lane % 4) * 2 + (j & 1);
-            if (head >= rows) continue;
-            const float l = sum_s[head];
-            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
-            char* out = P.o + cur.b * P.o_sb + (int64_t)(hq0 + head) * P.o_sh;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const int d = wd * 64 + s * 16 + lane / 4 + (j >> 1) * 8;
-              if (d >= P.D) continue;
-              if (whole)
-                store16<F16>(out + d * 2, acc[s][n][j] * inv);
-              else
-                part[(int64_t)head * P.D + d] = acc[s][n][j];
+          for (int n = 0; n < NT; ++n) {
+            if (s0 == 0) {
+              const float2 other = ml_s[group + half][n * 8 + hq];
+              const float now = fmaxf(top[n], other.x);
+              const float base = now == -INFINITY ? 0.0f : now;
+              const float fa = ex2_approx(top[n] - base), fb = ex2_approx(other.x - base);
+              top[n] = now;
+              sum[n] = sum[n] * fa + other.y * fb;
+              f[n][0] = __shfl_sync(~0u, fa, c2 * 4);
+              f[n][1] = __shfl_sync(~0u, fa, c2 * 4 + 4);
+              f[n][2] = __shfl_sync(~0u, fb, c2 * 4);
+              f[n][3] = __shfl_sync(~0u, fb, c2 * 4 + 4);
             }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                acc[s0 + s][n][j] = acc[s0 + s][n][j] * f[n][j & 1] +
+                                    at[(n * 8 + (j & 1)) * JPITCH + s * 16 + (j >> 1) * 8] * f[n][2 + (j & 1)];
           }
+        }
+        named_bar_sync(3, N);
       }
-      for (int h = tid; h < rows; h += nthreads) {
-        if (whole) {
-          if (P.lse)
-            P.lse[(int64_t)cur.b * P.Hq + hq0 + h] =
-                sum_s[h] == 0.0f ? -INFINITY : (max_s[h] + log2f(sum_s[h])) * 0.69314718055994531f;
-        } else {
-          P.part_ml[slot * HEADS + h] = make_float2(max_s[h], sum_s[h]);
+    }
+    const bool done = i1 - i0 == cur.tiles - cur.t;
+    if (group == 0) {
+      // ---- written: a whole pair as it is, a cut one for the second launch
+      const bool whole = done && cur.t == 0;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.t == 0 ? 1 : 0);
+      float* part_o = P.part + slot * HEADS * P.D;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float inv = whole ? (sum[n] == 0.0f ? 0.0f : 1.0f / sum[n]) : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int head = n * 8 + c2 + (j & 1);
+          const float f = __shfl_sync(~0u, inv, c2 * 4 + (j & 1) * 4);
+          if (head >= rows) continue;
+          char* out = P.o + cur.b * P.o_sb + (int64_t)(hq0 + head) * P.o_sh;
+#pragma unroll
+          for (int s = 0; s < DT; ++s) {
+            const int d = (d0 + s) * 16 + hq + (j >> 1) * 8;
+            if (s >= dn || d >= P.D) continue;
+            if (whole)
+              store16<F16>(out + d * 2, acc[s][n][j] * f);
+            else
+              part_o[(int64_t)head * P.D + d] = acc[s][n][j];
+          }
+        }
+        const int head = n * 8 + hq;
+        if (wd == 0 && lane % 4 == 0 && head < rows) {
+          if (!whole)
+            P.part_ml[slot * HEADS + head] = make_float2(top[n], sum[n]);
+          else if (P.lse)
+            P.lse[(int64_t)cur.b * P.Hq + hq0 + head] =
+                sum[n] == 0.0f ? -INFINITY : (top[n] + log2f(sum[n])) * 0.69314718055994531f;
         }
       }
-      if (!done && t0 == 0 && tid == 0) {
+      if (!done && cur.t == 0 && tw == 0 && lane == 0) {
         // The pair goes on in the next CTAs; its last tile says how far.
-        const long long last = lo + i + (cur.tiles - 1 - cur.t);
+        const long long last = lo + i0 + cur.tiles - 1;
         P.meta[blockIdx.x] = make_int2(cur.b * pairs + cur.u, (int)(((last + 1) * runs - 1) / total));
       }
-      __syncthreads();         // the sums are read before the next pair clears them
     }
-    advance(P, pairs, cur);
+    i0 = i1;
+    cur.t = cur.tiles - 1;
+    advance(P, pairs, cur, T);
   }
-  copy_wait<0>();
 }
 
 // Joins the partial sums of a pair cut between CTAs: block (c, row) the row of
 // the pair that CTA c began, over CTAs c .. last, in that order.  Groups of
 // threads take every n-th CTA's sums and are added in their order.
 template <bool F16>
-__global__ void __launch_bounds__(512) join_kernel(const DecodeParams P, int heads) {
+__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ DecodeParams P, int heads) {
   const int2 m = P.meta[blockIdx.x];
   if (m.x < 0) return;
   const int pairs = P.Hkv * P.head_tiles;
@@ -598,12 +761,12 @@ DecodeSpace decode_space(int grid, int heads, int D) {
 // CTAs of any sm_103 part; the workspace is sized for them without asking a device.
 constexpr int DEC_GRID_MAX = 160;
 
-template <bool F16, int NT, int WARPS>
+template <bool F16, int NT, int T>
 ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int grid, int dev, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(&decode_kernel<F16, NT, WARPS>);
+  const void* fn = reinterpret_cast<const void*>(&decode_kernel<F16, NT, T>);
   const ffpa_status st = set_smem_attr_once(fn, dev, (int)pl.smem);
   if (st != FFPA_OK) return st;
-  decode_kernel<F16, NT, WARPS><<<grid, pl.wd * pl.wk * 32, pl.smem, stream>>>(P);
+  decode_kernel<F16, NT, T><<<grid, (pl.teams * DEC_TEAM + DEC_COPY_WARPS) * 32, pl.smem, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
   const int heads = 8 * NT;
   const int rows = P.group < heads ? P.group : heads;
@@ -611,14 +774,22 @@ ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int gr
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
+template <bool F16, int T>
+ffpa_status launch_decode_tile(const DecodeParams& P, const DecodePlan& pl, int grid, int dev, cudaStream_t stream) {
+  if (pl.nt == 1) return launch_decode_as<F16, 1, T>(P, pl, grid, dev, stream);
+  if (T < 32 || pl.nt == 2) return launch_decode_as<F16, 2, T>(P, pl, grid, dev, stream);
+  return launch_decode_as<F16, T < 32 ? 2 : 4, T>(P, pl, grid, dev, stream);
+}
+
 template <bool F16>
 ffpa_status launch_decode(const DecodeParams& P, const DecodePlan& pl, int grid, int dev, cudaStream_t stream) {
-  const bool wide = pl.wd * pl.wk > 8;
-  if (pl.nt == 1)
-    return wide ? launch_decode_as<F16, 1, 16>(P, pl, grid, dev, stream) : launch_decode_as<F16, 1, 8>(P, pl, grid, dev, stream);
-  if (pl.nt == 2)
-    return wide ? launch_decode_as<F16, 2, 16>(P, pl, grid, dev, stream) : launch_decode_as<F16, 2, 8>(P, pl, grid, dev, stream);
-  return launch_decode_as<F16, 4, 8>(P, pl, grid, dev, stream);
+  switch (pl.tile) {
+    case 16: return launch_decode_tile<F16, 16>(P, pl, grid, dev, stream);
+    case 32: return launch_decode_tile<F16, 32>(P, pl, grid, dev, stream);
+    case 64: return launch_decode_tile<F16, 64>(P, pl, grid, dev, stream);
+    case 128: return launch_decode_tile<F16, 128>(P, pl, grid, dev, stream);
+    default: return launch_decode_tile<F16, 256>(P, pl, grid, dev, stream);
+  }
 }
 
 }  // namespace
@@ -710,11 +881,35 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   P.num_pages = num_pages;
   P.page_size = page_size;
   P.max_pages = held ? max_pages : 0;   // without pages every request is empty
-  P.wd = pl.wd;
-  P.wk = pl.wk;
-  P.tile = pl.tile;
-  P.pitch = pl.pitch;
-  P.slots = pl.slots;
+  P.chunks = pl.chunks;
+  // Boxes of as many rows as divide a page, down to the 8 of the swizzle.
+  P.boxed = held && page_size % 8 == 0;
+  P.box_rows = pl.tile;
+  P.box_chunks = D % 64 == 0 ? pl.chunks : 1;
+  if (P.boxed) {
+    while (page_size % P.box_rows != 0) P.box_rows /= 2;
+    for (int i = 0; i < 2; ++i) {
+      const int64_t* s = i ? v_str : k_str;
+      CUtensorMap* map = i ? &P.map_v : &P.map_k;
+      const void* base = i ? v_cache : k_cache;
+      if (P.box_chunks > 1) {
+        const uint64_t dims[5] = {64, (uint64_t)page_size, (uint64_t)pl.chunks, (uint64_t)Hkv, (uint64_t)num_pages};
+        const uint64_t str[4] = {(uint64_t)s[1] * 2, 128, (uint64_t)s[2] * 2, (uint64_t)s[0] * 2};
+        const uint32_t box[5] = {64, (uint32_t)P.box_rows, (uint32_t)pl.chunks, 1, 1};
+        st = encode_rows(map, dt, 5, base, dims, str, box);
+      } else {
+        const uint64_t dims[4] = {(uint64_t)D, (uint64_t)page_size, (uint64_t)Hkv, (uint64_t)num_pages};
+        const uint64_t str[3] = {(uint64_t)s[1] * 2, (uint64_t)s[2] * 2, (uint64_t)s[0] * 2};
+        const uint32_t box[4] = {64, (uint32_t)P.box_rows, 1, 1};
+        st = encode_rows(map, dt, 4, base, dims, str, box);
+      }
+      if (st != FFPA_OK) return st;
+    }
+  }
+  P.ring_k = pl.ring_k;
+  P.ring_v = pl.ring_v;
+  P.timeout_ns = options && options->wait_timeout_ns ? options->wait_timeout_ns : 2000000000ull;
+  P.drop = options && options->test_drop_first_copy ? 1 : 0;
   P.scale_log2 = sc * 1.4426950408889634f;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dt == FFPA_FP16 ? launch_decode<true>(P, pl, grid, dev, s) : launch_decode<false>(P, pl, grid, dev, s);

@@ -17,6 +17,11 @@ ffpa_status call_device(std::initializer_list<const void*> ptrs, int* dev);
 // number of SMs.
 ffpa_status call_status(int dev, const ffpa_options* options, int** err, int* sms);
 
+// Tensor map of 64-column boxes of 16-bit rows with the 128-byte swizzle; byte
+// strides of dims 1 .. rank - 1, zeros outside.
+ffpa_status encode_rows(CUtensorMap* map, ffpa_dtype dt, int rank, const void* base, const uint64_t* dims,
+                        const uint64_t* stride_bytes, const uint32_t* box);
+
 inline bool on_boundary(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // As for the attention inputs: unit last stride, every other stride of a
@@ -61,13 +66,13 @@ __device__ __forceinline__ void store16(void* p, float x) {
 
 // 16 bytes from global to shared memory; bytes = 0 writes zeros and reads nothing.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes));
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// An arrival of this thread on `bar` once its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -78,12 +83,6 @@ __device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldm_x2(uint32_t addr, uint32_t (&r)[2]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-               : "=r"(r[0]), "=r"(r[1])
                : "r"(addr)
                : "memory");
 }

@@ -299,7 +299,8 @@ def decode_paged_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
 
 def ffpa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                       seq_lens: torch.Tensor, *, scale: float | None = None, enable_gqa: bool = False,
-                      return_lse: bool = False, out=None, lse=None, workspace=None, stream=None, status=None):
+                      return_lse: bool = False, out=None, lse=None, workspace=None, stream=None, status=None,
+                      wait_timeout_ns=None, test_drop_first_copy=False):
     """Attention of one new token per request over a paged cache, through ``ffpa_decode_paged``.
 
     q [B,Hq,D]; k_cache, v_cache [num_pages,page_size,Hkv,D] (any strides with D stride 1);
@@ -309,7 +310,8 @@ def ffpa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     The lengths stay on the device, so a captured call serves any lengths.  A page or length out of
     range is not followed; the status word (see ffpa_fwd) receives FFPA_ERR_INVALID.  workspace: a
     uint8 device tensor of decode_paged_workspace_bytes(...) bytes, 256-byte aligned (allocated here
-    when None); calls that may overlap on the GPU need one each."""
+    when None); calls that may overlap on the GPU need one each.  wait_timeout_ns and
+    test_drop_first_copy: as for ffpa_fwd."""
     if q.dim() != 3:
         raise ValueError("q must be 3-D [B, Hq, D]")
     B, Hq, D = q.shape
@@ -330,7 +332,7 @@ def ffpa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     lib = load_library()
     ws = _workspace(workspace, int(lib.ffpa_decode_paged_workspace_bytes(Hq, Hkv, D)), q.device, stream)
     sc = None if scale is None else ctypes.byref(ctypes.c_float(float(scale)))
-    opts = None if status is None else _options(q, None, status, None, False)
+    opts = _options(q, None, status, wait_timeout_ns, test_drop_first_copy)
     st = lib.ffpa_decode_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                                None if lse is None else lse.data_ptr(), _dtype_code(q), B, Hq, Hkv, D, num_pages,
                                page_size, block_table.shape[1], _I64x3(*q.stride()), _I64x4(*k_cache.stride()),

@@ -480,8 +480,9 @@ ffpa_status ffpa_bwd_noalloc(const void* q, const void* k, const void* v, const 
  * Page numbers, slots and lengths live on the device and cannot be checked by
  * the host.  The kernels check them: one that is out of range is never used
  * as an address, and the call's status word (ffpa_options.status, or the
- * device's fallback word) records FFPA_ERR_INVALID.  The other options have
- * no effect on these entry points.
+ * device's fallback word) records FFPA_ERR_INVALID.  ffpa_decode_paged takes
+ * the wait limit and the test hook too; the other options have no effect on
+ * these entry points.
  */
 
 /*

@@ -244,6 +244,19 @@ def test_decode_is_repeatable_on_streams_and_in_graphs():
     device_ok()
 
 
+def test_decode_reports_a_wait_that_runs_out():
+    """A copy that never starts: the call ends after its limit with the timeout status, and the next
+    call is whole."""
+    for D in (64, 512, 1024):
+        args, ref = decode_case([300, 20], 4, 2, D, 16, BF, seed=19)
+        word = status_word()
+        pkg.ffpa_decode_paged(*args, enable_gqa=True, status=word, wait_timeout_ns=3_000_000, test_drop_first_copy=True)
+        torch.cuda.synchronize()
+        assert word.item() == pkg.FFPA_ERR_DEVICE_TIMEOUT
+        check_decode(args, ref)
+    device_ok()
+
+
 # ------------------------------------------------------------------------------------ append
 def append_case(T, Hq, Hkv, D, rot, page, dtype, wdtype, norm, seed=0, far=4000):
     g = torch.Generator().manual_seed(seed)
