@@ -44,6 +44,8 @@ namespace {
 constexpr int DEC_TEAM = 8;           // warps of a team
 constexpr int DEC_COPY_WARPS = 4;     // two for K, two for V
 constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
+// CTAs of any sm_103 part; the workspace is sized for them without asking a device.
+constexpr int DEC_GRID_MAX = 160;
 
 struct DecodeParams {
   CUtensorMap map_k, map_v;
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
       if (P.lse)
         for (int h = tid; h < P.Hq; h += THREADS) P.lse[(int64_t)b * P.Hq + h] = -INFINITY;
     }
-    if (c >= runs) return;
+    if (c >= runs) return;   // (an exit counts for the dependent launch too)
     // Columns behind D meet zeros of Q and must be finite (boxes bring zeros).
     if (!P.boxed && P.D % 16 != 0) {
       char* ring = smem + decode_score_bytes(NT, T);
@@ -387,6 +389,7 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
     cur.u = (int)(r / cur.tiles);
     cur.t = (int)(r % cur.tiles);
   }
+  dependents_launch();
   const int n_tiles = (int)(hi - lo);
   float* scores = reinterpret_cast<float*>(smem);                  // [TEAMS][2, or 1 when OWN][PARTS][HEADS][SPITCH]
   const uint32_t ring_k = smem_u32(smem + decode_score_bytes(NT, T));
@@ -692,10 +695,16 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
 }
 
 // Joins the partial sums of a pair cut between CTAs: block (c, row) the row of
-// the pair that CTA c began, over CTAs c .. last, in that order.  Groups of
-// threads take every n-th CTA's sums and are added in their order.
+// the pair that CTA c began, over CTAs c .. last.  Their weights come first (a
+// thread each), then groups of threads add every n-th CTA's sums, with four
+// loads on the way, and the groups are added in their order.
+constexpr int JOIN_THREADS = 512;
 template <bool F16>
-__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ DecodeParams P, int heads) {
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const DecodeParams P, int heads) {
+  __shared__ float4 acc_s[JOIN_THREADS];
+  __shared__ float w_s[DEC_GRID_MAX];
+  __shared__ float red_s[JOIN_THREADS / 32];
+  dependency_wait();
   const int2 m = P.meta[blockIdx.x];
   if (m.x < 0) return;
   const int pairs = P.Hkv * P.head_tiles;
@@ -703,40 +712,54 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Decod
   const int hk = u / P.head_tiles, ht = u % P.head_tiles;
   if (row >= P.group - ht * heads) return;
   const int hq = hk * P.group + ht * heads + row;
-  const int n = m.y - blockIdx.x + 1;
-  const int cols = P.D / 4;                        // float4 columns
-  const int groups = blockDim.x / cols;            // at least 2 (D <= 1024)
-  const int g = threadIdx.x / cols, col = threadIdx.x % cols;
-  __shared__ float4 acc_s[512];
-  __shared__ float sum_sh[512];
-  auto slot_of = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1 : 2 * (int64_t)(blockIdx.x + i); };
-  float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, P.part_ml[slot_of(i) * heads + row].x);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float4 a = make_float4(0, 0, 0, 0);
-  float l = 0.0f;
-  if (g < groups)
-    for (int i = g; i < n; i += groups) {
-      const float2 ml = P.part_ml[slot_of(i) * heads + row];
-      const float w = ex2_approx(ml.x - base);
-      const float4 x = *reinterpret_cast<const float4*>(P.part + (slot_of(i) * heads + row) * P.D + col * 4);
-      a.x += w * x.x;
-      a.y += w * x.y;
-      a.z += w * x.z;
-      a.w += w * x.w;
-      l += w * ml.y;
+  const int n = m.y - blockIdx.x + 1;              // at most DEC_GRID_MAX
+  const int tid = threadIdx.x;
+  // The first CTA's sums are its second partial pair, the others' their first.
+  const int64_t first = 2 * (int64_t)blockIdx.x + 1;
+  auto slot_of = [&](int i) { return i == 0 ? first : first - 1 + 2 * i; };
+  auto reduce = [&](float x, bool max) {           // over the block, in a fixed tree
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const float y = __shfl_xor_sync(~0u, x, d);
+      x = max ? fmaxf(x, y) : x + y;
     }
-  acc_s[threadIdx.x] = a;
-  sum_sh[threadIdx.x] = l;
+    __syncthreads();
+    if (tid % 32 == 0) red_s[tid / 32] = x;
+    __syncthreads();
+    x = red_s[0];
+    for (int i = 1; i < (DEC_GRID_MAX + 31) / 32; ++i) x = max ? fmaxf(x, red_s[i]) : x + red_s[i];
+    return x;
+  };
+  const float2 ml = tid < n ? P.part_ml[slot_of(tid) * heads + row] : make_float2(-INFINITY, 0.0f);
+  const float top = reduce(ml.x, true);
+  const float w = ex2_approx(ml.x - (top == -INFINITY ? 0.0f : top));
+  if (tid < n) w_s[tid] = w;
+  const float l = reduce(w * ml.y, false);         // (also: the weights are written)
+  const int cols = P.D / 4;                        // float4 columns
+  const int groups = JOIN_THREADS / cols;          // at least 2 (D <= 1024)
+  const int g = tid / cols, col = tid % cols;
+  float4 a = make_float4(0, 0, 0, 0);
+  if (g < groups) {
+    const float* from = P.part + row * P.D + col * 4;
+#pragma unroll 4
+    for (int i = g; i < n; i += groups) {
+      const float f = w_s[i];
+      const float4 x = *reinterpret_cast<const float4*>(from + slot_of(i) * heads * P.D);
+      a.x += f * x.x;
+      a.y += f * x.y;
+      a.z += f * x.z;
+      a.w += f * x.w;
+    }
+  }
+  acc_s[tid] = a;
   __syncthreads();
   if (g != 0) return;
-  for (int w = 1; w < groups; ++w) {
-    const float4 x = acc_s[w * cols + col];
+  for (int i = 1; i < groups; ++i) {
+    const float4 x = acc_s[i * cols + col];
     a.x += x.x;
     a.y += x.y;
     a.z += x.z;
     a.w += x.w;
-    l += sum_sh[w * cols + col];
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   *reinterpret_cast<uint2*>(P.o + b * P.o_sb + (int64_t)hq * P.o_sh + col * 8) =
@@ -758,9 +781,6 @@ DecodeSpace decode_space(int grid, int heads, int D) {
   return s;
 }
 
-// CTAs of any sm_103 part; the workspace is sized for them without asking a device.
-constexpr int DEC_GRID_MAX = 160;
-
 template <bool F16, int NT, int T>
 ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int grid, int dev, cudaStream_t stream) {
   const void* fn = reinterpret_cast<const void*>(&decode_kernel<F16, NT, T>);
@@ -770,8 +790,21 @@ ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int gr
   if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
   const int heads = 8 * NT;
   const int rows = P.group < heads ? P.group : heads;
-  join_kernel<F16><<<dim3(grid, rows), 512, 0, stream>>>(P, heads);
-  return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
+  // A dependent launch: its blocks are set up while the first kernel runs out.
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, rows);
+  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<F16>, P, heads) != cudaSuccess) {
+    cudaGetLastError();
+    return FFPA_ERR_CUDA;
+  }
+  return FFPA_OK;
 }
 
 template <bool F16, int T>
