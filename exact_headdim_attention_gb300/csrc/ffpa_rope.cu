@@ -2,158 +2,265 @@
 // the same with keys and values going to their slots of a paged cache.
 //
 // Each row is read once and written once: the memory's bandwidth is the bound.
-// A work item is a few heads of one token, so that the cosines and sines of
-// that token (one sincospif per pair) are shared by its heads.
+//  - A work item is some heads of one token, so that the token's cosines and
+//    sines (one sincospif per pair) are shared by its heads; with the weights
+//    they make four factors a pair, and a row costs two products and the
+//    row's scale for each value.
+//  - Rows come through shared memory by asynchronous copies, DEPTH - 1 of them
+//    ahead: each thread copies the very bytes that it will work on, so the
+//    ring needs no barrier and the rows on their way no registers.  Some 100 KB an
+//    SM are in flight, which the memory's latency takes (with loads into
+//    registers, one row at a time read and wrote 3.1 TB/s, four at a time 3.9).
 #include "ffpa_rope.cuh"
 
 namespace ffpa {
 namespace {
 
 constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_DEPTH = 6;
+
+// Where the rows of a work item are: queries, keys or (append) values.
+struct RopeItem {
+  const char* src;
+  int64_t src_h;
+  int which, wt, heads, h0, b, n;
+};
+__device__ __forceinline__ RopeItem rope_item(const RopeParams& P, int64_t item) {
+  RopeItem r;
+  const bool in = item < P.items[0] + P.items[1] + P.items_v;
+  r.which = item < P.items[0] ? 0 : item < P.items[0] + P.items[1] ? 1 : 2;
+  r.wt = r.which == 0 ? 0 : 1;
+  const int64_t local = !in ? 0 : r.which == 0 ? item : r.which == 1 ? item - P.items[0] : item - P.items[0] - P.items[1];
+  const int64_t token = local / P.chunks[r.wt];
+  r.h0 = (int)(local - token * P.chunks[r.wt]) * P.heads_per[r.wt];
+  r.heads = in ? min(P.t[r.wt].H - r.h0, P.heads_per[r.wt]) : 0;
+  r.b = (int)(token / P.N);
+  r.n = (int)(token - (int64_t)r.b * P.N);
+  if (r.which == 2) {
+    r.src_h = P.vs[0];
+    r.src = P.v + r.n * P.vs[1] + r.h0 * r.src_h;
+  } else {
+    const RopeTensor& t = P.t[r.wt];
+    r.src_h = t.xs[1];
+    r.src = t.x + r.b * t.xs[0] + r.n * t.xs[2] + r.h0 * r.src_h;
+  }
+  return r;
+}
+
+template <int VEC, int ITER>
+__host__ __device__ constexpr int rope_row_bytes() {   // of one row, for all threads of a block
+  return ROPE_THREADS * ITER * 2 * VEC * 2;
+}
 
 template <bool F16, int VEC, int LPR, int ITER, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) {
+__global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(const __grid_constant__ RopeParams P) {
+  constexpr int ROW = rope_row_bytes<VEC, ITER>(), PIECE = ROPE_THREADS * VEC * 2;
+  extern __shared__ __align__(16) char ring[];     // [ROPE_DEPTH][ITER][2][thread] vectors
+  __shared__ long long freq_s[512];
+  load_freqs(P, freq_s);
   const int lane = threadIdx.x % LPR;
-  const int64_t group = (int64_t)blockIdx.x * (ROPE_THREADS / LPR) + threadIdx.x / LPR;
   const int64_t all = P.items[0] + P.items[1] + P.items_v;
-  // Whole warps stay in the loop: the lanes of a row talk through shuffles.
-  const int64_t warp_first = group - (threadIdx.x % 32) / LPR;
   const int64_t stride = (int64_t)gridDim.x * (ROPE_THREADS / LPR);
   RopeChunk<VEC> ch[ITER];
-  long long freq[ITER][VEC];
 #pragma unroll
-  for (int k = 0; k < ITER; ++k) {
-    ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
+  for (int k = 0; k < ITER; ++k) ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
+  const float inv_d = 1.0f / P.D;
+  // Whole warps stay in the loop: the lanes of a row talk through shuffles.
+  const int sub = threadIdx.x % 32 / LPR;
+  int64_t first = (int64_t)blockIdx.x * (ROPE_THREADS / LPR) + threadIdx.x / 32 * (32 / LPR);
+  const int per = P.heads_max;                     // steps of an item
+  char* own = ring + threadIdx.x * (VEC * 2);
+  const uint32_t own_at = smem_u32(own);
+
+  // The copying runs ahead of the work by DEPTH - 1 steps, into later items too.
+  int64_t ahead = first;
+  int ahead_h = 0, ahead_heads = 0, ahead_slot = 0;
+  const char* ahead_src = nullptr;
+  int64_t ahead_stride = 0;
+  auto issue = [&] {
+    if (ahead < all) {
+      if (ahead_h == 0) {
+        const RopeItem it = rope_item(P, ahead + sub);
+        ahead_heads = it.heads;
+        ahead_src = it.src;
+        ahead_stride = it.src_h;
+      }
+      if (ahead_h < ahead_heads) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      freq[k][i] = ch[k].live && ch[k].pair ? freq_turns(P.inv_freq[(lane + k * LPR) * VEC + i]) : 0;
-  }
-  for (int64_t first = warp_first; first < all; first += stride) {
-    const int64_t item = first + (threadIdx.x % 32) / LPR;
-    const bool in = item < all;
-    const int which = item < P.items[0] ? 0 : item < P.items[0] + P.items[1] ? 1 : 2;
-    const int64_t local = !in ? 0 : which == 0 ? item : which == 1 ? item - P.items[0] : item - P.items[0] - P.items[1];
-    const int wt = which == 2 ? 1 : which;
-    const RopeTensor& t = P.t[wt];
-    const int64_t token = local / P.chunks[wt];
-    const int h0 = (int)(local % P.chunks[wt]) * P.heads_per[wt];
-    const int h1 = in ? min(t.H, h0 + P.heads_per[wt]) : h0;
-    const int b = (int)(token / P.N), n = (int)(token % P.N);
-    // The slot of a cached row; a negative one is padding and is not stored.
-    int64_t page = 0, slot = -1;
-    if (which > 0 && P.slots && in) {
-      slot = P.slots[n];
+        for (int k = 0; k < ITER; ++k)
+          if (ch[k].live) {
+            const uint32_t to = own_at + ahead_slot * ROW + 2 * k * PIECE;
+            copy_async<VEC * 2>(to, ahead_src + ch[k].a * 2);
+            copy_async<VEC * 2>(to + PIECE, ahead_src + ch[k].b * 2);
+          }
+        ahead_src += ahead_stride;
+      }
+      if (++ahead_h == per) {
+        ahead_h = 0;
+        ahead += stride;
+      }
+      if (++ahead_slot == ROPE_DEPTH) ahead_slot = 0;
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < ROPE_DEPTH - 1; ++i) issue();
+
+  int ring_slot = 0;
+  for (; first < all; first += stride) {
+    const RopeItem it = rope_item(P, first + sub);
+    const RopeTensor& t = P.t[it.wt];
+    const bool norm = it.which < 2 && t.w;
+    int heads = it.heads;
+    char* dst;
+    int64_t dst_h;
+    if (it.which > 0 && P.slots) {
+      // The slot of a cached row; a negative one is padding and is not stored.
+      int64_t slot = heads > 0 ? P.slots[it.n] : -1;
       if (slot >= P.n_slots) {
         report_invalid(P.err);
         slot = -1;
       }
-      if (slot >= 0) {
-        page = slot / P.slot_page;
-        slot -= page * P.slot_page;
-      }
+      if (slot < 0) heads = 0;
+      const int64_t page = slot / P.slot_page;
+      slot -= page * P.slot_page;
+      dst_h = it.which == 2 ? P.vcs[2] : P.kcs[2];
+      dst = it.which == 2 ? P.vc + page * P.vcs[0] + slot * P.vcs[1] : P.kc + page * P.kcs[0] + slot * P.kcs[1];
+    } else {
+      dst_h = t.ys[1];
+      dst = t.y + it.b * t.ys[0] + it.n * t.ys[2];
     }
-    if (which == 2) {
-      if (slot >= 0)
-        for (int h = h0; h < h1; ++h) {
-          const uint4* src = reinterpret_cast<const uint4*>(P.v + h * P.vs[0] + n * P.vs[1]);
-          uint4* dst = reinterpret_cast<uint4*>(P.vc + page * P.vcs[0] + slot * P.vcs[1] + h * P.vcs[2]);
-          for (int i = lane; i < P.D / 8; i += LPR) dst[i] = src[i];
-        }
-    }
-    float cs[ITER][VEC], sn[ITER][VEC], w[ITER][2 * VEC];
-    if (which < 2 && in) {
-      const long long pos = P.rot ? position_of(P, b, n) : 0;
+    dst += it.h0 * dst_h;
+    // Factors of a pair: (a, b) -> (a fa[i] - b fb[i], b ga[i] + a gb[i]); of
+    // columns that are not rotated: (a fa[i], b ga[i]).
+    float fa[ITER][VEC], fb[ITER][VEC], ga[ITER][VEC], gb[ITER][VEC];
+    if (it.which < 2 && heads > 0) {
+      const long long pos = P.rot ? position_of(P, it.b, it.n) : 0;
 #pragma unroll
       for (int k = 0; k < ITER; ++k) {
         if (!ch[k].live) continue;
-        if (ch[k].pair) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) turn(pos, freq[k][i], P.rope_scale, cs[k][i], sn[k][i]);
+        float w[2 * VEC];
+        if (norm) {
+          load_weight<F16, VEC>(t.w, P.w32, ch[k].a, w);
+          load_weight<F16, VEC>(t.w, P.w32, ch[k].b, w + VEC);
         }
-        if (t.w) {
-          load_weight<F16, VEC>(t.w, P.w32, ch[k].a, w[k]);
-          load_weight<F16, VEC>(t.w, P.w32, ch[k].b, w[k] + VEC);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float wa = norm ? w[pair_a<VEC, INTER>(i)] : 1.0f, wb = norm ? w[pair_b<VEC, INTER>(i)] : 1.0f;
+          fa[k][i] = wa;
+          ga[k][i] = wb;
+          if (ch[k].pair) {
+            float c, s;
+            turn(pos, freq_s[(lane + k * LPR) * VEC + i], P.rope_scale, c, s);
+            fa[k][i] = wa * c;
+            fb[k][i] = wb * s;
+            ga[k][i] = wb * c;
+            gb[k][i] = wa * s;
+          }
         }
       }
     }
-    const int heads = P.heads_per[0] > P.heads_per[1] ? P.heads_per[0] : P.heads_per[1];
-    for (int i = 0; i < heads; ++i) {
-      const int h = h0 + i;
-      const bool on = which < 2 && h < h1;
-      float x[ITER][2 * VEC];
+#pragma unroll 1
+    for (int h = 0; h < per; ++h) {
+      copy_wait<ROPE_DEPTH - 2>();
+      const char* row = own + ring_slot * ROW;
+      if (++ring_slot == ROPE_DEPTH) ring_slot = 0;
+      const bool on = h < heads;
+      Raw<VEC> ra[ITER], rb[ITER];
       float sq = 0.0f;
       if (on) {
-        const char* src = t.x + b * t.xs[0] + h * t.xs[1] + n * t.xs[2];
 #pragma unroll
-        for (int k = 0; k < ITER; ++k) {
-          if (!ch[k].live) continue;
-          widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(src + ch[k].a * 2), x[k]);
-          widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(src + ch[k].b * 2), x[k] + VEC);
+        for (int k = 0; k < ITER; ++k)
+          if (ch[k].live) {
+            ra[k] = own_load<VEC>(row + 2 * k * PIECE);
+            rb[k] = own_load<VEC>(row + (2 * k + 1) * PIECE);
+            if (norm) {
+              float x[2 * VEC];
+              widen<F16, VEC>(ra[k], x);
+              widen<F16, VEC>(rb[k], x + VEC);
 #pragma unroll
-          for (int j = 0; j < 2 * VEC; ++j) sq += x[k][j] * x[k][j];
-        }
+              for (int i = 0; i < 2 * VEC; ++i) sq += x[i] * x[i];
+            }
+          }
       }
+      issue();
       sq = row_sum<LPR>(sq);
       if (!on) continue;
-      const float r = rsqrtf(sq / P.D + P.eps);
-      char* dst = t.y + b * t.ys[0] + h * t.ys[1] + n * t.ys[2];
-      if (which == 1 && P.slots) {
-        if (slot < 0) continue;
-        dst = P.kc + page * P.kcs[0] + slot * P.kcs[1] + h * P.kcs[2];
-      }
+      const float r = norm ? rsqrtf(sq * inv_d + P.eps) : 1.0f;
 #pragma unroll
-      for (int k = 0; k < ITER; ++k) {
-        if (!ch[k].live) continue;
-        if (t.w) {
+      for (int k = 0; k < ITER; ++k)
+        if (ch[k].live) {
+          if (it.which < 2) {
+            float x[2 * VEC], y[2 * VEC];
+            widen<F16, VEC>(ra[k], x);
+            widen<F16, VEC>(rb[k], x + VEC);
 #pragma unroll
-          for (int j = 0; j < 2 * VEC; ++j) x[k][j] *= r * w[k][j];
+            for (int i = 0; i < VEC; ++i) {
+              const int ia = pair_a<VEC, INTER>(i), ib = pair_b<VEC, INTER>(i);
+              float u = x[ia] * fa[k][i], v = x[ib] * ga[k][i];
+              if (ch[k].pair) {
+                u -= x[ib] * fb[k][i];
+                v += x[ia] * gb[k][i];
+              }
+              y[ia] = u * r;
+              y[ib] = v * r;
+            }
+            ra[k] = narrow<F16, VEC>(y);
+            rb[k] = narrow<F16, VEC>(y + VEC);
+          }
+          *reinterpret_cast<Raw<VEC>*>(dst + ch[k].a * 2) = ra[k];
+          *reinterpret_cast<Raw<VEC>*>(dst + ch[k].b * 2) = rb[k];
         }
-        if (ch[k].pair) rotate<VEC, INTER, false>(x[k], cs[k], sn[k]);
-        *reinterpret_cast<Raw<VEC>*>(dst + ch[k].a * 2) = narrow<F16, VEC>(x[k]);
-        *reinterpret_cast<Raw<VEC>*>(dst + ch[k].b * 2) = narrow<F16, VEC>(x[k] + VEC);
-      }
+      dst += dst_h;
     }
   }
+  copy_wait<0>();
 }
 
 template <bool F16, int VEC, int LPR, int ITER>
-ffpa_status launch_rope_as(const RopeParams& P, bool inter, int sms, cudaStream_t stream) {
+ffpa_status launch_rope_as(const RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t all = P.items[0] + P.items[1] + P.items_v;
   const int64_t per = ROPE_THREADS / LPR;
   int64_t grid = (all + per - 1) / per;
-  if (grid > (int64_t)sms * 16) grid = (int64_t)sms * 16;
-  if (inter)
-    rope_kernel<F16, VEC, LPR, ITER, true><<<(int)grid, ROPE_THREADS, 0, stream>>>(P);
-  else
-    rope_kernel<F16, VEC, LPR, ITER, false><<<(int)grid, ROPE_THREADS, 0, stream>>>(P);
+  // As many blocks as are resident, so that the frequencies are formed once
+  // and no last wave is left over.
+  const int64_t resident = (int64_t)sms * (ITER == 1 ? 3 : 2);
+  if (grid > resident) grid = resident;
+  const int smem = ROPE_DEPTH * rope_row_bytes<VEC, ITER>();
+  auto fn = inter ? &rope_kernel<F16, VEC, LPR, ITER, true> : &rope_kernel<F16, VEC, LPR, ITER, false>;
+  const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(fn), dev, smem);
+  if (st != FFPA_OK) return st;
+  fn<<<(int)grid, ROPE_THREADS, smem, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
 template <bool F16>
-ffpa_status launch_rope(RopeParams& P, bool inter, int sms, cudaStream_t stream) {
+ffpa_status launch_rope(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t tokens = (int64_t)P.B * P.N;
-  // Heads of an item: as many as leave every SM some 32 rows in work.
+  // Heads of an item: 8 share a token's sines, fewer where that would leave
+  // SMs without work.
   for (int i = 0; i < 2; ++i) {
     int per = 8;
     while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
-    P.heads_per[i] = per;
     P.chunks[i] = (P.t[i].H + per - 1) / per;
+    P.heads_per[i] = (P.t[i].H + P.chunks[i] - 1) / P.chunks[i];
     P.items[i] = P.t[i].x ? tokens * P.chunks[i] : 0;
   }
+  P.heads_max = P.items[0] && P.heads_per[0] > P.heads_per[1] ? P.heads_per[0] : P.heads_per[1];
   P.items_v = P.slots ? tokens * P.chunks[1] : 0;
   if (rope_vec(P.D, P.rot) == 8) {
     const int n = P.D / 16;
-    if (n <= 4) return launch_rope_as<F16, 8, 4, 1>(P, inter, sms, stream);
-    if (n <= 8) return launch_rope_as<F16, 8, 8, 1>(P, inter, sms, stream);
-    if (n <= 16) return launch_rope_as<F16, 8, 16, 1>(P, inter, sms, stream);
-    if (n <= 32) return launch_rope_as<F16, 8, 32, 1>(P, inter, sms, stream);
-    return launch_rope_as<F16, 8, 32, 2>(P, inter, sms, stream);
+    if (n <= 4) return launch_rope_as<F16, 8, 4, 1>(P, inter, sms, dev, stream);
+    if (n <= 8) return launch_rope_as<F16, 8, 8, 1>(P, inter, sms, dev, stream);
+    if (n <= 16) return launch_rope_as<F16, 8, 16, 1>(P, inter, sms, dev, stream);
+    if (n <= 32) return launch_rope_as<F16, 8, 32, 1>(P, inter, sms, dev, stream);
+    return launch_rope_as<F16, 8, 32, 2>(P, inter, sms, dev, stream);
   }
   const int n = P.D / 8;
-  if (n <= 16) return launch_rope_as<F16, 4, 16, 1>(P, inter, sms, stream);
-  if (n <= 32) return launch_rope_as<F16, 4, 32, 1>(P, inter, sms, stream);
-  if (n <= 64) return launch_rope_as<F16, 4, 32, 2>(P, inter, sms, stream);
-  return launch_rope_as<F16, 4, 32, 4>(P, inter, sms, stream);
+  if (n <= 16) return launch_rope_as<F16, 4, 16, 1>(P, inter, sms, dev, stream);
+  if (n <= 32) return launch_rope_as<F16, 4, 32, 1>(P, inter, sms, dev, stream);
+  if (n <= 64) return launch_rope_as<F16, 4, 32, 2>(P, inter, sms, dev, stream);
+  return launch_rope_as<F16, 4, 32, 4>(P, inter, sms, dev, stream);
 }
 
 }  // namespace
@@ -233,8 +340,8 @@ ffpa_status ffpa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k
     }
   }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return dt == FFPA_FP16 ? launch_rope<true>(P, rope->interleaved != 0, sms, s)
-                         : launch_rope<false>(P, rope->interleaved != 0, sms, s);
+  return dt == FFPA_FP16 ? launch_rope<true>(P, rope->interleaved != 0, sms, dev, s)
+                         : launch_rope<false>(P, rope->interleaved != 0, sms, dev, s);
 }
 
 ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
@@ -293,8 +400,8 @@ ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_
   P.n_slots = (int64_t)num_pages * page_size;
   P.slot_page = page_size;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return dt == FFPA_FP16 ? launch_rope<true>(P, rope->interleaved != 0, sms, s)
-                         : launch_rope<false>(P, rope->interleaved != 0, sms, s);
+  return dt == FFPA_FP16 ? launch_rope<true>(P, rope->interleaved != 0, sms, dev, s)
+                         : launch_rope<false>(P, rope->interleaved != 0, sms, dev, s);
 }
 
 }  // extern "C"

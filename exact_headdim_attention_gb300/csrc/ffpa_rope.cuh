@@ -36,6 +36,7 @@ struct RopeParams {
   int pos64, rot, w32, B, N, D;
   float eps, rope_scale;
   int heads_per[2];    // heads of one work item
+  int heads_max;       // the larger of the two
   int64_t items[2];    // work items of queries and of keys
   int chunks[2];       // head chunks of a token
   // append (keys go to pages, values are copied): slots == NULL otherwise
@@ -85,6 +86,13 @@ struct alignas(VEC * 2) Raw {
   uint32_t u[VEC / 2];
 };
 
+// The two vectors of a chunk as a thread keeps them in its own place of shared
+// memory: vector v of chunk k at [k][v][thread].
+template <int VEC>
+__device__ __forceinline__ Raw<VEC> own_load(const char* at) {
+  return *reinterpret_cast<const Raw<VEC>*>(at);
+}
+
 template <bool F16, int VEC>
 __device__ __forceinline__ void widen(const Raw<VEC>& r, float* x) {
 #pragma unroll
@@ -122,6 +130,11 @@ __device__ __forceinline__ long long freq_turns(double inv_freq) {
   f -= rint(f);
   return __double2ll_rn(f * 18446744073709551616.0);
 }
+// The call's frequencies in turns, once per block (rot / 2 <= 512 of them).
+__device__ __forceinline__ void load_freqs(const RopeParams& P, long long* freq_s) {
+  for (int i = threadIdx.x; i < P.rot / 2; i += blockDim.x) freq_s[i] = freq_turns(P.inv_freq[i]);
+  __syncthreads();
+}
 __device__ __forceinline__ void turn(long long pos, long long freq, float scale, float& c, float& s) {
   const unsigned long long t = static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(freq);
   const int hi = static_cast<int>(static_cast<unsigned>(t >> 32));   // turns in [-1/2, 1/2), times 2^32
@@ -135,18 +148,11 @@ __device__ __forceinline__ long long position_of(const RopeParams& P, int b, int
   return P.pos64 ? *reinterpret_cast<const long long*>(p) : *reinterpret_cast<const int*>(p);
 }
 
-// (a, b) of a chunk rotated by +t or, BACK, by -t; the vectors hold pairs
-// (a[i], b[i]), or interleaved ones in the order a then b.
-template <int VEC, bool INTER, bool BACK>
-__device__ __forceinline__ void rotate(float* x, const float* c, const float* s) {
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : VEC + i;
-    const float a = x[ia], b = x[ib], sn = BACK ? -s[i] : s[i];
-    x[ia] = a * c[i] - b * sn;
-    x[ib] = b * c[i] + a * sn;
-  }
-}
+// Values of pair i in a chunk's 2 VEC.
+template <int VEC, bool INTER>
+__device__ __forceinline__ constexpr int pair_a(int i) { return INTER ? 2 * i : i; }
+template <int VEC, bool INTER>
+__device__ __forceinline__ constexpr int pair_b(int i) { return INTER ? 2 * i + 1 : VEC + i; }
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {

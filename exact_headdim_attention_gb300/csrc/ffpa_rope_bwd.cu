@@ -8,6 +8,9 @@
 // row sum in registers) instead of being stored by the forward.  Each row is
 // read twice (x, g) and written once: the memory's bandwidth is the bound.
 //
+// Rows and gradients come through shared memory as in the forward, DEPTH - 1
+// rows ahead (loads into registers, two rows at a time: 2.9 TB/s).
+//
 // dw is summed in fp32 in a fixed order (no atomics): each lane keeps its
 // columns' sums over its rows in registers, a block adds its lanes and writes
 // one row of partial sums, a second launch adds the blocks.
@@ -17,25 +20,32 @@ namespace ffpa {
 namespace {
 
 constexpr int RB_THREADS = 256;
+constexpr int RB_DEPTH = 4;
 constexpr int RB_BLOCKS_MAX = 512;   // blocks of queries and keys together
 
+template <int VEC, int ITER>
+__host__ __device__ constexpr int rb_row_bytes() {     // of one row and its gradient, for all threads of a block
+  return RB_THREADS * ITER * 4 * VEC * 2;
+}
+
 template <bool F16, int VEC, int LPR, int ITER, bool INTER>
-__global__ void __launch_bounds__(RB_THREADS) rope_bwd_kernel(const RopeParams P) {
+__global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel(const __grid_constant__ RopeParams P) {
   constexpr int GROUPS = RB_THREADS / LPR, COLS = LPR * 2 * VEC * ITER;
-  __shared__ float sums[GROUPS][COLS];
-  const int lane = threadIdx.x % LPR, row = threadIdx.x / LPR;
+  constexpr int ROW = rb_row_bytes<VEC, ITER>(), PIECE = RB_THREADS * VEC * 2;
+  static_assert(RB_DEPTH * ROW >= GROUPS * COLS * 4, "the ring holds a block's sums");
+  extern __shared__ __align__(16) char ring[];     // [RB_DEPTH][ITER][g, g, x, x][thread] vectors
+  __shared__ long long freq_s[512];
+  load_freqs(P, freq_s);
+  const int lane = threadIdx.x % LPR, row = threadIdx.x / LPR, sub = threadIdx.x % 32 / LPR;
   const int wt = blockIdx.x < P.blocks[0] ? 0 : 1;
   const int block = blockIdx.x - (wt ? P.blocks[0] : 0);
   const RopeTensor& t = P.t[wt];
+  const float inv_d = 1.0f / P.D;
   RopeChunk<VEC> ch[ITER];
-  long long freq[ITER][VEC];
   float w[ITER][2 * VEC], dw[ITER][2 * VEC];
 #pragma unroll
   for (int k = 0; k < ITER; ++k) {
     ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      freq[k][i] = ch[k].live && ch[k].pair ? freq_turns(P.inv_freq[(lane + k * LPR) * VEC + i]) : 0;
 #pragma unroll
     for (int i = 0; i < 2 * VEC; ++i) dw[k][i] = 0.0f;
     if (ch[k].live && t.w) {
@@ -43,72 +53,138 @@ __global__ void __launch_bounds__(RB_THREADS) rope_bwd_kernel(const RopeParams P
       load_weight<F16, VEC>(t.w, P.w32, ch[k].b, w[k] + VEC);
     }
   }
-  const int64_t stride = (int64_t)P.blocks[wt] * GROUPS;
-  // Whole warps stay in the loop: the lanes of a row talk through shuffles.
-  for (int64_t first = (int64_t)block * GROUPS + (threadIdx.x / 32) * (32 / LPR); first < P.items[wt]; first += stride) {
-    const int64_t item = first + (threadIdx.x % 32) / LPR;
-    const bool in = item < P.items[wt];
+  const int64_t stride = (int64_t)P.blocks[wt] * GROUPS, all = P.items[wt];
+  const int per = P.heads_per[wt];
+  // First head, token and number of heads of an item.
+  struct Item {
+    int h0, heads, b, n;
+  };
+  auto item_of = [&](int64_t item) {
+    Item r;
+    const bool in = item < all;
     const int64_t token = in ? item / P.chunks[wt] : 0;
-    const int h0 = in ? (int)(item % P.chunks[wt]) * P.heads_per[wt] : 0;
-    const int h1 = in ? min(t.H, h0 + P.heads_per[wt]) : h0;
-    const int b = (int)(token / P.N), n = (int)(token % P.N);
+    r.h0 = in ? (int)(item - token * P.chunks[wt]) * per : 0;
+    r.heads = in ? min(t.H - r.h0, per) : 0;
+    r.b = (int)(token / P.N);
+    r.n = (int)(token - (int64_t)r.b * P.N);
+    return r;
+  };
+  // Whole warps stay in the loop: the lanes of a row talk through shuffles.
+  int64_t first = (int64_t)block * GROUPS + threadIdx.x / 32 * (32 / LPR);
+  char* own = ring + threadIdx.x * (VEC * 2);
+  const uint32_t own_at = smem_u32(own);
+  int64_t ahead = first;
+  int ahead_h = 0, ahead_heads = 0, ahead_slot = 0;
+  const char *ahead_g = nullptr, *ahead_x = nullptr;
+  auto issue = [&] {
+    if (ahead < all) {
+      if (ahead_h == 0) {
+        const Item it = item_of(ahead + sub);
+        ahead_heads = it.heads;
+        ahead_g = P.g[wt] + it.b * P.gs[wt][0] + it.h0 * P.gs[wt][1] + it.n * P.gs[wt][2];
+        ahead_x = t.x + it.b * t.xs[0] + it.h0 * t.xs[1] + it.n * t.xs[2];
+      }
+      if (ahead_h < ahead_heads) {
+#pragma unroll
+        for (int k = 0; k < ITER; ++k)
+          if (ch[k].live) {
+            const uint32_t to = own_at + ahead_slot * ROW + 4 * k * PIECE;
+            copy_async<VEC * 2>(to, ahead_g + ch[k].a * 2);
+            copy_async<VEC * 2>(to + PIECE, ahead_g + ch[k].b * 2);
+            if (t.w) {
+              copy_async<VEC * 2>(to + 2 * PIECE, ahead_x + ch[k].a * 2);
+              copy_async<VEC * 2>(to + 3 * PIECE, ahead_x + ch[k].b * 2);
+            }
+          }
+        ahead_g += P.gs[wt][1];
+        ahead_x += t.xs[1];
+      }
+      if (++ahead_h == per) {
+        ahead_h = 0;
+        ahead += stride;
+      }
+      if (++ahead_slot == RB_DEPTH) ahead_slot = 0;
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < RB_DEPTH - 1; ++i) issue();
+
+  int ring_slot = 0;
+  for (; first < all; first += stride) {
+    const Item it = item_of(first + sub);
+    char* to = t.y + it.b * t.ys[0] + it.h0 * t.ys[1] + it.n * t.ys[2];
     float cs[ITER][VEC], sn[ITER][VEC];
-    const long long pos = P.rot ? position_of(P, b, n) : 0;
+    const long long pos = P.rot ? position_of(P, it.b, it.n) : 0;
 #pragma unroll
     for (int k = 0; k < ITER; ++k) {
       if (!ch[k].live || !ch[k].pair) continue;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) turn(pos, freq[k][i], P.rope_scale, cs[k][i], sn[k][i]);
+      for (int i = 0; i < VEC; ++i) turn(pos, freq_s[(lane + k * LPR) * VEC + i], P.rope_scale, cs[k][i], sn[k][i]);
     }
-    for (int i = 0; i < P.heads_per[wt]; ++i) {
-      const int h = h0 + i;
-      const bool on = h < h1;
+#pragma unroll 1
+    for (int h = 0; h < per; ++h) {
+      copy_wait<RB_DEPTH - 2>();
+      const char* from = own + ring_slot * ROW;
+      if (++ring_slot == RB_DEPTH) ring_slot = 0;
+      const bool on = h < it.heads;
       float g[ITER][2 * VEC], x[ITER][2 * VEC];
       float sq = 0.0f, dot = 0.0f;
       if (on) {
-        const char* gp = P.g[wt] + b * P.gs[wt][0] + h * P.gs[wt][1] + n * P.gs[wt][2];
-        const char* xp = t.x + b * t.xs[0] + h * t.xs[1] + n * t.xs[2];
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
           if (!ch[k].live) continue;
-          widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(gp + ch[k].a * 2), g[k]);
-          widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(gp + ch[k].b * 2), g[k] + VEC);
-          if (ch[k].pair) rotate<VEC, INTER, true>(g[k], cs[k], sn[k]);
-          if (t.w) {
-            widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(xp + ch[k].a * 2), x[k]);
-            widen<F16, VEC>(*reinterpret_cast<const Raw<VEC>*>(xp + ch[k].b * 2), x[k] + VEC);
+          widen<F16, VEC>(own_load<VEC>(from + 4 * k * PIECE), g[k]);
+          widen<F16, VEC>(own_load<VEC>(from + (4 * k + 1) * PIECE), g[k] + VEC);
+          if (ch[k].pair) {
 #pragma unroll
-            for (int j = 0; j < 2 * VEC; ++j) {
-              sq += x[k][j] * x[k][j];
-              dot += w[k][j] * g[k][j] * x[k][j];
+            for (int i = 0; i < VEC; ++i) {
+              const int ia = pair_a<VEC, INTER>(i), ib = pair_b<VEC, INTER>(i);
+              const float u = g[k][ia], v = g[k][ib];
+              g[k][ia] = u * cs[k][i] + v * sn[k][i];
+              g[k][ib] = v * cs[k][i] - u * sn[k][i];
+            }
+          }
+          if (t.w) {
+            widen<F16, VEC>(own_load<VEC>(from + (4 * k + 2) * PIECE), x[k]);
+            widen<F16, VEC>(own_load<VEC>(from + (4 * k + 3) * PIECE), x[k] + VEC);
+#pragma unroll
+            for (int i = 0; i < 2 * VEC; ++i) {
+              sq += x[k][i] * x[k][i];
+              dot += w[k][i] * g[k][i] * x[k][i];
             }
           }
         }
       }
+      issue();
       if (t.w) {
         sq = row_sum<LPR>(sq);
         dot = row_sum<LPR>(dot);
       }
       if (!on) continue;
-      const float r = rsqrtf(sq / P.D + P.eps);
-      const float back = r * r * dot / P.D;      // r mean(w g' xn)
-      char* dst = t.y + b * t.ys[0] + h * t.ys[1] + n * t.ys[2];
+      const float r = rsqrtf(sq * inv_d + P.eps);
+      const float back = r * r * dot * inv_d;      // r mean(w g' xn)
 #pragma unroll
       for (int k = 0; k < ITER; ++k) {
         if (!ch[k].live) continue;
         if (t.w) {
 #pragma unroll
-          for (int j = 0; j < 2 * VEC; ++j) {
-            dw[k][j] += g[k][j] * (x[k][j] * r);
-            g[k][j] = r * (w[k][j] * g[k][j] - x[k][j] * back);
+          for (int i = 0; i < 2 * VEC; ++i) {
+            dw[k][i] += g[k][i] * (x[k][i] * r);
+            g[k][i] = r * (w[k][i] * g[k][i] - x[k][i] * back);
           }
         }
-        *reinterpret_cast<Raw<VEC>*>(dst + ch[k].a * 2) = narrow<F16, VEC>(g[k]);
-        *reinterpret_cast<Raw<VEC>*>(dst + ch[k].b * 2) = narrow<F16, VEC>(g[k] + VEC);
+        *reinterpret_cast<Raw<VEC>*>(to + ch[k].a * 2) = narrow<F16, VEC>(g[k]);
+        *reinterpret_cast<Raw<VEC>*>(to + ch[k].b * 2) = narrow<F16, VEC>(g[k] + VEC);
       }
+      to += t.ys[1];
     }
   }
+  copy_wait<0>();
   if (!t.w) return;
+  // The block's sums, where the ring was.
+  __syncthreads();
+  float(*sums)[COLS] = reinterpret_cast<float(*)[COLS]>(ring);
 #pragma unroll
   for (int k = 0; k < ITER; ++k) {
     if (!ch[k].live) continue;
@@ -152,23 +228,25 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const RopeParams P) {
 }
 
 template <bool F16, int VEC, int LPR, int ITER>
-ffpa_status launch_bwd_as(RopeParams& P, bool inter, int sms, cudaStream_t stream) {
+ffpa_status launch_bwd_as(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t groups = RB_THREADS / LPR;
-  // Blocks in proportion to the rows, some two per SM in all.
-  const int64_t all = P.items[0] + P.items[1];
-  const int64_t most = sms * 2 < RB_BLOCKS_MAX - 2 ? sms * 2 : RB_BLOCKS_MAX - 2;
+  // As many blocks as are resident, in proportion to the rows.
+  const int64_t rows[2] = {P.items[0] * P.heads_per[0], P.items[1] * P.heads_per[1]};
+  int64_t most = (int64_t)sms * (ITER == 1 ? 2 : 1);
+  if (most > RB_BLOCKS_MAX) most = RB_BLOCKS_MAX;
+  int64_t share = (most * rows[0] + (rows[0] + rows[1]) / 2) / (rows[0] + rows[1]);
+  share = share < 1 ? 1 : share > most - 1 ? most - 1 : share;
   for (int i = 0; i < 2; ++i) {
-    int64_t n = (P.items[i] + groups - 1) / groups;
-    const int64_t share = (most * P.items[i] + all - 1) / all;
-    if (n > share) n = share;
-    P.blocks[i] = (int)(n < 1 ? 1 : n);
+    const int64_t n = (P.items[i] + groups - 1) / groups, cap = i == 0 ? share : most - share;
+    P.blocks[i] = (int)(n < cap ? n : cap);
   }
   P.part[1] = P.part[0] + (int64_t)P.blocks[0] * P.D;
   const int grid = P.blocks[0] + P.blocks[1];
-  if (inter)
-    rope_bwd_kernel<F16, VEC, LPR, ITER, true><<<grid, RB_THREADS, 0, stream>>>(P);
-  else
-    rope_bwd_kernel<F16, VEC, LPR, ITER, false><<<grid, RB_THREADS, 0, stream>>>(P);
+  const int smem = RB_DEPTH * rb_row_bytes<VEC, ITER>();
+  auto fn = inter ? &rope_bwd_kernel<F16, VEC, LPR, ITER, true> : &rope_bwd_kernel<F16, VEC, LPR, ITER, false>;
+  const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(fn), dev, smem);
+  if (st != FFPA_OK) return st;
+  fn<<<grid, RB_THREADS, smem, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
   if (P.dw[0] || P.dw[1]) {
     weight_sum_kernel<F16><<<dim3((P.D + 31) / 32, 2), 1024, 0, stream>>>(P);
@@ -178,28 +256,28 @@ ffpa_status launch_bwd_as(RopeParams& P, bool inter, int sms, cudaStream_t strea
 }
 
 template <bool F16>
-ffpa_status launch_bwd_rope(RopeParams& P, bool inter, int sms, cudaStream_t stream) {
+ffpa_status launch_bwd_rope(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t tokens = (int64_t)P.B * P.N;
   for (int i = 0; i < 2; ++i) {
     int per = 8;
     while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
-    P.heads_per[i] = per;
     P.chunks[i] = (P.t[i].H + per - 1) / per;
+    P.heads_per[i] = (P.t[i].H + P.chunks[i] - 1) / P.chunks[i];
     P.items[i] = tokens * P.chunks[i];
   }
   if (rope_vec(P.D, P.rot) == 8) {
     const int n = P.D / 16;
-    if (n <= 4) return launch_bwd_as<F16, 8, 4, 1>(P, inter, sms, stream);
-    if (n <= 8) return launch_bwd_as<F16, 8, 8, 1>(P, inter, sms, stream);
-    if (n <= 16) return launch_bwd_as<F16, 8, 16, 1>(P, inter, sms, stream);
-    if (n <= 32) return launch_bwd_as<F16, 8, 32, 1>(P, inter, sms, stream);
-    return launch_bwd_as<F16, 8, 32, 2>(P, inter, sms, stream);
+    if (n <= 4) return launch_bwd_as<F16, 8, 4, 1>(P, inter, sms, dev, stream);
+    if (n <= 8) return launch_bwd_as<F16, 8, 8, 1>(P, inter, sms, dev, stream);
+    if (n <= 16) return launch_bwd_as<F16, 8, 16, 1>(P, inter, sms, dev, stream);
+    if (n <= 32) return launch_bwd_as<F16, 8, 32, 1>(P, inter, sms, dev, stream);
+    return launch_bwd_as<F16, 8, 32, 2>(P, inter, sms, dev, stream);
   }
   const int n = P.D / 8;
-  if (n <= 16) return launch_bwd_as<F16, 4, 16, 1>(P, inter, sms, stream);
-  if (n <= 32) return launch_bwd_as<F16, 4, 32, 1>(P, inter, sms, stream);
-  if (n <= 64) return launch_bwd_as<F16, 4, 32, 2>(P, inter, sms, stream);
-  return launch_bwd_as<F16, 4, 32, 4>(P, inter, sms, stream);
+  if (n <= 16) return launch_bwd_as<F16, 4, 16, 1>(P, inter, sms, dev, stream);
+  if (n <= 32) return launch_bwd_as<F16, 4, 32, 1>(P, inter, sms, dev, stream);
+  if (n <= 64) return launch_bwd_as<F16, 4, 32, 2>(P, inter, sms, dev, stream);
+  return launch_bwd_as<F16, 4, 32, 4>(P, inter, sms, dev, stream);
 }
 
 }  // namespace
@@ -281,8 +359,8 @@ ffpa_status ffpa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const 
     }
   }
   P.part[0] = static_cast<float*>(workspace);
-  return dt == FFPA_FP16 ? launch_bwd_rope<true>(P, rope->interleaved != 0, sms, s)
-                         : launch_bwd_rope<false>(P, rope->interleaved != 0, sms, s);
+  return dt == FFPA_FP16 ? launch_bwd_rope<true>(P, rope->interleaved != 0, sms, dev, s)
+                         : launch_bwd_rope<false>(P, rope->interleaved != 0, sms, dev, s);
 }
 
 }  // extern "C"
