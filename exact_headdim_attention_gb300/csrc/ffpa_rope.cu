@@ -25,17 +25,17 @@ struct RopeItem {
   int64_t src_h;
   int which, wt, heads, h0, b, n;
 };
-__device__ __forceinline__ RopeItem rope_item(const RopeParams& P, int64_t item) {
+__device__ __forceinline__ RopeItem rope_item(const RopeParams& P, unsigned item) {
   RopeItem r;
   const bool in = item < P.items[0] + P.items[1] + P.items_v;
   r.which = item < P.items[0] ? 0 : item < P.items[0] + P.items[1] ? 1 : 2;
   r.wt = r.which == 0 ? 0 : 1;
-  const int64_t local = !in ? 0 : r.which == 0 ? item : r.which == 1 ? item - P.items[0] : item - P.items[0] - P.items[1];
-  const int64_t token = local / P.chunks[r.wt];
-  r.h0 = (int)(local - token * P.chunks[r.wt]) * P.heads_per[r.wt];
+  const unsigned local = !in ? 0 : r.which == 0 ? item : r.which == 1 ? item - P.items[0] : item - P.items[0] - P.items[1];
+  const unsigned token = local / P.chunks[r.wt];
+  r.h0 = (local - token * P.chunks[r.wt]) * P.heads_per[r.wt];
   r.heads = in ? min(P.t[r.wt].H - r.h0, P.heads_per[r.wt]) : 0;
-  r.b = (int)(token / P.N);
-  r.n = (int)(token - (int64_t)r.b * P.N);
+  r.b = P.B == 1 ? 0 : token / P.N;
+  r.n = token - r.b * P.N;
   if (r.which == 2) {
     r.src_h = P.vs[0];
     r.src = P.v + r.n * P.vs[1] + r.h0 * r.src_h;
@@ -57,30 +57,41 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
   constexpr int ROW = rope_row_bytes<VEC, ITER>(), PIECE = ROPE_THREADS * VEC * 2;
   extern __shared__ __align__(16) char ring[];     // [ROPE_DEPTH][ITER][2][thread] vectors
   __shared__ long long freq_s[512];
+  // The weights in fp32, behind the ring: queries', then keys'.
+  float* weight_s = reinterpret_cast<float*>(ring + ROPE_DEPTH * ROW);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (P.t[i].w)
+      for (int d = threadIdx.x; d < P.D; d += ROPE_THREADS) weight_s[i * P.D + d] = one_weight<F16>(P.t[i].w, P.w32, d);
   load_freqs(P, freq_s);
   const int lane = threadIdx.x % LPR;
-  const int64_t all = P.items[0] + P.items[1] + P.items_v;
-  const int64_t stride = (int64_t)gridDim.x * (ROPE_THREADS / LPR);
+  const unsigned all = P.items[0] + P.items[1] + P.items_v;
+  const unsigned stride = gridDim.x * (ROPE_THREADS / LPR);
   RopeChunk<VEC> ch[ITER];
 #pragma unroll
   for (int k = 0; k < ITER; ++k) ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
   const float inv_d = 1.0f / P.D;
   // Whole warps stay in the loop: the lanes of a row talk through shuffles.
   const int sub = threadIdx.x % 32 / LPR;
-  int64_t first = (int64_t)blockIdx.x * (ROPE_THREADS / LPR) + threadIdx.x / 32 * (32 / LPR);
-  const int per = P.heads_max;                     // steps of an item
+  unsigned first = blockIdx.x * (ROPE_THREADS / LPR) + threadIdx.x / 32 * (32 / LPR);
+  // Rows that the items first .. of a warp take (queries' and keys' items differ).
+  auto steps = [&](unsigned f) {
+    const int q = f < P.items[0] ? P.heads_per[0] : 0;
+    return f + (32 / LPR - 1) >= P.items[0] && P.heads_per[1] > q ? P.heads_per[1] : q;
+  };
   char* own = ring + threadIdx.x * (VEC * 2);
   const uint32_t own_at = smem_u32(own);
 
   // The copying runs ahead of the work by DEPTH - 1 steps, into later items too.
-  int64_t ahead = first;
-  int ahead_h = 0, ahead_heads = 0, ahead_slot = 0;
+  unsigned ahead = first;
+  int ahead_h = 0, ahead_heads = 0, ahead_slot = 0, ahead_steps = 0;
   const char* ahead_src = nullptr;
   int64_t ahead_stride = 0;
   auto issue = [&] {
     if (ahead < all) {
       if (ahead_h == 0) {
         const RopeItem it = rope_item(P, ahead + sub);
+        ahead_steps = steps(ahead);
         ahead_heads = it.heads;
         ahead_src = it.src;
         ahead_stride = it.src_h;
@@ -95,7 +106,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
           }
         ahead_src += ahead_stride;
       }
-      if (++ahead_h == per) {
+      if (++ahead_h == ahead_steps) {
         ahead_h = 0;
         ahead += stride;
       }
@@ -131,35 +142,43 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
       dst = t.y + it.b * t.ys[0] + it.n * t.ys[2];
     }
     dst += it.h0 * dst_h;
-    // Factors of a pair: (a, b) -> (a fa[i] - b fb[i], b ga[i] + a gb[i]); of
-    // columns that are not rotated: (a fa[i], b ga[i]).
-    float fa[ITER][VEC], fb[ITER][VEC], ga[ITER][VEC], gb[ITER][VEC];
+    // The factors of a value: itself times f0, its partner times f1 (not of
+    // columns that are not rotated).
+    float2 f0[ITER][VEC], f1[ITER][VEC];
     if (it.which < 2 && heads > 0) {
       const long long pos = P.rot ? position_of(P, it.b, it.n) : 0;
 #pragma unroll
       for (int k = 0; k < ITER; ++k) {
         if (!ch[k].live) continue;
-        float w[2 * VEC];
-        if (norm) {
-          load_weight<F16, VEC>(t.w, P.w32, ch[k].a, w);
-          load_weight<F16, VEC>(t.w, P.w32, ch[k].b, w + VEC);
-        }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float wa = norm ? w[pair_a<VEC, INTER>(i)] : 1.0f, wb = norm ? w[pair_b<VEC, INTER>(i)] : 1.0f;
-          fa[k][i] = wa;
-          ga[k][i] = wb;
-          if (ch[k].pair) {
-            float c, s;
-            turn(pos, freq_s[(lane + k * LPR) * VEC + i], P.rope_scale, c, s);
-            fa[k][i] = wa * c;
-            fb[k][i] = wb * s;
-            ga[k][i] = wb * c;
-            gb[k][i] = wa * s;
+        for (int i = 0; i < VEC; ++i) f0[k][i] = make_float2(1.0f, 1.0f);
+        if (norm) {
+          const float* w = weight_s + it.wt * P.D;
+#pragma unroll
+          for (int i = 0; i < VEC; i += 2) {
+            const float4 v = *reinterpret_cast<const float4*>(w + (i < VEC / 2 ? ch[k].a + 2 * i : ch[k].b + 2 * i - VEC));
+            f0[k][i] = make_float2(v.x, v.y);
+            f0[k][i + 1] = make_float2(v.z, v.w);
+          }
+        }
+        if (ch[k].pair) {
+          float c[VEC], s[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) turn(pos, freq_s[(lane + k * LPR) * VEC + i], P.rope_scale, c[i], s[i]);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) f1[k][i] = partner<VEC, INTER>(f0[k], i);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const int p0 = pair_of<VEC, INTER>(i, 0), p1 = pair_of<VEC, INTER>(i, 1);
+            f0[k][i].x *= c[p0];
+            f0[k][i].y *= c[p1];
+            f1[k][i].x *= second_of<VEC, INTER>(i, 0) ? s[p0] : -s[p0];
+            f1[k][i].y *= second_of<VEC, INTER>(i, 1) ? s[p1] : -s[p1];
           }
         }
       }
     }
+    const int per = steps(first);
 #pragma unroll 1
     for (int h = 0; h < per; ++h) {
       copy_wait<ROPE_DEPTH - 2>();
@@ -167,7 +186,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
       if (++ring_slot == ROPE_DEPTH) ring_slot = 0;
       const bool on = h < heads;
       Raw<VEC> ra[ITER], rb[ITER];
-      float sq = 0.0f;
+      float2 sq = make_float2(0.0f, 0.0f);
       if (on) {
 #pragma unroll
         for (int k = 0; k < ITER; ++k)
@@ -175,38 +194,36 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
             ra[k] = own_load<VEC>(row + 2 * k * PIECE);
             rb[k] = own_load<VEC>(row + (2 * k + 1) * PIECE);
             if (norm) {
-              float x[2 * VEC];
+              float2 x[VEC];
               widen<F16, VEC>(ra[k], x);
-              widen<F16, VEC>(rb[k], x + VEC);
+              widen<F16, VEC>(rb[k], x + VEC / 2);
 #pragma unroll
-              for (int i = 0; i < 2 * VEC; ++i) sq += x[i] * x[i];
+              for (int i = 0; i < VEC; ++i) sq = fma2(x[i], x[i], sq);
             }
           }
       }
       issue();
-      sq = row_sum<LPR>(sq);
+      const float sum = row_sum<LPR>(sq.x + sq.y);
       if (!on) continue;
-      const float r = norm ? rsqrtf(sq * inv_d + P.eps) : 1.0f;
+      const float r = norm ? rsqrtf(sum * inv_d + P.eps) : 1.0f;
+      const float2 r2 = make_float2(r, r);
 #pragma unroll
       for (int k = 0; k < ITER; ++k)
         if (ch[k].live) {
           if (it.which < 2) {
-            float x[2 * VEC], y[2 * VEC];
+            float2 x[VEC], y[VEC];
             widen<F16, VEC>(ra[k], x);
-            widen<F16, VEC>(rb[k], x + VEC);
+            widen<F16, VEC>(rb[k], x + VEC / 2);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              const int ia = pair_a<VEC, INTER>(i), ib = pair_b<VEC, INTER>(i);
-              float u = x[ia] * fa[k][i], v = x[ib] * ga[k][i];
-              if (ch[k].pair) {
-                u -= x[ib] * fb[k][i];
-                v += x[ia] * gb[k][i];
-              }
-              y[ia] = u * r;
-              y[ib] = v * r;
+            for (int i = 0; i < VEC; ++i) y[i] = mul2(x[i], f0[k][i]);
+            if (ch[k].pair) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) y[i] = fma2(partner<VEC, INTER>(x, i), f1[k][i], y[i]);
             }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) y[i] = mul2(y[i], r2);
             ra[k] = narrow<F16, VEC>(y);
-            rb[k] = narrow<F16, VEC>(y + VEC);
+            rb[k] = narrow<F16, VEC>(y + VEC / 2);
           }
           *reinterpret_cast<Raw<VEC>*>(dst + ch[k].a * 2) = ra[k];
           *reinterpret_cast<Raw<VEC>*>(dst + ch[k].b * 2) = rb[k];
@@ -226,7 +243,7 @@ ffpa_status launch_rope_as(const RopeParams& P, bool inter, int sms, int dev, cu
   // and no last wave is left over.
   const int64_t resident = (int64_t)sms * (ITER == 1 ? 3 : 2);
   if (grid > resident) grid = resident;
-  const int smem = ROPE_DEPTH * rope_row_bytes<VEC, ITER>();
+  const int smem = ROPE_DEPTH * rope_row_bytes<VEC, ITER>() + 2 * P.D * 4;
   auto fn = inter ? &rope_kernel<F16, VEC, LPR, ITER, true> : &rope_kernel<F16, VEC, LPR, ITER, false>;
   const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(fn), dev, smem);
   if (st != FFPA_OK) return st;
@@ -237,17 +254,16 @@ ffpa_status launch_rope_as(const RopeParams& P, bool inter, int sms, int dev, cu
 template <bool F16>
 ffpa_status launch_rope(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t tokens = (int64_t)P.B * P.N;
-  // Heads of an item: 8 share a token's sines, fewer where that would leave
+  // Heads of an item: up to 16 share a token's sines, fewer where that would leave
   // SMs without work.
   for (int i = 0; i < 2; ++i) {
-    int per = 8;
+    int per = 16;
     while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
     P.chunks[i] = (P.t[i].H + per - 1) / per;
     P.heads_per[i] = (P.t[i].H + P.chunks[i] - 1) / P.chunks[i];
-    P.items[i] = P.t[i].x ? tokens * P.chunks[i] : 0;
+    P.items[i] = P.t[i].x ? (unsigned)(tokens * P.chunks[i]) : 0;
   }
-  P.heads_max = P.items[0] && P.heads_per[0] > P.heads_per[1] ? P.heads_per[0] : P.heads_per[1];
-  P.items_v = P.slots ? tokens * P.chunks[1] : 0;
+  P.items_v = P.slots ? P.items[1] : 0;
   if (rope_vec(P.D, P.rot) == 8) {
     const int n = P.D / 16;
     if (n <= 4) return launch_rope_as<F16, 8, 4, 1>(P, inter, sms, dev, stream);
@@ -277,7 +293,7 @@ ffpa_status rope_params(const ffpa_rope* r, ffpa_dtype dt, int B, int Hq, int Hk
   if (!std::isfinite(r->eps) || r->eps < 0.0f || !std::isfinite(r->rope_scale)) return FFPA_ERR_INVALID;
   const size_t wa = r->weight_f32 ? 4 : 2;
   if (!on_boundary(r->q_weight, wa) || !on_boundary(r->k_weight, wa)) return FFPA_ERR_INVALID;
-  if ((int64_t)B * N > 0x7fffffffLL) return FFPA_ERR_INVALID;
+  if ((int64_t)B * N > 0x7fffffffLL / ((int64_t)Hq + 2 * (int64_t)Hkv)) return FFPA_ERR_INVALID;   // rows in 31 bits
   P->pos = static_cast<const char*>(r->positions);
   const int64_t pb = r->position_bits / 8;
   P->pos_s[0] = r->position_str[0] * pb;

@@ -36,8 +36,7 @@ struct RopeParams {
   int pos64, rot, w32, B, N, D;
   float eps, rope_scale;
   int heads_per[2];    // heads of one work item
-  int heads_max;       // the larger of the two
-  int64_t items[2];    // work items of queries and of keys
+  unsigned items[2];   // work items of queries and of keys
   int chunks[2];       // head chunks of a token
   // append (keys go to pages, values are copied): slots == NULL otherwise
   const int64_t* slots;
@@ -45,7 +44,7 @@ struct RopeParams {
   char *kc, *vc;
   const char* v;
   int64_t vs[2], kcs[3], vcs[3];   // byte strides (h, n); (page, slot, h)
-  int64_t items_v;
+  unsigned items_v;    // and of values
   int* err;
   // backward
   const char* g[2];    // gradients of the outputs
@@ -94,34 +93,28 @@ __device__ __forceinline__ Raw<VEC> own_load(const char* at) {
 }
 
 template <bool F16, int VEC>
-__device__ __forceinline__ void widen(const Raw<VEC>& r, float* x) {
+__device__ __forceinline__ void widen(const Raw<VEC>& r, float2* x) {
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) {
-    const float2 f = unpack2<F16>(r.u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+  for (int i = 0; i < VEC / 2; ++i) x[i] = unpack2<F16>(r.u[i]);
 }
 template <bool F16, int VEC>
-__device__ __forceinline__ Raw<VEC> narrow(const float* x) {
+__device__ __forceinline__ Raw<VEC> narrow(const float2* x) {
   Raw<VEC> r;
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) r.u[i] = pack2<F16>(x[2 * i], x[2 * i + 1]);
+  for (int i = 0; i < VEC / 2; ++i) r.u[i] = pack2<F16>(x[i].x, x[i].y);
   return r;
 }
 
+template <bool F16>
+__device__ __forceinline__ float one_weight(const void* w, int w32, int d) {
+  return w32 ? static_cast<const float*>(w)[d] : unpack2<F16>(static_cast<const uint16_t*>(w)[d]).x;
+}
+// VEC weights from column col on.
 template <bool F16, int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int w32, int col, float* x) {
-  if (w32) {
+__device__ __forceinline__ void load_weight(const void* w, int w32, int col, float2* x) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = static_cast<const float*>(w)[col + i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const uint16_t h = static_cast<const uint16_t*>(w)[col + i];
-      x[i] = unpack2<F16>(h).x;
-    }
-  }
+  for (int i = 0; i < VEC / 2; ++i)
+    x[i] = make_float2(one_weight<F16>(w, w32, col + 2 * i), one_weight<F16>(w, w32, col + 2 * i + 1));
 }
 
 // A frequency in turns per position, as a fraction of 2^64 (whole turns drop out).
@@ -148,11 +141,40 @@ __device__ __forceinline__ long long position_of(const RopeParams& P, int b, int
   return P.pos64 ? *reinterpret_cast<const long long*>(p) : *reinterpret_cast<const int*>(p);
 }
 
-// Values of pair i in a chunk's 2 VEC.
+// Two fp32 values in one instruction.
+__device__ __forceinline__ uint64_t pair2(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 both2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair2(a)), "l"(pair2(b)), "l"(pair2(c)));
+  return both2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair2(a)), "l"(pair2(b)));
+  return both2(r);
+}
+
+// A chunk in fp32 is VEC twos of neighbouring columns, those of the first
+// vector, then of the second.  The other halves of the pairs in two i: two
+// i +- VEC / 2, or the same two swapped when interleaved.
 template <int VEC, bool INTER>
-__device__ __forceinline__ constexpr int pair_a(int i) { return INTER ? 2 * i : i; }
+__device__ __forceinline__ float2 partner(const float2* x, int i) {
+  return INTER ? make_float2(x[i].y, x[i].x) : x[i < VEC / 2 ? i + VEC / 2 : i - VEC / 2];
+}
+// The pair that value j (0, 1) of two i belongs to, and whether as its b.
 template <int VEC, bool INTER>
-__device__ __forceinline__ constexpr int pair_b(int i) { return INTER ? 2 * i + 1 : VEC + i; }
+__device__ __forceinline__ constexpr int pair_of(int i, int j) { return INTER ? i : 2 * (i % (VEC / 2)) + j; }
+template <int VEC, bool INTER>
+__device__ __forceinline__ constexpr bool second_of(int i, int j) { return INTER ? j == 1 : i >= VEC / 2; }
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {

@@ -42,38 +42,38 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
   const RopeTensor& t = P.t[wt];
   const float inv_d = 1.0f / P.D;
   RopeChunk<VEC> ch[ITER];
-  float w[ITER][2 * VEC], dw[ITER][2 * VEC];
+  float2 w[ITER][VEC], dw[ITER][VEC];
 #pragma unroll
   for (int k = 0; k < ITER; ++k) {
     ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
 #pragma unroll
-    for (int i = 0; i < 2 * VEC; ++i) dw[k][i] = 0.0f;
+    for (int i = 0; i < VEC; ++i) dw[k][i] = make_float2(0.0f, 0.0f);
     if (ch[k].live && t.w) {
       load_weight<F16, VEC>(t.w, P.w32, ch[k].a, w[k]);
-      load_weight<F16, VEC>(t.w, P.w32, ch[k].b, w[k] + VEC);
+      load_weight<F16, VEC>(t.w, P.w32, ch[k].b, w[k] + VEC / 2);
     }
   }
-  const int64_t stride = (int64_t)P.blocks[wt] * GROUPS, all = P.items[wt];
+  const unsigned stride = P.blocks[wt] * GROUPS, all = P.items[wt];
   const int per = P.heads_per[wt];
   // First head, token and number of heads of an item.
   struct Item {
     int h0, heads, b, n;
   };
-  auto item_of = [&](int64_t item) {
+  auto item_of = [&](unsigned item) {
     Item r;
     const bool in = item < all;
-    const int64_t token = in ? item / P.chunks[wt] : 0;
-    r.h0 = in ? (int)(item - token * P.chunks[wt]) * per : 0;
+    const unsigned token = in ? item / P.chunks[wt] : 0;
+    r.h0 = in ? (item - token * P.chunks[wt]) * per : 0;
     r.heads = in ? min(t.H - r.h0, per) : 0;
-    r.b = (int)(token / P.N);
-    r.n = (int)(token - (int64_t)r.b * P.N);
+    r.b = P.B == 1 ? 0 : token / P.N;
+    r.n = token - r.b * P.N;
     return r;
   };
   // Whole warps stay in the loop: the lanes of a row talk through shuffles.
-  int64_t first = (int64_t)block * GROUPS + threadIdx.x / 32 * (32 / LPR);
+  unsigned first = block * GROUPS + threadIdx.x / 32 * (32 / LPR);
   char* own = ring + threadIdx.x * (VEC * 2);
   const uint32_t own_at = smem_u32(own);
-  int64_t ahead = first;
+  unsigned ahead = first;
   int ahead_h = 0, ahead_heads = 0, ahead_slot = 0;
   const char *ahead_g = nullptr, *ahead_x = nullptr;
   auto issue = [&] {
@@ -128,30 +128,35 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
       const char* from = own + ring_slot * ROW;
       if (++ring_slot == RB_DEPTH) ring_slot = 0;
       const bool on = h < it.heads;
-      float g[ITER][2 * VEC], x[ITER][2 * VEC];
+      float2 g[ITER][VEC], x[ITER][VEC];
       float sq = 0.0f, dot = 0.0f;
       if (on) {
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
           if (!ch[k].live) continue;
           widen<F16, VEC>(own_load<VEC>(from + 4 * k * PIECE), g[k]);
-          widen<F16, VEC>(own_load<VEC>(from + (4 * k + 1) * PIECE), g[k] + VEC);
+          widen<F16, VEC>(own_load<VEC>(from + (4 * k + 1) * PIECE), g[k] + VEC / 2);
           if (ch[k].pair) {
+            float2 y[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-              const int ia = pair_a<VEC, INTER>(i), ib = pair_b<VEC, INTER>(i);
-              const float u = g[k][ia], v = g[k][ib];
-              g[k][ia] = u * cs[k][i] + v * sn[k][i];
-              g[k][ib] = v * cs[k][i] - u * sn[k][i];
+              const int p0 = pair_of<VEC, INTER>(i, 0), p1 = pair_of<VEC, INTER>(i, 1);
+              const float2 z = partner<VEC, INTER>(g[k], i);
+              y[i].x = g[k][i].x * cs[k][p0] + (second_of<VEC, INTER>(i, 0) ? -z.x : z.x) * sn[k][p0];
+              y[i].y = g[k][i].y * cs[k][p1] + (second_of<VEC, INTER>(i, 1) ? -z.y : z.y) * sn[k][p1];
             }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) g[k][i] = y[i];
           }
           if (t.w) {
             widen<F16, VEC>(own_load<VEC>(from + (4 * k + 2) * PIECE), x[k]);
-            widen<F16, VEC>(own_load<VEC>(from + (4 * k + 3) * PIECE), x[k] + VEC);
+            widen<F16, VEC>(own_load<VEC>(from + (4 * k + 3) * PIECE), x[k] + VEC / 2);
 #pragma unroll
-            for (int i = 0; i < 2 * VEC; ++i) {
-              sq += x[k][i] * x[k][i];
-              dot += w[k][i] * g[k][i] * x[k][i];
+            for (int i = 0; i < VEC; ++i) {
+              sq += x[k][i].x * x[k][i].x;
+              sq += x[k][i].y * x[k][i].y;
+              dot += w[k][i].x * g[k][i].x * x[k][i].x;
+              dot += w[k][i].y * g[k][i].y * x[k][i].y;
             }
           }
         }
@@ -169,13 +174,15 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
         if (!ch[k].live) continue;
         if (t.w) {
 #pragma unroll
-          for (int i = 0; i < 2 * VEC; ++i) {
-            dw[k][i] += g[k][i] * (x[k][i] * r);
-            g[k][i] = r * (w[k][i] * g[k][i] - x[k][i] * back);
+          for (int i = 0; i < VEC; ++i) {
+            dw[k][i].x += g[k][i].x * (x[k][i].x * r);
+            dw[k][i].y += g[k][i].y * (x[k][i].y * r);
+            g[k][i].x = r * (w[k][i].x * g[k][i].x - x[k][i].x * back);
+            g[k][i].y = r * (w[k][i].y * g[k][i].y - x[k][i].y * back);
           }
         }
         *reinterpret_cast<Raw<VEC>*>(to + ch[k].a * 2) = narrow<F16, VEC>(g[k]);
-        *reinterpret_cast<Raw<VEC>*>(to + ch[k].b * 2) = narrow<F16, VEC>(g[k] + VEC);
+        *reinterpret_cast<Raw<VEC>*>(to + ch[k].b * 2) = narrow<F16, VEC>(g[k] + VEC / 2);
       }
       to += t.ys[1];
     }
@@ -189,9 +196,9 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
   for (int k = 0; k < ITER; ++k) {
     if (!ch[k].live) continue;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      sums[row][ch[k].a + i] = dw[k][i];
-      sums[row][ch[k].b + i] = dw[k][VEC + i];
+    for (int i = 0; i < VEC / 2; ++i) {
+      *reinterpret_cast<float2*>(&sums[row][ch[k].a + 2 * i]) = dw[k][i];
+      *reinterpret_cast<float2*>(&sums[row][ch[k].b + 2 * i]) = dw[k][VEC / 2 + i];
     }
   }
   __syncthreads();
@@ -231,7 +238,7 @@ template <bool F16, int VEC, int LPR, int ITER>
 ffpa_status launch_bwd_as(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t groups = RB_THREADS / LPR;
   // As many blocks as are resident, in proportion to the rows.
-  const int64_t rows[2] = {P.items[0] * P.heads_per[0], P.items[1] * P.heads_per[1]};
+  const int64_t rows[2] = {(int64_t)P.items[0] * P.heads_per[0], (int64_t)P.items[1] * P.heads_per[1]};
   int64_t most = (int64_t)sms * (ITER == 1 ? 2 : 1);
   if (most > RB_BLOCKS_MAX) most = RB_BLOCKS_MAX;
   int64_t share = (most * rows[0] + (rows[0] + rows[1]) / 2) / (rows[0] + rows[1]);
@@ -259,11 +266,11 @@ template <bool F16>
 ffpa_status launch_bwd_rope(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t tokens = (int64_t)P.B * P.N;
   for (int i = 0; i < 2; ++i) {
-    int per = 8;
+    int per = 16;
     while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
     P.chunks[i] = (P.t[i].H + per - 1) / per;
     P.heads_per[i] = (P.t[i].H + P.chunks[i] - 1) / P.chunks[i];
-    P.items[i] = tokens * P.chunks[i];
+    P.items[i] = (unsigned)(tokens * P.chunks[i]);
   }
   if (rope_vec(P.D, P.rot) == 8) {
     const int n = P.D / 16;
