@@ -17,7 +17,7 @@ namespace ffpa {
 namespace {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_DEPTH = 6;
+constexpr int ROPE_DEPTH = 4;
 
 // Where the rows of a work item are: queries, keys or (append) values.
 struct RopeItem {
@@ -52,8 +52,16 @@ __host__ __device__ constexpr int rope_row_bytes() {   // of one row, for all th
   return ROPE_THREADS * ITER * 2 * VEC * 2;
 }
 
+// Resident blocks an SM.  Two keep the 8-wide vectors' factors and the next
+// item's addresses in registers (append of 16384 tokens at D = 256: 78 us, with
+// three 91); the 4-wide vectors fit three (T16384 D120: 62 us, with two 74).
+template <int VEC, int ITER>
+__host__ __device__ constexpr int rope_blocks() {
+  return VEC == 4 && ITER == 1 ? 3 : 2;
+}
+
 template <bool F16, int VEC, int LPR, int ITER, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_kernel(const __grid_constant__ RopeParams P) {
   constexpr int ROW = rope_row_bytes<VEC, ITER>(), PIECE = ROPE_THREADS * VEC * 2;
   extern __shared__ __align__(16) char ring[];     // [ROPE_DEPTH][ITER][2][thread] vectors
   __shared__ long long freq_s[512];
@@ -69,7 +77,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
   const unsigned stride = gridDim.x * (ROPE_THREADS / LPR);
   RopeChunk<VEC> ch[ITER];
 #pragma unroll
-  for (int k = 0; k < ITER; ++k) ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
+  for (int k = 0; k < ITER; ++k) ch[k] = rope_chunk<VEC>(lane + k * LPR, P.D, P.rot);
   const float inv_d = 1.0f / P.D;
   // Whole warps stay in the loop: the lanes of a row talk through shuffles.
   const int sub = threadIdx.x % 32 / LPR;
@@ -118,8 +126,20 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
   for (int i = 0; i < ROPE_DEPTH - 1; ++i) issue();
 
   int ring_slot = 0;
+  // The position and slot of an item are asked for while the one before it is worked on.
+  RopeItem next;
+  int64_t next_pos = 0, next_slot = -1;
+  auto ask = [&](unsigned item) {
+    next = rope_item(P, item);
+    if (P.rot && next.which < 2) next_pos = position_of(P, next.b, next.n);
+    if (P.slots && next.which > 0 && next.heads > 0) next_slot = P.slots[next.n];
+  };
+  if (first < all) ask(first + sub);
   for (; first < all; first += stride) {
-    const RopeItem it = rope_item(P, first + sub);
+    const RopeItem it = next;
+    const int64_t pos = next_pos;
+    int64_t slot = next_slot;
+    if (first + stride < all) ask(first + stride + sub);
     const RopeTensor& t = P.t[it.wt];
     const bool norm = it.which < 2 && t.w;
     int heads = it.heads;
@@ -127,7 +147,6 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
     int64_t dst_h;
     if (it.which > 0 && P.slots) {
       // The slot of a cached row; a negative one is padding and is not stored.
-      int64_t slot = heads > 0 ? P.slots[it.n] : -1;
       if (slot >= P.n_slots) {
         report_invalid(P.err);
         slot = -1;
@@ -146,7 +165,6 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
     // columns that are not rotated).
     float2 f0[ITER][VEC], f1[ITER][VEC];
     if (it.which < 2 && heads > 0) {
-      const long long pos = P.rot ? position_of(P, it.b, it.n) : 0;
 #pragma unroll
       for (int k = 0; k < ITER; ++k) {
         if (!ch[k].live) continue;
@@ -164,7 +182,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ITER == 1 ? 3 : 2) rope_kernel(c
         if (ch[k].pair) {
           float c[VEC], s[VEC];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) turn(pos, freq_s[(lane + k * LPR) * VEC + i], P.rope_scale, c[i], s[i]);
+          for (int i = 0; i < VEC; ++i) turn(pos, freq_s[pair_number<VEC, INTER>(ch[k], i)], P.rope_scale, c[i], s[i]);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) f1[k][i] = partner<VEC, INTER>(f0[k], i);
 #pragma unroll
@@ -241,7 +259,7 @@ ffpa_status launch_rope_as(const RopeParams& P, bool inter, int sms, int dev, cu
   int64_t grid = (all + per - 1) / per;
   // As many blocks as are resident, so that the frequencies are formed once
   // and no last wave is left over.
-  const int64_t resident = (int64_t)sms * (ITER == 1 ? 3 : 2);
+  const int64_t resident = (int64_t)sms * rope_blocks<VEC, ITER>();
   if (grid > resident) grid = resident;
   const int smem = ROPE_DEPTH * rope_row_bytes<VEC, ITER>() + 2 * P.D * 4;
   auto fn = inter ? &rope_kernel<F16, VEC, LPR, ITER, true> : &rope_kernel<F16, VEC, LPR, ITER, false>;
@@ -254,10 +272,10 @@ ffpa_status launch_rope_as(const RopeParams& P, bool inter, int sms, int dev, cu
 template <bool F16>
 ffpa_status launch_rope(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t tokens = (int64_t)P.B * P.N;
-  // Heads of an item: up to 16 share a token's sines, fewer where that would leave
+  // Heads of an item: up to 8 share a token's sines, fewer where that would leave
   // SMs without work.
   for (int i = 0; i < 2; ++i) {
-    int per = 16;
+    int per = 8;
     while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
     P.chunks[i] = (P.t[i].H + per - 1) / per;
     P.heads_per[i] = (P.t[i].H + P.chunks[i] - 1) / P.chunks[i];

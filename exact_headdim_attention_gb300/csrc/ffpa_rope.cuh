@@ -8,9 +8,8 @@
 //   pairs (i, rot/2 + i), or (2i, 2i+1) when interleaved; later columns stay.
 //
 // A row (one head of one token) belongs to LPR lanes.  A lane holds ITER
-// chunks of 2 VEC values: the two VEC-wide vectors that hold VEC whole pairs,
-// so that a rotation never leaves its lane, or 2 VEC columns behind the
-// rotated ones.
+// chunks of 2 VEC values: two VEC-wide vectors that hold VEC whole pairs, so
+// that a rotation never leaves its lane, or two behind the rotated columns.
 //
 // Angles are taken in turns, as 64-bit fixed-point fractions: position times
 // frequency wraps there as the angle does, so that far positions need neither
@@ -64,20 +63,24 @@ struct RopeChunk {
   bool live;
 };
 
-template <int VEC, bool INTER>
+// Chunk j of a row: a vector of the first half of the rotated columns and the
+// one as far into their second half, then so for the columns behind them: the
+// lanes of a row read neighbouring vectors.  A vector holds whole pairs when
+// they are interleaved; else the two vectors hold each other's.
+template <int VEC>
 __device__ __forceinline__ RopeChunk<VEC> rope_chunk(int j, int D, int rot) {
   RopeChunk<VEC> c;
   const int np = rot / (2 * VEC);
   c.live = j < D / (2 * VEC);
   c.pair = j < np;
-  if (c.pair) {
-    c.a = INTER ? 2 * j * VEC : j * VEC;
-    c.b = INTER ? c.a + VEC : rot / 2 + j * VEC;
-  } else {
-    c.a = rot + (j - np) * 2 * VEC;
-    c.b = c.a + VEC;
-  }
+  c.a = c.pair ? j * VEC : rot + (j - np) * VEC;
+  c.b = c.a + (c.pair ? rot : D - rot) / 2;
   return c;
+}
+// Number (of a frequency) of pair i of a chunk.
+template <int VEC, bool INTER>
+__device__ __forceinline__ int pair_number(const RopeChunk<VEC>& c, int i) {
+  return !INTER ? c.a + i : i < VEC / 2 ? c.a / 2 + i : c.b / 2 + i - VEC / 2;
 }
 
 template <int VEC>

@@ -20,7 +20,7 @@ namespace ffpa {
 namespace {
 
 constexpr int RB_THREADS = 256;
-constexpr int RB_DEPTH = 4;
+constexpr int RB_DEPTH = 3;
 constexpr int RB_BLOCKS_MAX = 512;   // blocks of queries and keys together
 
 template <int VEC, int ITER>
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
   float2 w[ITER][VEC], dw[ITER][VEC];
 #pragma unroll
   for (int k = 0; k < ITER; ++k) {
-    ch[k] = rope_chunk<VEC, INTER>(lane + k * LPR, P.D, P.rot);
+    ch[k] = rope_chunk<VEC>(lane + k * LPR, P.D, P.rot);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) dw[k][i] = make_float2(0.0f, 0.0f);
     if (ch[k].live && t.w) {
@@ -113,14 +113,14 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
   int ring_slot = 0;
   for (; first < all; first += stride) {
     const Item it = item_of(first + sub);
+    const long long pos = P.rot ? position_of(P, it.b, it.n) : 0;
     char* to = t.y + it.b * t.ys[0] + it.h0 * t.ys[1] + it.n * t.ys[2];
     float cs[ITER][VEC], sn[ITER][VEC];
-    const long long pos = P.rot ? position_of(P, it.b, it.n) : 0;
 #pragma unroll
     for (int k = 0; k < ITER; ++k) {
       if (!ch[k].live || !ch[k].pair) continue;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) turn(pos, freq_s[(lane + k * LPR) * VEC + i], P.rope_scale, cs[k][i], sn[k][i]);
+      for (int i = 0; i < VEC; ++i) turn(pos, freq_s[pair_number<VEC, INTER>(ch[k], i)], P.rope_scale, cs[k][i], sn[k][i]);
     }
 #pragma unroll 1
     for (int h = 0; h < per; ++h) {
