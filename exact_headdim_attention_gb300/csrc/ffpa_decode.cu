@@ -327,6 +327,10 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
       if (lane >= d) incl += x;
     }
     if (lane == 31) scan_s[warp] = incl;
+    if (P.boxed && tid == 32) {
+      prefetch_tmap(&P.map_k);
+      prefetch_tmap(&P.map_v);
+    }
     if (tid == 0) {
       abort_flag = 0;
       const int arrivals = P.boxed ? 1 : 64;

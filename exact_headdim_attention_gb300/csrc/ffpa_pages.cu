@@ -16,7 +16,7 @@ namespace ffpa {
 namespace {
 
 constexpr int PLAN_WARPS = 8;
-constexpr int PLAN_STRETCH = 2048;   // tokens of a request that one warp writes
+constexpr int PLAN_STRETCH = 512;    // tokens of a request that one warp writes
 
 struct PlanParams {
   int32_t* table;
@@ -29,22 +29,22 @@ struct PlanParams {
 };
 
 struct Grow {
-  int old, add, before, need;   // tokens held and added, pages held and needed
+  unsigned old, add, before, need;   // tokens held and added, pages held and needed
   bool bad;
 };
 
+// (32-bit arithmetic: max_pages * page_size is at most 0x7fff0000.)
 __device__ __forceinline__ Grow grow(const PlanParams& P, int b) {
   Grow g;
   const int o = P.seq_lens[b], a = P.new_lens[b];
-  const long long cap = (long long)P.max_pages * P.page_size;
-  g.old = o < 0 ? 0 : o > cap ? (int)cap : o;
-  const int add = a < 0 ? 0 : a;
+  const unsigned cap = (unsigned)P.max_pages * P.page_size, page = P.page_size;
+  g.old = o < 0 ? 0 : min((unsigned)o, cap);
+  g.add = a < 0 ? 0 : a;
   // Tokens past the end of the request's row of the table get no page.
-  const int fit = (int)(cap - g.old < add ? cap - g.old : add);
-  g.add = add;
-  g.before = (g.old + P.page_size - 1) / P.page_size;
-  g.need = (int)(((long long)g.old + fit + P.page_size - 1) / P.page_size) - g.before;
-  g.bad = o != g.old || a < 0 || fit != add;
+  const unsigned fit = min(cap - g.old, g.add);
+  g.before = (g.old + page - 1) / page;
+  g.need = (g.old + fit + page - 1) / page - g.before;
+  g.bad = o != (int)g.old || a < 0 || fit != g.add;
   return g;
 }
 
@@ -52,7 +52,13 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32) plan_kernel(const PlanParams 
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int first = blockIdx.x * PLAN_WARPS;
   __shared__ long long sums[PLAN_WARPS][4];
-  __shared__ int4 mine[PLAN_WARPS];
+  __shared__ uint4 mine[PLAN_WARPS];
+  // Later stretches exist for long prompts only.
+  if (blockIdx.y > 0) {
+    const int b = first + lane;
+    const int add = lane < PLAN_WARPS && b < P.B ? P.new_lens[b] : 0;
+    if (!__any_sync(~0u, add > (int)blockIdx.y * PLAN_STRETCH)) return;
+  }
   // Tokens and pages before this block's requests, and of all of them.
   long long before_t = 0, before_p = 0, all_t = 0, all_p = 0;
   bool bad = false;
@@ -65,7 +71,7 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32) plan_kernel(const PlanParams 
       before_t += g.add;
       before_p += g.need;
     } else if (b < first + PLAN_WARPS) {
-      mine[b - first] = make_int4(g.old, g.add, g.before, g.need);
+      mine[b - first] = make_uint4(g.old, g.add, g.before, g.need);
     }
   }
 #pragma unroll
@@ -98,48 +104,46 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32) plan_kernel(const PlanParams 
     P.cu_seqlens[P.B] = (int)(all_t < P.tokens ? all_t : P.tokens);
   }
   // Entries behind the last token belong to none.
-  const long long threads = (long long)gridDim.x * gridDim.y * blockDim.x;
-  const long long me = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + tid;
-  for (long long t = all_t + me; t < P.tokens; t += threads) {
-    P.slots[t] = -1;
-    P.positions[t] = 0;
-  }
+  if (blockIdx.y == 0)
+    for (long long t = all_t + (long long)blockIdx.x * blockDim.x + tid; t < P.tokens; t += (long long)gridDim.x * blockDim.x) {
+      P.slots[t] = -1;
+      P.positions[t] = 0;
+    }
   const int b = first + warp;
   if (b >= P.B) return;
   for (int w = 0; w < warp; ++w) {
     before_t += mine[w].y;
     before_p += mine[w].w;
   }
-  const int old = mine[warp].x, add = mine[warp].y, held = mine[warp].z, need = mine[warp].w;
+  const unsigned old = mine[warp].x, add = mine[warp].y, held = mine[warp].z, need = mine[warp].w;
+  const unsigned page_size = P.page_size;
   // Pages of this request that the free list still has.
   const long long left = count - before_p;
-  const int got = left <= 0 ? 0 : left < need ? (int)left : need;
-  // New page i: the free list's entry, or -1 when the list has run out or
-  // holds something that is no page (a page number is never negative).
-  auto fresh = [&](int i) { return i < got ? P.free_pages[count - 1 - (before_p + i)] : -1; };
+  const unsigned got = left <= 0 ? 0 : left < need ? (unsigned)left : need;
   int32_t* table = P.table + b * P.table_str;
-  const long long room = (long long)(held + got) * P.page_size;     // tokens that have a page
-  const long long end = (long long)old + add < room ? (long long)old + add : room;
+  const unsigned room = min((unsigned long long)(held + got) * page_size, ~0ull >> 32);   // tokens that have a page
   if (blockIdx.y == 0 && lane == 0) {
     P.cu_seqlens[b] = (int)(before_t < P.tokens ? before_t : P.tokens);
-    P.lens_out[b] = (int)(end > old ? end : old);
+    P.lens_out[b] = (int)max(old, min(old + add, room));
   }
   // This warp's stretch of the request's new tokens, and the pages that begin in it.
-  for (long long from = (long long)blockIdx.y * PLAN_STRETCH; from < add; from += (long long)gridDim.y * PLAN_STRETCH) {
-    const long long to = from + PLAN_STRETCH < add ? from + PLAN_STRETCH : add;
-    for (long long i = from + lane; i < to; i += 32) {
-      const long long pos = (long long)old + i, at = before_t + i;
-      const long long j = pos / P.page_size;
-      const int in = (int)(pos - j * P.page_size);
+  const unsigned step = gridDim.y * PLAN_STRETCH;
+  for (unsigned from = blockIdx.y * PLAN_STRETCH; from < add; from += step) {
+    const unsigned to = min(from + PLAN_STRETCH, add);
+    for (unsigned i = from + lane; i < to; i += 32) {
+      const unsigned pos = old + i, j = pos / page_size, in = pos - j * page_size;
+      const long long at = before_t + i;
+      // New page: the free list's entry, or -1 when the list has run out or
+      // holds something that is no page (a page number is never negative).
       int page = -1;
       if (j < held)
         page = table[j];
       else if (j < held + need) {
-        page = fresh((int)(j - held));
+        if (j - held < got) page = P.free_pages[count - 1 - (before_p + (j - held))];
         if (in == 0) table[j] = page;
       }
       if (at < P.tokens) {
-        P.slots[at] = page < 0 ? -1 : (long long)page * P.page_size + in;
+        P.slots[at] = page < 0 ? -1 : (long long)page * page_size + in;
         P.positions[at] = (int)pos;
       }
     }
@@ -197,8 +201,8 @@ extern "C" ffpa_status ffpa_page_plan(int32_t* block_table, int64_t table_str, i
   P.n_free = n_free;
   P.tokens = tokens;
   const int gx = (B + PLAN_WARPS - 1) / PLAN_WARPS;
-  int gy = (tokens + PLAN_STRETCH - 1) / PLAN_STRETCH;   // a request may have all the tokens
-  const int most = gx < 1024 ? 1024 / gx : 1;
+  int gy = (tokens - 1) / PLAN_STRETCH + 1;              // a request may have all the tokens
+  const int most = gx < 2048 ? 2048 / gx : 1;
   gy = gy < 1 ? 1 : gy > most ? most : gy;
   plan_kernel<<<dim3(gx, gy), PLAN_WARPS * 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;

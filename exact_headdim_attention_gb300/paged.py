@@ -14,14 +14,13 @@ ABI (include/ffpa.h), which also checks what this module does not.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 
 from ._binding import (FFPA_OK, Rope, _check_buffer, _dtype_code, _options, _raise, _stream_handle,
                        load_library)
-
-_I64x2, _I64x3, _I64x4 = ctypes.c_int64 * 2, ctypes.c_int64 * 3, ctypes.c_int64 * 4
 
 
 def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -73,58 +72,89 @@ def _rope_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, 
     if inv_freq is not None:
         if inv_freq.dtype != torch.float64:
             raise TypeError(f"inv_freq must be float64, got {inv_freq.dtype}")
-        if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 0 < 2 * inv_freq.numel() <= D:
+        if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 0 < 2 * len(inv_freq) <= D:
             raise ValueError(f"inv_freq must be contiguous [rot_dim / 2] with rot_dim in 8..{D}")
         if positions is None:
             raise ValueError("a rotation needs positions")
         if positions.dtype not in (torch.int32, torch.int64):
             raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-        shape = tuple(positions.shape)
+        shape = positions.shape
         if shape == (N,):
             r.position_str[1] = positions.stride(0)
-        elif shape in ((B, N), (1, N)):
+        elif shape == (B, N) or shape == (1, N):
             r.position_str[0] = positions.stride(0) if shape[0] == B else 0
             r.position_str[1] = positions.stride(1)
         else:
+            shape = tuple(shape)
             raise ValueError(f"positions must have shape {(N,)} or {(B, N)}, got {shape}")
-        if positions.device != k.device or inv_freq.device != k.device:
-            raise ValueError("positions and inv_freq must be on the keys' device")
         r.positions, r.position_bits = positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32
         r.inv_freq, r.rot_dim = inv_freq.data_ptr(), 2 * inv_freq.numel()
-    w32 = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if w.dtype not in (torch.float32, k.dtype):
-            raise TypeError(f"{name} must be float32 or {k.dtype}, got {w.dtype}")
-        if tuple(w.shape) != (D,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [{D}], got {tuple(w.shape)}")
-        if w.device != k.device:
-            raise ValueError(f"{name} must be on the keys' device")
-        if w32 not in (None, w.dtype == torch.float32):
+    if q_weight is not None:
+        r.q_weight, r.weight_f32 = _weight_pointer(q_weight, "q_weight", k, D)
+    if k_weight is not None:
+        if q_weight is not None and q_weight.dtype != k_weight.dtype:
             raise TypeError("q_weight and k_weight must share one dtype")
-        w32 = w.dtype == torch.float32
-        setattr(r, name, w.data_ptr())
-    r.weight_f32 = int(bool(w32))
-    r.interleaved, r.rope_scale, r.eps = int(bool(interleaved)), float(rope_scale), float(eps)
+        r.k_weight, r.weight_f32 = _weight_pointer(k_weight, "k_weight", k, D)
+    r.interleaved, r.rope_scale, r.eps = bool(interleaved), rope_scale, eps
     return r
 
 
-def _rows4(t):
+def _weight_pointer(w, name, k, D):
+    f32 = w.dtype == torch.float32
+    if not f32 and w.dtype != k.dtype:
+        raise TypeError(f"{name} must be float32 or {k.dtype}, got {w.dtype}")
+    if w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{D}], got {tuple(w.shape)}")
+    return w.data_ptr(), f32
+
+
+def _strides(*tensors):
+    """Strides of the tensors, one after the other, in one int64 array that the caller keeps alive
+    over the call, and the address of each tensor's.  None has no strides."""
+    flat, at = [], []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        at.append(8 * len(flat))
+        flat += t.stride()
+    keep = (ctypes.c_int64 * len(flat))(*flat)
+    base = ctypes.addressof(keep)
+    return keep, [None if x is None else base + x for x in at]
+
+
+def _bhnd(t):
     """Strides of [B, H, N, D] or packed [T, H, D] rows as (b, h, n, d)."""
     s = t.stride()
-    return _I64x4(*s) if len(s) == 4 else _I64x4(0, s[1], s[0], s[2])
+    return s if len(s) == 4 else (0, s[1], s[0], s[2])
+
+
+def _strides4(*tensors):
+    """As _strides, for [B, H, N, D] or packed [T, H, D] rows as (b, h, n, d)."""
+    flat = []
+    for t in tensors:
+        flat += _bhnd(t)
+    keep = (ctypes.c_int64 * len(flat))(*flat)
+    base = ctypes.addressof(keep)
+    return keep, range(base, base + 32 * len(tensors), 32)
+
+
+def _stream_of(stream, t):
+    """As _stream_handle, with a short way to torch's current stream of t's device."""
+    if stream is None and t.is_cuda:
+        return torch._C._cuda_getCurrentRawStream(t.device.index) or None
+    return _stream_handle(stream, t)
 
 
 def _qk_shape(q, k):
-    """(B, Hq, Hkv, N, D) of [B, H, N, D] or packed [T, H, D] queries and keys."""
-    if q.dim() != k.dim() or q.dim() not in (3, 4):
+    """(B, Hq, Hkv, N, D) of [B, H, N, D] or packed [T, H, D] queries and keys.  (That every tensor of
+    a call is memory of one device is the C ABI's check, here and below.)"""
+    rank = q.dim()
+    if rank != k.dim() or rank not in (3, 4):
         raise ValueError("q and k must both be 4-D [B, H, N, D] or 3-D [T, H, D]")
     if q.dtype != k.dtype:
         raise TypeError("q and k must share one dtype")
-    if q.device != k.device:
-        raise ValueError("q and k must be on one device")
-    if q.dim() == 4:
+    if rank == 4:
         (B, Hq, N, D), (Bk, Hkv, Nk, Dk) = q.shape, k.shape
     else:
         (N, Hq, D), (Nk, Hkv, Dk) = q.shape, k.shape
@@ -154,9 +184,10 @@ def ffpa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions=None, inv_freq
     B, Hq, Hkv, N, D = _qk_shape(q, k)
     r = _rope_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, B, N)
     q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
+    keep, (qs, ks, qos, kos) = _strides4(q, k, q_out, k_out)
     st = load_library().ffpa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                                          _dtype_code(q), B, Hq, Hkv, N, D, _rows4(q), _rows4(k), _rows4(q_out),
-                                          _rows4(k_out), r, _stream_handle(stream, q))
+                                          _dtype_code(q), B, Hq, Hkv, N, D, qs, ks, qos, kos, r,
+                                          _stream_of(stream, q))
     if st != FFPA_OK:
         _raise(st, "ffpa_qk_norm_rope")
     return q_out, k_out
@@ -185,18 +216,19 @@ def ffpa_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     lib = load_library()
     ws = None
     if q_weight is not None or k_weight is not None:
-        ws = _workspace(workspace, int(lib.ffpa_qk_norm_rope_bwd_workspace_bytes(D)), q.device, stream)
+        ws = _workspace(workspace, qk_norm_rope_bwd_workspace_bytes(D), q.device, stream)
+    keep, (gqs, gks, qs, ks, dqs, dks) = _strides4(dq_out, dk_out, q, k, dq, dk)
     st = lib.ffpa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
                                    dk.data_ptr(), None if dqw is None else dqw.data_ptr(),
                                    None if dkw is None else dkw.data_ptr(), _dtype_code(q), B, Hq, Hkv, N, D,
-                                   _rows4(dq_out), _rows4(dk_out), _rows4(q), _rows4(k), _rows4(dq), _rows4(dk), r,
-                                   None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                   _stream_handle(stream, q))
+                                   gqs, gks, qs, ks, dqs, dks, r, None if ws is None else ws.data_ptr(),
+                                   0 if ws is None else ws.numel(), _stream_of(stream, q))
     if st != FFPA_OK:
         _raise(st, "ffpa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
 
+@functools.lru_cache(maxsize=None)
 def qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
     """Bytes of the workspace of ffpa_qk_norm_rope_bwd (0 for an unsupported head dim)."""
     return int(load_library().ffpa_qk_norm_rope_bwd_workspace_bytes(D))
@@ -216,41 +248,37 @@ def _workspace(workspace, need: int, device, stream):
     return workspace
 
 
-def _check_cache(k_cache, v_cache, dtype, Hkv, D, device):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+def _check_cache(k_cache, v_cache, dtype, D):
+    """(num_pages, page_size, Hkv) of the cache."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be 4-D [num_pages, page_size, Hkv, D] of one shape")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError(f"the cache must be {dtype}, got {k_cache.dtype} and {v_cache.dtype}")
-    if Hkv is not None and k_cache.shape[2] != Hkv:
-        raise ValueError(f"the cache has {k_cache.shape[2]} key heads, the keys have {Hkv}")
-    if k_cache.shape[3] != D:
-        raise ValueError(f"the cache has head dim {k_cache.shape[3]}, the call {D}")
-    if k_cache.device != device or v_cache.device != device:
-        raise ValueError(f"the cache must be on {device}")
+    num_pages, page_size, Hkv, Dk = shape
+    if Dk != D:
+        raise ValueError(f"the cache has head dim {Dk}, the call {D}")
+    return num_pages, page_size, Hkv
 
 
-def _check_ints(t, name, shape, dtype, device):
-    """A contiguous integer tensor of the call (any length where a size is None)."""
+def _check_ints(t, name, n, dtype):
+    """A contiguous 1-D integer tensor of the call with n entries (any number where n is None)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() != 1 or (n is not None and len(t) != n):
+        raise ValueError(f"{name} must have shape {('any',) if n is None else (n,)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _check_table(t, device):
+def _check_table(t):
     """block_table [B, max_pages]: int32, entries of a row adjacent.  Returns its row stride."""
     if t.dtype != torch.int32:
         raise TypeError(f"block_table must be int32, got {t.dtype}")
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("block_table must be 2-D [B, max_pages] with adjacent entries")
-    if t.device != device:
-        raise ValueError(f"block_table must be on {device}, got {t.device}")
     return t.stride(0)
 
 
@@ -277,21 +305,23 @@ def ffpa_kv_append(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v
         raise ValueError("q_out and q_weight need q")
     else:
         Hq = Hkv
-    _check_cache(k_cache, v_cache, k.dtype, Hkv, D, k.device)
-    _check_ints(slots, "slots", (T,), torch.int64, k.device)
+    num_pages, page_size, heads = _check_cache(k_cache, v_cache, k.dtype, D)
+    if heads != Hkv:
+        raise ValueError(f"the cache has {heads} key heads, the keys have {Hkv}")
+    _check_ints(slots, "slots", T, torch.int64)
     r = _rope_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, 1, T)
     opts = None if status is None else _options(k, None, status, None, False)
+    keep, (qs, ks, vs, qos, kcs, vcs) = _strides(q, k, v, q_out, k_cache, v_cache)
     st = load_library().ffpa_kv_append(
         None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), None if q is None else q_out.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k), T, Hq, Hkv, D, k_cache.shape[0], k_cache.shape[1],
-        None if q is None else _I64x3(*q.stride()), _I64x3(*k.stride()), _I64x3(*v.stride()),
-        None if q is None else _I64x3(*q_out.stride()), _I64x4(*k_cache.stride()), _I64x4(*v_cache.stride()),
-        slots.data_ptr(), r, _stream_handle(stream, k), opts)
+        k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k), T, Hq, Hkv, D, num_pages, page_size, qs, ks, vs, qos,
+        kcs, vcs, slots.data_ptr(), r, _stream_of(stream, k), opts)
     if st != FFPA_OK:
         _raise(st, "ffpa_kv_append")
     return q_out
 
 
+@functools.lru_cache(maxsize=None)
 def decode_paged_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
     """Bytes of the workspace of ffpa_decode_paged, for any batch and lengths (0 for unsupported heads)."""
     return int(load_library().ffpa_decode_paged_workspace_bytes(Hq, Hkv, D))
@@ -315,12 +345,12 @@ def ffpa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     if q.dim() != 3:
         raise ValueError("q must be 3-D [B, Hq, D]")
     B, Hq, D = q.shape
-    _check_cache(k_cache, v_cache, q.dtype, None, D, q.device)
-    num_pages, page_size, Hkv, _ = k_cache.shape
-    table_str = _check_table(block_table, q.device)
-    _check_ints(seq_lens, "seq_lens", (B,), torch.int32, q.device)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows for {B} requests")
+    num_pages, page_size, Hkv = _check_cache(k_cache, v_cache, q.dtype, D)
+    table_str = _check_table(block_table)
+    rows, max_pages = block_table.shape
+    if rows != B:
+        raise ValueError(f"block_table has {rows} rows for {B} requests")
+    _check_ints(seq_lens, "seq_lens", B, torch.int32)
     if out is None:
         out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
     else:
@@ -329,16 +359,16 @@ def ffpa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         _check_buffer(lse, "lse", (B, Hq), torch.float32, q.device, contiguous=True)
     elif return_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    lib = load_library()
-    ws = _workspace(workspace, int(lib.ffpa_decode_paged_workspace_bytes(Hq, Hkv, D)), q.device, stream)
+    ws = _workspace(workspace, decode_paged_workspace_bytes(Hq, Hkv, D), q.device, stream)
     sc = None if scale is None else ctypes.byref(ctypes.c_float(float(scale)))
-    opts = _options(q, None, status, wait_timeout_ns, test_drop_first_copy)
-    st = lib.ffpa_decode_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
-                               None if lse is None else lse.data_ptr(), _dtype_code(q), B, Hq, Hkv, D, num_pages,
-                               page_size, block_table.shape[1], _I64x3(*q.stride()), _I64x4(*k_cache.stride()),
-                               _I64x4(*v_cache.stride()), _I64x3(*out.stride()), block_table.data_ptr(), table_str,
-                               seq_lens.data_ptr(), sc, int(bool(enable_gqa)), ws.data_ptr(), ws.numel(),
-                               _stream_handle(stream, q), opts)
+    opts = None
+    if status is not None or wait_timeout_ns or test_drop_first_copy:
+        opts = _options(q, None, status, wait_timeout_ns, test_drop_first_copy)
+    keep, (qs, ks, vs, os) = _strides(q, k_cache, v_cache, out)
+    st = load_library().ffpa_decode_paged(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        _dtype_code(q), B, Hq, Hkv, D, num_pages, page_size, max_pages, qs, ks, vs, os, block_table.data_ptr(),
+        table_str, seq_lens.data_ptr(), sc, bool(enable_gqa), ws.data_ptr(), ws.numel(), _stream_of(stream, q), opts)
     if st != FFPA_OK:
         _raise(st, "ffpa_decode_paged")
     return (out, lse) if return_lse else out
@@ -359,12 +389,12 @@ def ffpa_page_plan(block_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: 
 
     Pages of a finished request go back by the caller: written at free_pages[free_count:]."""
     device = block_table.device
-    table_str = _check_table(block_table, device)
+    table_str = _check_table(block_table)
     B, max_pages = block_table.shape
-    _check_ints(seq_lens, "seq_lens", (B,), torch.int32, device)
-    _check_ints(new_lens, "new_lens", (B,), torch.int32, device)
-    _check_ints(free_pages, "free_pages", (None,), torch.int32, device)
-    _check_ints(free_count, "free_count", (1,), torch.int32, device)
+    _check_ints(seq_lens, "seq_lens", B, torch.int32)
+    _check_ints(new_lens, "new_lens", B, torch.int32)
+    _check_ints(free_pages, "free_pages", None, torch.int32)
+    _check_ints(free_count, "free_count", 1, torch.int32)
     if num_tokens < 0 or page_size < 1:
         raise ValueError("num_tokens must not be negative and page_size must be positive")
     slots = torch.empty(num_tokens, dtype=torch.int64, device=device)
@@ -376,7 +406,7 @@ def ffpa_page_plan(block_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: 
                                        new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
                                        free_count.data_ptr(), int(page_size), int(num_tokens), slots.data_ptr(),
                                        positions.data_ptr(), cu.data_ptr(), lens.data_ptr(), count.data_ptr(),
-                                       _stream_handle(stream, block_table), opts)
+                                       _stream_of(stream, block_table), opts)
     if st != FFPA_OK:
         _raise(st, "ffpa_page_plan")
     return slots, positions, cu, lens, count
