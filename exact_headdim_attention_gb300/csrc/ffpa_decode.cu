@@ -79,10 +79,12 @@ struct DecodePlan {
   size_t smem;
 };
 
-// Heads of one pass: 8 NT, as many as the accumulators have registers for.  A
-// larger group is split over pairs that read the same keys (the second from L2).
-int decode_nt(int group, int D) { return group <= 8 ? 1 : group <= 16 || D > 512 ? 2 : 4; }
-// Two teams leave 96 registers a thread.
+// Heads of one pass: 8 NT.  A larger group is split over pairs that read the
+// same keys again (B64 Hq32 Hkv1 D512: 335 us in two passes of 16 heads; one
+// pass of 32 heads, whose accumulators leave the registers, 524).
+__host__ __device__ constexpr int decode_nt(int group) { return group <= 8 ? 1 : 2; }
+// Two teams leave 96 registers a thread, too few for 16 heads (B32 Hq32 Hkv2
+// D512: 194 us with one team, 222 with two).
 __host__ __device__ constexpr int decode_teams(int nt) { return nt == 1 ? 2 : 1; }
 // Parts of D in the first product, and groups of warps with keys of their own in the second.
 __host__ __device__ constexpr int decode_parts(int tile) { return tile >= 128 ? 1 : 128 / tile; }
@@ -100,7 +102,7 @@ __host__ __device__ constexpr size_t decode_score_bytes(int nt, int tile) {
 
 DecodePlan decode_plan(int D, int group) {
   DecodePlan p;
-  p.nt = decode_nt(group, D);
+  p.nt = decode_nt(group);
   p.teams = decode_teams(p.nt);
   p.head_tiles = (group + 8 * p.nt - 1) / (8 * p.nt);
   p.tile = D > 512 ? 16 : D > 256 ? 32 : D > 128 ? 64 : D > 64 ? 128 : 256;
@@ -267,14 +269,21 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, boo
     for (int j = 0; j < 4; ++j) {
       if (32 * j >= mine) break;
       const int end = min(32, mine - 32 * j);
-#pragma unroll 2
-      for (int r = 0; r < end; r += step) {
-        const int64_t at_row = __shfl_sync(~0u, from[j], r + r0);
-        if (r + r0 >= end) continue;
-        const int row = first + 32 * j + r + r0;
-        for (int c = c0; c < cpr; c += wide)
-          copy16_async(tile + (c >> 3) * (T * 128) + row * 128 + ((c ^ row) & 7) * 16,
-                       at_row >= 0 ? head + at_row + c * 16 : base, at_row >= 0 ? 16 : 0);
+      // Four rows a lane at a time: their offsets first, then the copies.
+      for (int r = 0; r < end; r += 4 * step) {
+        int64_t row_at[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) row_at[y] = __shfl_sync(~0u, from[j], (r + y * step + r0) & 31);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int in = r + y * step + r0;
+          if (in >= end) continue;
+          const int row = first + 32 * j + in;
+          const char* src = row_at[y] >= 0 ? head + row_at[y] : base;
+          const uint32_t bytes = row_at[y] >= 0 ? 16 : 0;
+          for (int c = c0; c < cpr; c += wide)
+            copy16_async(tile + (c >> 3) * (T * 128) + row * 128 + ((c ^ row) & 7) * 16, bytes ? src + c * 16 : base, bytes);
+        }
       }
     }
     copy_arrive(smem_u32(full + slot));
@@ -813,9 +822,8 @@ ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int gr
 
 template <bool F16, int T>
 ffpa_status launch_decode_tile(const DecodeParams& P, const DecodePlan& pl, int grid, int dev, cudaStream_t stream) {
-  if (pl.nt == 1) return launch_decode_as<F16, 1, T>(P, pl, grid, dev, stream);
-  if (T < 32 || pl.nt == 2) return launch_decode_as<F16, 2, T>(P, pl, grid, dev, stream);
-  return launch_decode_as<F16, T < 32 ? 2 : 4, T>(P, pl, grid, dev, stream);
+  return pl.nt == 1 ? launch_decode_as<F16, 1, T>(P, pl, grid, dev, stream)
+                    : launch_decode_as<F16, 2, T>(P, pl, grid, dev, stream);
 }
 
 template <bool F16>
@@ -836,7 +844,7 @@ extern "C" {
 
 size_t ffpa_decode_paged_workspace_bytes(int Hq, int Hkv, int D) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 64 || D > 1024 || D % 8 != 0) return 0;
-  return ffpa::decode_space(ffpa::DEC_GRID_MAX, 8 * ffpa::decode_nt(Hq / Hkv, D), D).total;
+  return ffpa::decode_space(ffpa::DEC_GRID_MAX, 8 * ffpa::decode_nt(Hq / Hkv), D).total;
 }
 
 ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
