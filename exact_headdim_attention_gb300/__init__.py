@@ -50,4 +50,11 @@ from .paged import (  # noqa: F401,E402
     qk_norm_rope_bwd_workspace_bytes,
     rope_inv_freq,
 )
-from .torch_ops import ffpa_attn_func, ffpa_attn_varlen_func  # noqa: F401,E402
+from .torch_ops import (  # noqa: F401,E402
+    ffpa_attn_decode_func,
+    ffpa_attn_func,
+    ffpa_attn_varlen_func,
+    ffpa_kv_append_func,
+    ffpa_page_plan_func,
+    ffpa_qk_norm_rope_func,
+)

@@ -13,6 +13,15 @@ backward), no dropout.  The dense operator is
 differentiable through ``ffpa_bwd`` (the backward kernels; a mask enters
 the recomputed scores, but no gradient is formed for the mask itself), and
 the varlen operator through ``ffpa_bwd_varlen``.
+
+``torch.ops.ffpa.qk_norm_rope`` (differentiable through
+``ffpa_qk_norm_rope_bwd``), ``kv_append``, ``decode_paged`` and
+``page_plan`` do the same for the calls around a paged key/value cache
+(paged.py); the last three serve and have no gradient, and ``kv_append`` and
+``page_plan`` declare the cache and the block table that they write.  As with
+any operator of torch, a backward that is captured into a CUDA graph must
+not meet leaves that an eager graph made on another stream still holds: free
+that graph first, or capture ``ffpa_qk_norm_rope_bwd`` itself.
 """
 from __future__ import annotations
 
@@ -20,7 +29,7 @@ from typing import Optional
 
 import torch
 
-from . import _binding
+from . import _binding, paged
 
 
 @torch.library.custom_op("ffpa::attn_fwd", mutates_args=())
@@ -138,3 +147,129 @@ def ffpa_attn_varlen_func(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                             int(max_seqlen_k), bool(causal), softmax_scale,
                                             bool(enable_gqa))
     return (o, lse) if return_lse else o
+
+
+@torch.library.custom_op("ffpa::qk_norm_rope", mutates_args=())
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
+                 inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                 k_weight: Optional[torch.Tensor], eps: float, interleaved: bool,
+                 rope_scale: float) -> tuple[torch.Tensor, torch.Tensor]:
+    """Queries and keys normed per head and rotated by position."""
+    return paged.ffpa_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps=eps,
+                                   interleaved=interleaved, rope_scale=rope_scale)
+
+
+@qk_norm_rope.register_fake
+def _qk_norm_rope_fake(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, rope_scale):
+    return (torch.empty_like(q, memory_format=torch.contiguous_format),
+            torch.empty_like(k, memory_format=torch.contiguous_format))
+
+
+def _qk_norm_rope_setup_context(ctx, inputs, output):
+    q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, rope_scale = inputs
+    ctx.save_for_backward(q, k, positions, inv_freq, q_weight, k_weight)
+    ctx.eps, ctx.interleaved, ctx.rope_scale = eps, interleaved, rope_scale
+    ctx.set_materialize_grads(False)
+
+
+def _qk_norm_rope_backward(ctx, grad_q, grad_k):
+    if ctx.needs_input_grad[3]:
+        raise NotImplementedError("no gradient is formed for inv_freq")
+    q, k, positions, inv_freq, q_weight, k_weight = ctx.saved_tensors
+    # An output that the loss does not use has no gradient: zeros for its rows.
+    grad_q = torch.zeros_like(q, memory_format=torch.contiguous_format) if grad_q is None else grad_q.contiguous()
+    grad_k = torch.zeros_like(k, memory_format=torch.contiguous_format) if grad_k is None else grad_k.contiguous()
+    dq, dk, dqw, dkw = paged.ffpa_qk_norm_rope_bwd(grad_q, grad_k, q, k, positions, inv_freq, q_weight, k_weight,
+                                                   eps=ctx.eps, interleaved=ctx.interleaved,
+                                                   rope_scale=ctx.rope_scale)
+    return dq, dk, None, None, dqw, dkw, None, None, None
+
+
+qk_norm_rope.register_autograd(_qk_norm_rope_backward, setup_context=_qk_norm_rope_setup_context)
+
+
+@torch.library.custom_op("ffpa::kv_append", mutates_args=("k_cache", "v_cache"))
+def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+              v_cache: torch.Tensor, slots: torch.Tensor, positions: Optional[torch.Tensor],
+              inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+              eps: float, interleaved: bool, rope_scale: float) -> torch.Tensor:
+    """Keys and values into cache slots; the normed and rotated queries (no rows without q)."""
+    out = paged.ffpa_kv_append(q, k, v, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps=eps,
+                               interleaved=interleaved, rope_scale=rope_scale)
+    return k.new_empty((0,) + tuple(k.shape[1:])) if out is None else out
+
+
+@kv_append.register_fake
+def _kv_append_fake(q, k, v, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps, interleaved,
+                    rope_scale):
+    if q is None:
+        return k.new_empty((0,) + tuple(k.shape[1:]))
+    return torch.empty_like(q, memory_format=torch.contiguous_format)
+
+
+@torch.library.custom_op("ffpa::decode_paged", mutates_args=())
+def decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, scale: Optional[float],
+                 enable_gqa: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    """O [B,Hq,D] and LSE [B,Hq] (fp32) of one new token per request over a paged cache."""
+    return paged.ffpa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=scale, enable_gqa=enable_gqa,
+                                   return_lse=True)
+
+
+@decode_paged.register_fake
+def _decode_paged_fake(q, k_cache, v_cache, block_table, seq_lens, scale, enable_gqa):
+    B, Hq, _ = q.shape
+    return (torch.empty_like(q, memory_format=torch.contiguous_format),
+            q.new_empty((B, Hq), dtype=torch.float32))
+
+
+@torch.library.custom_op("ffpa::page_plan", mutates_args=("block_table",))
+def page_plan(block_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+              free_count: torch.Tensor, page_size: int, num_tokens: int
+              ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Slots, positions, cumulative lengths, new lengths and free count; the table in place."""
+    return paged.ffpa_page_plan(block_table, seq_lens, new_lens, free_pages, free_count, page_size, num_tokens)
+
+
+@page_plan.register_fake
+def _page_plan_fake(block_table, seq_lens, new_lens, free_pages, free_count, page_size, num_tokens):
+    return (seq_lens.new_empty(num_tokens, dtype=torch.int64), seq_lens.new_empty(num_tokens),
+            seq_lens.new_empty(seq_lens.shape[0] + 1), torch.empty_like(seq_lens), torch.empty_like(free_count))
+
+
+def ffpa_qk_norm_rope_func(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                           inv_freq: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                           k_weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6, interleaved: bool = False,
+                           rope_scale: float = 1.0):
+    """RMS norm of every query and key head and rotation by position (see paged.ffpa_qk_norm_rope),
+    differentiable in q, k and the weights.  Returns (q, k) for ffpa_attn_func ([B,H,N,D]) or
+    ffpa_attn_varlen_func ([T,H,D])."""
+    return torch.ops.ffpa.qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, float(eps), bool(interleaved),
+                                       float(rope_scale))
+
+
+def ffpa_kv_append_func(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, slots: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                        inv_freq: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6, interleaved: bool = False,
+                        rope_scale: float = 1.0):
+    """Keys (normed and rotated) and values into cache slots (see paged.ffpa_kv_append).  Returns the
+    queries, or None without q."""
+    out = torch.ops.ffpa.kv_append(q, k, v, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight,
+                                   float(eps), bool(interleaved), float(rope_scale))
+    return None if q is None else out
+
+
+def ffpa_attn_decode_func(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                          seq_lens: torch.Tensor, scale: Optional[float] = None, enable_gqa: bool = False, *,
+                          return_lse: bool = False):
+    """Attention of one new token per request over a paged cache (see paged.ffpa_decode_paged)."""
+    o, lse = torch.ops.ffpa.decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale, bool(enable_gqa))
+    return (o, lse) if return_lse else o
+
+
+def ffpa_page_plan_func(block_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor,
+                        free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, num_tokens: int):
+    """Pages, slots and positions of one step's new tokens (see paged.ffpa_page_plan)."""
+    return torch.ops.ffpa.page_plan(block_table, seq_lens, new_lens, free_pages, free_count, int(page_size),
+                                    int(num_tokens))
