@@ -8,12 +8,12 @@
 // is laid out for it:
 //
 //  - The keys of all (request, key head) pairs form one line of T-key tiles,
-//    cut into equal runs, one run per CTA (one CTA per SM): a long request is
-//    shared by many CTAs and short ones share a CTA, whatever the mix, and the
-//    host needs no lengths.  A pair that ends inside its CTA is written at
-//    once; a pair cut between CTAs leaves fp32 partial sums with their maximum
-//    and sum, which the second launch joins in the order of the CTAs.
-//  - Two rings of shared-memory tiles, one of K and one of V (some 200 KB, all
+//    cut into equal runs, one run per CTA (two CTAs per SM, or one): a long
+//    request is shared by many CTAs and short ones share a CTA, whatever the
+//    mix, and the host needs no lengths.  A pair that ends inside its CTA is
+//    written at once; a pair cut between CTAs leaves fp32 partial sums with
+//    their maximum and sum, which the second launch joins in the order of the CTAs.
+//  - Two rings of shared-memory tiles, one of K and one of V (some 200 KB an SM, all
 //    but the tiles in work in flight), are kept full by warps of their own.
 //    Where pages hold a multiple of 8 keys a tile arrives as tensor boxes of
 //    up to T rows of one page, with the 128-byte swizzle that the matrix
@@ -22,17 +22,19 @@
 //    cycles, 1.65 TB/s with the 256-byte rows of D = 128.)
 //  - Keys (then columns of V) are the 16 rows of mma.m16n8k16 and the heads its
 //    8 columns: K and V are the operands read once, and up to 8 heads cost one
-//    instruction per 256 elements.  Eight warps make a team.  For the scores a
-//    warp takes 16 keys and a part of D; for the output it takes 32 keys and a
-//    share of the columns.  Between them lies the only barrier of a tile: each
+//    instruction per 256 elements.  For the scores each of eight warps takes 16
+//    keys and a part of D; for the output it takes 32 keys and a share of the
+//    columns.  Between them lies the only barrier of a tile: each
 //    warp reads the scores of its keys from shared memory, adds the parts and
 //    forms its own P operand in registers (the warps that share keys repeat
 //    the 8 exponentials a lane, which costs less than a second barrier).
 //  - A tile is a chain of dependent steps that leaves most issue slots empty,
-//    so two teams take the tiles in turn where the registers allow it.
+//    so two CTAs share an SM where the registers allow it, each with half of
+//    the rings.
 //  - Maximum and sum are kept in fp32 by each group of warps that has keys of
-//    its own and joined at the pair's end in a fixed tree.  P is rounded to
-//    the input type, as in the forward kernels; the sum is of the unrounded values.
+//    its own and joined at the pair's end in the order of the groups.  P is
+//    rounded to the input type, as in the forward kernels; the sum is of the
+//    unrounded values.
 //
 // Every wait on a copy has a time limit, after which the call's status word
 // receives FFPA_ERR_DEVICE_TIMEOUT and the CTA runs out without waiting.
@@ -41,11 +43,11 @@
 namespace ffpa {
 namespace {
 
-constexpr int DEC_TEAM = 8;           // warps of a team
-constexpr int DEC_COPY_WARPS = 4;     // two for K, two for V
+constexpr int DEC_WARPS = 8;          // that multiply
+constexpr int DEC_THREADS = (DEC_WARPS + 2) * 32;   // and one each that brings K and V
 constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
 // CTAs of any sm_103 part; the workspace is sized for them without asking a device.
-constexpr int DEC_GRID_MAX = 160;
+constexpr int DEC_GRID_MAX = 320;
 
 struct DecodeParams {
   CUtensorMap map_k, map_v;
@@ -75,7 +77,7 @@ struct DecodeParams {
 // Sizes of one call.  A tile has T = 16 keys for D > 512 and twice as many each
 // time D halves (at most 32 KB).
 struct DecodePlan {
-  int nt, teams, tile, chunks, ring_k, ring_v, head_tiles;
+  int nt, ctas, tile, chunks, ring_k, ring_v, head_tiles;
   size_t smem;
 };
 
@@ -83,41 +85,32 @@ struct DecodePlan {
 // same keys again (B64 Hq32 Hkv1 D512: 335 us in two passes of 16 heads; one
 // pass of 32 heads, whose accumulators leave the registers, 524).
 __host__ __device__ constexpr int decode_nt(int group) { return group <= 8 ? 1 : 2; }
-// Two teams leave 96 registers a thread, too few for 16 heads (B32 Hq32 Hkv2
-// D512: 194 us with one team, 222 with two).
-__host__ __device__ constexpr int decode_teams(int nt) { return nt == 1 ? 2 : 1; }
+// CTAs of an SM: two leave 96 registers a thread, too few for 16 heads (B32 Hq32
+// Hkv2 D512: 194 us with 8 computing warps an SM, 222 with 16).
+__host__ __device__ constexpr int decode_ctas(int nt) { return nt == 1 ? 2 : 1; }
 // Parts of D in the first product, and groups of warps with keys of their own in the second.
 __host__ __device__ constexpr int decode_parts(int tile) { return tile >= 128 ? 1 : 128 / tile; }
 __host__ __device__ constexpr int decode_groups(int tile) { return tile >= 32 ? tile / 32 : 1; }
-// Scores of two tiles a team (one where a warp reads no other's); at a pair's
-// end half of the groups' outputs, 64 columns of a warp at a time.
-__host__ __device__ constexpr bool decode_own_keys(int tile) { return tile / 16 > DEC_TEAM; }
+// Scores of two tiles (of one where a warp reads no other's).
+__host__ __device__ constexpr bool decode_own_keys(int tile) { return tile / 16 > DEC_WARPS; }
 __host__ __device__ constexpr size_t decode_score_bytes(int nt, int tile) {
-  const int teams = decode_teams(nt);
-  const size_t scores = (size_t)teams * (decode_own_keys(tile) ? 1 : 2) * decode_parts(tile) * 8 * nt * (tile + 8) * 4;
-  const int groups = teams * decode_groups(tile);
-  const size_t join = groups > 1 ? (size_t)(groups / 2) * 8 * nt * (DEC_TEAM / decode_groups(tile) * 64 + 4) * 4 : 0;
-  return ((scores > join ? scores : join) + 1023) / 1024 * 1024;
+  return ((size_t)(decode_own_keys(tile) ? 1 : 2) * decode_parts(tile) * 8 * nt * (tile + 8) * 4 + 1023) / 1024 * 1024;
 }
 
 DecodePlan decode_plan(int D, int group) {
   DecodePlan p;
   p.nt = decode_nt(group);
-  p.teams = decode_teams(p.nt);
+  p.ctas = decode_ctas(p.nt);
   p.head_tiles = (group + 8 * p.nt - 1) / (8 * p.nt);
   p.tile = D > 512 ? 16 : D > 256 ? 32 : D > 128 ? 64 : D > 64 ? 128 : 256;
   p.chunks = (D + 63) / 64;
   const size_t fixed = decode_score_bytes(p.nt, p.tile);
   const size_t stage = (size_t)p.tile * p.chunks * 128;
-  // 4 KB stay for static shared memory and the alignment of the boxes.
-  int n = static_cast<int>((SMEM_LIMIT - 4096 - fixed) / stage);
+  // 4 KB a CTA stay for static shared memory, the alignment of the boxes and the system.
+  int n = static_cast<int>((SMEM_LIMIT / p.ctas - 4096 - fixed) / stage);
   if (n > 2 * DEC_RING_MAX) n = 2 * DEC_RING_MAX;
-  // A slot belongs to one team (rings of an even length with two of them): the
-  // parity of its barrier tells a tile from the slot's previous one only while
-  // one reader takes the slot's tiles in order.
-  p.ring_v = p.teams == 2 ? n / 4 * 2 : n / 2;
-  p.ring_k = p.teams == 2 ? (n - p.ring_v) / 2 * 2 : n - p.ring_v;
-  if (p.ring_k > DEC_RING_MAX) p.ring_k = DEC_RING_MAX;
+  p.ring_v = n / 2;
+  p.ring_k = n - n / 2;
   p.smem = 1024 + fixed + (size_t)(p.ring_k + p.ring_v) * stage;
   return p;
 }
@@ -205,7 +198,7 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, bool
       lap ^= 1u;
     }
   }
-  // Copies still in flight land before the CTA ends (the teams wait for them,
+  // Copies still in flight land before the CTA ends (the computing warps wait for them,
   // unless they gave up).
   for (int j = i < slots ? i : slots; j > 0; --j) {
     if (slot == 0) {
@@ -217,11 +210,11 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, bool
   }
 }
 
-// The same tile for any page size: a warp looks half of its rows up lane by
-// lane, one tile ahead, and copies them in pieces of 16 bytes, a power of two of
+// The same tile for any page size: the warp looks its rows up lane by lane,
+// one tile ahead, and copies them in pieces of 16 bytes, a power of two of
 // lanes to a row.  A row without a key, or of a page that does not exist,
 // becomes zeros.
-__device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, bool is_v, int half, Place at, int n_tiles,
+__device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, bool is_v, Place at, int n_tiles,
                                                uint32_t ring, int slots, uint64_t* full, uint64_t* empty,
                                                volatile int* abort_flag) {
   const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles;
@@ -229,17 +222,16 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, boo
   int wide = 8;                                    // lanes of a row
   while (wide < cpr && wide < 32) wide *= 2;
   const int c0 = lane % wide, r0 = lane / wide, step = 32 / wide;
-  const int mine = T / 2, first = half * mine;     // rows of this warp
   const char* base = is_v ? P.v : P.k;
   const int64_t sp = is_v ? P.v_sp : P.k_sp, ss = is_v ? P.v_ss : P.k_ss, sh = is_v ? P.v_sh : P.k_sh;
   const uint32_t stage = T * P.chunks * 128;
-  int page[4];
+  int page[8];
   auto look_up = [&](const Place& p) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (32 * j >= mine) break;
-      const int r = lane + 32 * j, key = p.t * T + first + r;
-      page[j] = r < mine && key < p.len ? P.table[p.b * P.table_str + key / P.page_size] : -1;
+    for (int j = 0; j < 8; ++j) {
+      if (32 * j >= T) break;
+      const int r = lane + 32 * j, key = p.t * T + r;
+      page[j] = r < T && key < p.len ? P.table[p.b * P.table_str + key / P.page_size] : -1;
     }
   };
   look_up(at);
@@ -248,13 +240,13 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, boo
   for (int i = 0; i < n_tiles; ++i) {
     // Offsets of this tile's rows (-1: zeros), then the pages of the next.
     const char* head = base + (at.u / P.head_tiles) * sh;
-    int64_t from[4];
+    int64_t from[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       from[j] = -1;
-      if (32 * j >= mine) break;
-      const int r = lane + 32 * j, key = at.t * T + first + r;
-      if (r < mine && key < at.len) {
+      if (32 * j >= T) break;
+      const int r = lane + 32 * j, key = at.t * T + r;
+      if (r < T && key < at.len) {
         if (page[j] >= 0 && page[j] < P.num_pages)
           from[j] = page[j] * sp + key % P.page_size * ss;
         else
@@ -266,9 +258,9 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, boo
     if (!all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) || P.drop) break;
     const uint32_t tile = ring + slot * stage;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (32 * j >= mine) break;
-      const int end = min(32, mine - 32 * j);
+    for (int j = 0; j < 8; ++j) {
+      if (32 * j >= T) break;
+      const int end = min(32, T - 32 * j);
       // Four rows a lane at a time: their offsets first, then the copies.
       for (int r = 0; r < end; r += 4 * step) {
         int64_t row_at[4];
@@ -278,7 +270,7 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, boo
         for (int y = 0; y < 4; ++y) {
           const int in = r + y * step + r0;
           if (in >= end) continue;
-          const int row = first + 32 * j + in;
+          const int row = 32 * j + in;
           const char* src = row_at[y] >= 0 ? head + row_at[y] : base;
           const uint32_t bytes = row_at[y] >= 0 ? 16 : 0;
           for (int c = c0; c < cpr; c += wide)
@@ -296,19 +288,18 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, boo
 }
 
 template <bool F16, int NT, int T>
-__global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS) * 32, 1)
-    decode_kernel(const __grid_constant__ DecodeParams P) {
-  constexpr int HEADS = 8 * NT, TEAMS = decode_teams(NT), THREADS = (TEAMS * DEC_TEAM + DEC_COPY_WARPS) * 32;
-  constexpr int PARTS = decode_parts(T), WK = decode_groups(T), MT = T / 16, GROUPS = TEAMS * WK;
+__global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(const __grid_constant__ DecodeParams P) {
+  constexpr int HEADS = 8 * NT, THREADS = DEC_THREADS;
+  constexpr int PARTS = decode_parts(T), GROUPS = decode_groups(T), MT = T / 16;
   constexpr int KSTEPS = T < 32 ? 1 : 2;      // of 16 keys, of a warp in the second product
   constexpr int DT = T < 32 ? 8 : 4;          // column tiles of a warp there
-  constexpr int WDS = DEC_TEAM / WK;          // warps that share keys there
+  constexpr int WDS = DEC_WARPS / GROUPS;     // warps that share keys there
   constexpr int SPITCH = T + 8, SBUF = PARTS * HEADS * SPITCH;
   constexpr bool OWN = decode_own_keys(T);    // a warp's scores are those of its own keys
   extern __shared__ char smem_raw[];
   __shared__ uint64_t full_k[DEC_RING_MAX], full_v[DEC_RING_MAX], empty_k[DEC_RING_MAX], empty_v[DEC_RING_MAX];
   __shared__ float2 ml_s[GROUPS][HEADS];
-  __shared__ long long scan_s[25];
+  __shared__ long long scan_s[DEC_THREADS / 32 + 1];
   __shared__ int start_s;
   __shared__ int abort_flag;
   char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -342,12 +333,12 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
     }
     if (tid == 0) {
       abort_flag = 0;
-      const int arrivals = P.boxed ? 1 : 64;
+      const int arrivals = P.boxed ? 1 : 32;
       for (int i = 0; i < DEC_RING_MAX; ++i) {
         mbar_init(smem_u32(full_k + i), arrivals);
         mbar_init(smem_u32(full_v + i), arrivals);
-        mbar_init(smem_u32(empty_k + i), DEC_TEAM);
-        mbar_init(smem_u32(empty_v + i), DEC_TEAM);
+        mbar_init(smem_u32(empty_k + i), DEC_WARPS);
+        mbar_init(smem_u32(empty_v + i), DEC_WARPS);
       }
       fence_mbar_init();
       P.meta[blockIdx.x] = make_int2(-1, 0);
@@ -373,7 +364,7 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
         at += tiles * pairs;
       }
       start_s = b;
-      scan_s[24] = lo - at;
+      scan_s[DEC_THREADS / 32] = lo - at;
     }
     // Requests without keys have no tile: their rows are written here.
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
@@ -398,45 +389,43 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
     cur.b = start_s;
     cur.len = clamped_len(P, cur.b);
     cur.tiles = (cur.len + T - 1) / T;
-    const long long r = scan_s[24];
+    const long long r = scan_s[DEC_THREADS / 32];
     cur.u = (int)(r / cur.tiles);
     cur.t = (int)(r % cur.tiles);
   }
   dependents_launch();
   const int n_tiles = (int)(hi - lo);
-  float* scores = reinterpret_cast<float*>(smem);                  // [TEAMS][2, or 1 when OWN][PARTS][HEADS][SPITCH]
+  float* scores = reinterpret_cast<float*>(smem);                  // [2, or 1 when OWN][PARTS][HEADS][SPITCH]
   const uint32_t ring_k = smem_u32(smem + decode_score_bytes(NT, T));
   const uint32_t ring_v = ring_k + P.ring_k * stage;
 
-  if (warp >= TEAMS * DEC_TEAM) {
-    const int w = warp - TEAMS * DEC_TEAM;
-    const bool is_v = w >= 2;
+  if (warp >= DEC_WARPS) {
+    const bool is_v = warp > DEC_WARPS;
     uint64_t *full = is_v ? full_v : full_k, *empty = is_v ? empty_v : empty_k;
     const uint32_t ring = is_v ? ring_v : ring_k;
     const int slots = is_v ? P.ring_v : P.ring_k;
-    if (!P.boxed)
-      produce_pieces(P, T, is_v, w & 1, cur, n_tiles, ring, slots, full, empty, &abort_flag);
-    else if ((w & 1) == 0)
+    if (P.boxed)
       produce_boxes(P, T, is_v, cur, n_tiles, ring, slots, full, empty, &abort_flag);
+    else
+      produce_pieces(P, T, is_v, cur, n_tiles, ring, slots, full, empty, &abort_flag);
     return;
   }
 
-  // ---- the teams
-  const int team = warp / DEC_TEAM, tw = warp % DEC_TEAM;
+  // ---- the computing warps
   const long long runs = total < gridDim.x ? total : gridDim.x;
   const int ksteps = (P.D + 15) / 16;
   // Shares of D are whole chunks, so that a chunk's swizzle is a constant of the code.
-  const int part = tw / MT;                        // in the first product (0 when a warp has two key tiles)
+  const int part = warp / MT;                        // in the first product (0 when a warp has two key tiles)
   const int kper = (P.chunks + PARTS - 1) / PARTS * 4;
   const int k0 = part * kper, kn = max(0, min(kper, ksteps - k0));
-  const int wkey = tw / WDS, wd = tw % WDS, group = team * WK + wkey;
+  const int wkey = warp / WDS, wd = warp % WDS;    // group of keys, share of columns
   const int dper = (P.chunks + WDS - 1) / WDS * 4;
   const int d0 = wd * dper, dn = max(0, min(dper, ksteps - d0));
   const int c2 = (lane % 4) * 2, hq = lane / 4;
   const uint32_t chunk_bytes = P.box_rows * 128;
   // Row r of a tile: boxes of box_rows rows, in each chunk after chunk.
   auto row_at = [&](int r) { return r / P.box_rows * (P.chunks * chunk_bytes) + r % P.box_rows * 128; };
-  const int key0 = OWN ? tw * 32 : tw % MT * 16;   // first key of the first product
+  const int key0 = OWN ? warp * 32 : warp % MT * 16;   // first key of the first product
   const int kr = key0 + (lane & 15), vr = wkey * 32 + (lane >> 4) * 8 + (lane & 7);
   const uint32_t k_at = ring_k + row_at(kr) + (k0 >> 2) * chunk_bytes + (((lane >> 4) ^ (lane & 7)) << 4);
   const uint32_t k_at2 = OWN ? k_at - row_at(kr) + row_at(kr + 16) : 0;
@@ -445,10 +434,11 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
   uint32_t qf[8][NT][2];
   float acc[DT][NT][4];
   float top[NT], sum[NT];                          // of head 8 n + lane / 4
-  int slot_k = team, slot_v = team;                // team < 2 <= ring
+  int slot_k = 0, slot_v = 0;
   uint32_t lap_k = 0, lap_v = 0;
   bool alive = true;
   int buf = 0;
+  constexpr int N = DEC_WARPS * 32;
 
   for (int i0 = 0; i0 < n_tiles;) {
     // ---- one pair's tiles of this run: [i0, i1)
@@ -456,7 +446,6 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
     const int hk = cur.u / P.head_tiles, ht = cur.u % P.head_tiles;
     const int hq0 = hk * P.group + ht * HEADS;
     const int rows = min(HEADS, P.group - ht * HEADS);
-    int i = i0 + ((i0 ^ team) & (TEAMS - 1));      // the team's first tile
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int head = n * 8 + hq;
@@ -466,7 +455,7 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int d = (k0 + s) * 16 + j * 8 + c2;
-          qf[s][n][j] = head < rows && s < kn && d < P.D && i < i1 ? *reinterpret_cast<const uint32_t*>(src + d * 2) : 0u;
+          qf[s][n][j] = head < rows && s < kn && d < P.D ? *reinterpret_cast<const uint32_t*>(src + d * 2) : 0u;
         }
 #pragma unroll
       for (int s = 0; s < DT; ++s)
@@ -475,9 +464,9 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
       top[n] = -INFINITY;
       sum[n] = 0.0f;
     }
-    int left = cur.len - (cur.t + (i - i0)) * T - wkey * 32;    // keys from this warp's first one on
-    for (; i < i1; i += TEAMS, left -= TEAMS * T) {
-      float* sc = scores + (OWN ? team : team * 2 + buf) * SBUF;
+    int left = cur.len - cur.t * T - wkey * 32;    // keys from this warp's first one on
+    for (int i = i0; i < i1; ++i, left -= T) {
+      float* sc = scores + (OWN ? 0 : buf) * SBUF;
       buf ^= 1;
       if (OWN) __syncwarp();
 
@@ -510,12 +499,12 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(empty_k + slot_k));
-      if ((slot_k += TEAMS) >= P.ring_k) {
-        slot_k -= P.ring_k;
+      if (++slot_k == P.ring_k) {
+        slot_k = 0;
         lap_k ^= 1u;
       }
       // The scores are complete (the next tile writes the other buffer).
-      if (!OWN) named_bar_sync(1 + team, DEC_TEAM * 32);
+      if (!OWN) named_bar_sync(1, N);
 
       // ---- P of this warp's keys, as the operand of the second product
       uint32_t pf[KSTEPS][NT][2];
@@ -603,70 +592,26 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(empty_v + slot_v));
-      if ((slot_v += TEAMS) >= P.ring_v) {
-        slot_v -= P.ring_v;
+      if (++slot_v == P.ring_v) {
+        slot_v = 0;
         lap_v ^= 1u;
       }
     }
 
-    // ---- the pair's sums, joined over the groups of warps in a fixed tree
+    // ---- the pair's sums: written (a whole pair), or left for the second launch (a cut one)
+    const bool done = i1 - i0 == cur.tiles - cur.t;
+    const bool whole = done && cur.t == 0;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.t == 0 ? 1 : 0);
+    float* part_o = P.part + slot * HEADS * P.D;
+    float2* part_ml = P.part_ml + slot * HEADS;
+    char* out = P.o + cur.b * P.o_sb + (int64_t)hq0 * P.o_sh;
+    float* lse = P.lse + (int64_t)cur.b * P.Hq + hq0;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       sum[n] += __shfl_xor_sync(~0u, sum[n], 1);
       sum[n] += __shfl_xor_sync(~0u, sum[n], 2);
     }
-    constexpr int N = TEAMS * DEC_TEAM * 32;
-    constexpr int JPITCH = WDS * 64 + 4;
-    if (GROUPS > 1) named_bar_sync(3, N);          // the scores are read, their place is free
-#pragma unroll 1
-    for (int half = GROUPS / 2; half > 0; half /= 2) {
-      float f[NT][4];                              // factors of this group's columns and of the other's
-#pragma unroll
-      for (int s0 = 0; s0 < DT; s0 += 4) {
-        float* at = scores + ((group & (half - 1)) * HEADS + c2) * JPITCH + wd * 64 + hq;
-        if (group >= half && group < 2 * half) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (s0 == 0 && wd == 0 && lane % 4 == 0) ml_s[group][n * 8 + hq] = make_float2(top[n], sum[n]);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) at[(n * 8 + (j & 1)) * JPITCH + s * 16 + (j >> 1) * 8] = acc[s0 + s][n][j];
-          }
-        }
-        named_bar_sync(3, N);
-        if (group < half) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (s0 == 0) {
-              const float2 other = ml_s[group + half][n * 8 + hq];
-              const float now = fmaxf(top[n], other.x);
-              const float base = now == -INFINITY ? 0.0f : now;
-              const float fa = ex2_approx(top[n] - base), fb = ex2_approx(other.x - base);
-              top[n] = now;
-              sum[n] = sum[n] * fa + other.y * fb;
-              f[n][0] = __shfl_sync(~0u, fa, c2 * 4);
-              f[n][1] = __shfl_sync(~0u, fa, c2 * 4 + 4);
-              f[n][2] = __shfl_sync(~0u, fb, c2 * 4);
-              f[n][3] = __shfl_sync(~0u, fb, c2 * 4 + 4);
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                acc[s0 + s][n][j] = acc[s0 + s][n][j] * f[n][j & 1] +
-                                    at[(n * 8 + (j & 1)) * JPITCH + s * 16 + (j >> 1) * 8] * f[n][2 + (j & 1)];
-          }
-        }
-        named_bar_sync(3, N);
-      }
-    }
-    const bool done = i1 - i0 == cur.tiles - cur.t;
-    if (group == 0) {
-      // ---- written: a whole pair as it is, a cut one for the second launch
-      const bool whole = done && cur.t == 0;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.t == 0 ? 1 : 0);
-      float* part_o = P.part + slot * HEADS * P.D;
+    if (GROUPS == 1) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float inv = whole ? (sum[n] == 0.0f ? 0.0f : 1.0f / sum[n]) : 1.0f;
@@ -675,13 +620,12 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
           const int head = n * 8 + c2 + (j & 1);
           const float f = __shfl_sync(~0u, inv, c2 * 4 + (j & 1) * 4);
           if (head >= rows) continue;
-          char* out = P.o + cur.b * P.o_sb + (int64_t)(hq0 + head) * P.o_sh;
 #pragma unroll
           for (int s = 0; s < DT; ++s) {
             const int d = (d0 + s) * 16 + hq + (j >> 1) * 8;
             if (s >= dn || d >= P.D) continue;
             if (whole)
-              store16<F16>(out + d * 2, acc[s][n][j] * f);
+              store16<F16>(out + head * P.o_sh + d * 2, acc[s][n][j] * f);
             else
               part_o[(int64_t)head * P.D + d] = acc[s][n][j];
           }
@@ -689,17 +633,67 @@ __global__ void __launch_bounds__((decode_teams(NT) * DEC_TEAM + DEC_COPY_WARPS)
         const int head = n * 8 + hq;
         if (wd == 0 && lane % 4 == 0 && head < rows) {
           if (!whole)
-            P.part_ml[slot * HEADS + head] = make_float2(top[n], sum[n]);
+            part_ml[head] = make_float2(top[n], sum[n]);
           else if (P.lse)
-            P.lse[(int64_t)cur.b * P.Hq + hq0 + head] =
-                sum[n] == 0.0f ? -INFINITY : (top[n] + log2f(sum[n])) * 0.69314718055994531f;
+            lse[head] = sum[n] == 0.0f ? -INFINITY : (top[n] + log2f(sum[n])) * 0.69314718055994531f;
         }
       }
-      if (!done && cur.t == 0 && tw == 0 && lane == 0) {
-        // The pair goes on in the next CTAs; its last tile says how far.
-        const long long last = lo + i0 + cur.tiles - 1;
-        P.meta[blockIdx.x] = make_int2(cur.b * pairs + cur.u, (int)(((last + 1) * runs - 1) / total));
+    } else {
+      // Every group leaves its sums where the scores were, as many heads at a
+      // time as fit, and all threads join them two columns at a time.
+      constexpr int RP = WDS * DT * 16 + 4, ROUND = decode_score_bytes(NT, T) / (GROUPS * RP * 4);
+      static_assert(ROUND >= 1, "a head's sums fit");
+      const int half_d = P.D / 2;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += ROUND) {
+        const int rn = min(ROUND, rows - r0);
+        named_bar_sync(1, N);                      // the scores (the last heads' sums) are read
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (r0 == 0 && wd == 0 && lane % 4 == 0) ml_s[wkey][n * 8 + hq] = make_float2(top[n], sum[n]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = n * 8 + c2 + (j & 1) - r0;
+            if (row < 0 || row >= rn) continue;
+            float* to = scores + (wkey * ROUND + row) * RP + d0 * 16 + hq + (j >> 1) * 8;
+#pragma unroll
+            for (int s = 0; s < DT; ++s)
+              if (s < dn) to[s * 16] = acc[s][n][j];
+          }
+        }
+        named_bar_sync(1, N);
+        for (int x = tid; x < rn * half_d; x += N) {
+          const int r = x / half_d, d = (x - r * half_d) * 2, row = r0 + r;
+          float m = -INFINITY, l = 0.0f;
+#pragma unroll
+          for (int g = 0; g < GROUPS; ++g) m = fmaxf(m, ml_s[g][row].x);
+          const float base = m == -INFINITY ? 0.0f : m;
+          float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int g = 0; g < GROUPS; ++g) {
+            const float2 ml = ml_s[g][row];
+            const float f = ex2_approx(ml.x - base);
+            const float2 v = *reinterpret_cast<const float2*>(scores + (g * ROUND + r) * RP + d);
+            l += f * ml.y;
+            o.x += f * v.x;
+            o.y += f * v.y;
+          }
+          if (whole) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            *reinterpret_cast<uint32_t*>(out + row * P.o_sh + d * 2) = pack2<F16>(o.x * inv, o.y * inv);
+            if (d == 0 && P.lse) lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+          } else {
+            *reinterpret_cast<float2*>(part_o + (int64_t)row * P.D + d) = o;
+            if (d == 0) part_ml[row] = make_float2(m, l);
+          }
+        }
       }
+      named_bar_sync(1, N);                        // before the next pair's scores
+    }
+    if (!done && cur.t == 0 && tid == 0) {
+      // The pair goes on in the next CTAs; its last tile says how far.
+      const long long last = lo + i0 + cur.tiles - 1;
+      P.meta[blockIdx.x] = make_int2(cur.b * pairs + cur.u, (int)(((last + 1) * runs - 1) / total));
     }
     i0 = i1;
     cur.t = cur.tiles - 1;
@@ -740,7 +734,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const DecodeParams P
     if (tid % 32 == 0) red_s[tid / 32] = x;
     __syncthreads();
     x = red_s[0];
-    for (int i = 1; i < (DEC_GRID_MAX + 31) / 32; ++i) x = max ? fmaxf(x, red_s[i]) : x + red_s[i];
+    for (int i = 1; i < JOIN_THREADS / 32; ++i) x = max ? fmaxf(x, red_s[i]) : x + red_s[i];
     return x;
   };
   const float2 ml = tid < n ? P.part_ml[slot_of(tid) * heads + row] : make_float2(-INFINITY, 0.0f);
@@ -799,7 +793,7 @@ ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int gr
   const void* fn = reinterpret_cast<const void*>(&decode_kernel<F16, NT, T>);
   const ffpa_status st = set_smem_attr_once(fn, dev, (int)pl.smem);
   if (st != FFPA_OK) return st;
-  decode_kernel<F16, NT, T><<<grid, (pl.teams * DEC_TEAM + DEC_COPY_WARPS) * 32, pl.smem, stream>>>(P);
+  decode_kernel<F16, NT, T><<<grid, DEC_THREADS, pl.smem, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
   const int heads = 8 * NT;
   const int rows = P.group < heads ? P.group : heads;
@@ -888,7 +882,7 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   int* err = nullptr;
   int sms = 0;
   if ((st = call_status(dev, options, &err, &sms)) != FFPA_OK) return st;
-  const int grid = sms < DEC_GRID_MAX ? sms : DEC_GRID_MAX;
+  const int grid = sms * pl.ctas < DEC_GRID_MAX ? sms * pl.ctas : DEC_GRID_MAX;
 
   DecodeParams P{};
   P.q = static_cast<const char*>(q);

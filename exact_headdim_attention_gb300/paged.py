@@ -72,7 +72,7 @@ def _rope_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, 
     if inv_freq is not None:
         if inv_freq.dtype != torch.float64:
             raise TypeError(f"inv_freq must be float64, got {inv_freq.dtype}")
-        if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 0 < 2 * len(inv_freq) <= D:
+        if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 0 < 2 * inv_freq.shape[0] <= D:
             raise ValueError(f"inv_freq must be contiguous [rot_dim / 2] with rot_dim in 8..{D}")
         if positions is None:
             raise ValueError("a rotation needs positions")
@@ -88,7 +88,7 @@ def _rope_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, 
             shape = tuple(shape)
             raise ValueError(f"positions must have shape {(N,)} or {(B, N)}, got {shape}")
         r.positions, r.position_bits = positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32
-        r.inv_freq, r.rot_dim = inv_freq.data_ptr(), 2 * inv_freq.numel()
+        r.inv_freq, r.rot_dim = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
     if q_weight is not None:
         r.q_weight, r.weight_f32 = _weight_pointer(q_weight, "q_weight", k, D)
     if k_weight is not None:
@@ -267,7 +267,7 @@ def _check_ints(t, name, n, dtype):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or (n is not None and len(t) != n):
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must have shape {('any',) if n is None else (n,)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
