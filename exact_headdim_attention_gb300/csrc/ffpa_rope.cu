@@ -52,9 +52,9 @@ __host__ __device__ constexpr int rope_row_bytes() {   // of one row, for all th
   return ROPE_THREADS * ITER * 2 * VEC * 2;
 }
 
-// Resident blocks an SM.  Two keep the 8-wide vectors' factors and the next
-// item's addresses in registers (append of 16384 tokens at D = 256: 78 us, with
-// three 91); the 4-wide vectors fit three (T16384 D120: 62 us, with two 74).
+// Resident blocks an SM.  The 4-wide vectors fit three (T16384 D120: 62 us, with
+// two 74); more rows on their way than those of two blocks of 8-wide vectors
+// only slow the memory down (T8192 D512: 115 us, with three blocks 123).
 template <int VEC, int ITER>
 __host__ __device__ constexpr int rope_blocks() {
   return VEC == 4 && ITER == 1 ? 3 : 2;
@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
   for (int i = 0; i < 2; ++i)
     if (P.t[i].w)
       for (int d = threadIdx.x; d < P.D; d += ROPE_THREADS) weight_s[i * P.D + d] = one_weight<F16>(P.t[i].w, P.w32, d);
-  load_freqs(P, freq_s);
+  load_freqs<VEC, INTER>(P, freq_s);
+  const int np = P.rot / (2 * VEC);                // rotated chunks
   const int lane = threadIdx.x % LPR;
   const unsigned all = P.items[0] + P.items[1] + P.items_v;
   const unsigned stride = gridDim.x * (ROPE_THREADS / LPR);
@@ -126,20 +127,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
   for (int i = 0; i < ROPE_DEPTH - 1; ++i) issue();
 
   int ring_slot = 0;
-  // The position and slot of an item are asked for while the one before it is worked on.
-  RopeItem next;
-  int64_t next_pos = 0, next_slot = -1;
-  auto ask = [&](unsigned item) {
-    next = rope_item(P, item);
-    if (P.rot && next.which < 2) next_pos = position_of(P, next.b, next.n);
-    if (P.slots && next.which > 0 && next.heads > 0) next_slot = P.slots[next.n];
-  };
-  if (first < all) ask(first + sub);
   for (; first < all; first += stride) {
-    const RopeItem it = next;
-    const int64_t pos = next_pos;
-    int64_t slot = next_slot;
-    if (first + stride < all) ask(first + stride + sub);
+    const RopeItem it = rope_item(P, first + sub);
+    const int64_t pos = P.rot && it.which < 2 ? position_of(P, it.b, it.n) : 0;
+    int64_t slot = P.slots && it.which > 0 && it.heads > 0 ? P.slots[it.n] : -1;
     const RopeTensor& t = P.t[it.wt];
     const bool norm = it.which < 2 && t.w;
     int heads = it.heads;
@@ -182,7 +173,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
         if (ch[k].pair) {
           float c[VEC], s[VEC];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) turn(pos, freq_s[pair_number<VEC, INTER>(ch[k], i)], P.rope_scale, c[i], s[i]);
+          for (int i = 0; i < VEC; ++i) turn(pos, freq_s[i * np + lane + k * LPR], P.rope_scale, c[i], s[i]);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) f1[k][i] = partner<VEC, INTER>(f0[k], i);
 #pragma unroll
@@ -272,11 +263,8 @@ ffpa_status launch_rope_as(const RopeParams& P, bool inter, int sms, int dev, cu
 template <bool F16>
 ffpa_status launch_rope(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t tokens = (int64_t)P.B * P.N;
-  // Heads of an item: up to 8 share a token's sines, fewer where that would leave
-  // SMs without work.
   for (int i = 0; i < 2; ++i) {
-    int per = 8;
-    while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
+    const int per = rope_heads(P.D, P.rot, tokens, P.t[i].H, sms);
     P.chunks[i] = (P.t[i].H + per - 1) / per;
     P.heads_per[i] = (P.t[i].H + P.chunks[i] - 1) / P.chunks[i];
     P.items[i] = P.t[i].x ? (unsigned)(tokens * P.chunks[i]) : 0;

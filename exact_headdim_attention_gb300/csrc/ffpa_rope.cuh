@@ -55,6 +55,17 @@ struct RopeParams {
 
 // The vector width that the pairs' halves and the row's end allow.
 inline int rope_vec(int D, int rot) { return D % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
+// Heads that share a token's cosines and sines: 8 where the rows fill their
+// lanes (a power of two of chunks) and the memory is the bound, 16 where lanes
+// idle and the arithmetic weighs more (T8192 D512: 108 us with 8 and 120 with
+// 16; T8192 D320: 59 and 55; T16384 D120: 58 and 53); fewer where that would leave
+// SMs without work.
+inline int rope_heads(int D, int rot, int64_t tokens, int H, int sms) {
+  const int n = D / (2 * rope_vec(D, rot));
+  int per = (n & (n - 1)) == 0 ? 8 : 16;
+  while (per > 1 && tokens * ((H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
+  return per;
+}
 
 template <int VEC>
 struct RopeChunk {
@@ -126,17 +137,27 @@ __device__ __forceinline__ long long freq_turns(double inv_freq) {
   f -= rint(f);
   return __double2ll_rn(f * 18446744073709551616.0);
 }
-// The call's frequencies in turns, once per block (rot / 2 <= 512 of them).
+// The call's frequencies in turns, once per block (rot / 2 <= 512 of them):
+// that of pair i of chunk j at [i][j], so that the lanes of a row read neighbours.
+template <int VEC, bool INTER>
 __device__ __forceinline__ void load_freqs(const RopeParams& P, long long* freq_s) {
-  for (int i = threadIdx.x; i < P.rot / 2; i += blockDim.x) freq_s[i] = freq_turns(P.inv_freq[i]);
+  const int np = P.rot / (2 * VEC);
+  for (int x = threadIdx.x; x < P.rot / 2; x += blockDim.x) {
+    const int i = x / np, j = x - i * np;
+    freq_s[x] = freq_turns(P.inv_freq[pair_number<VEC, INTER>(rope_chunk<VEC>(j, P.D, P.rot), i)]);
+  }
   __syncthreads();
 }
+// Cosine and sine of position times frequency.  The angle is within [-pi, pi),
+// where __cosf and __sinf are off by at most 2^-21 (the CUDA guide's bounds):
+// 2^-12 and less of the outputs' half steps, for a sixth of sincospif's
+// instructions, which took as long as the rows' own arithmetic.
 __device__ __forceinline__ void turn(long long pos, long long freq, float scale, float& c, float& s) {
   const unsigned long long t = static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(freq);
   const int hi = static_cast<int>(static_cast<unsigned>(t >> 32));   // turns in [-1/2, 1/2), times 2^32
-  sincospif(static_cast<float>(hi) * 4.656612873077393e-10f, &s, &c);   // 2 hi / 2^32
-  c *= scale;
-  s *= scale;
+  const float a = static_cast<float>(hi) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  c = __cosf(a) * scale;
+  s = __sinf(a) * scale;
 }
 
 __device__ __forceinline__ long long position_of(const RopeParams& P, int b, int n) {

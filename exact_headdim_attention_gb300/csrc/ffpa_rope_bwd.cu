@@ -35,7 +35,8 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
   static_assert(RB_DEPTH * ROW >= GROUPS * COLS * 4, "the ring holds a block's sums");
   extern __shared__ __align__(16) char ring[];     // [RB_DEPTH][ITER][g, g, x, x][thread] vectors
   __shared__ long long freq_s[512];
-  load_freqs(P, freq_s);
+  load_freqs<VEC, INTER>(P, freq_s);
+  const int np = P.rot / (2 * VEC);                // rotated chunks
   const int lane = threadIdx.x % LPR, row = threadIdx.x / LPR, sub = threadIdx.x % 32 / LPR;
   const int wt = blockIdx.x < P.blocks[0] ? 0 : 1;
   const int block = blockIdx.x - (wt ? P.blocks[0] : 0);
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
     for (int k = 0; k < ITER; ++k) {
       if (!ch[k].live || !ch[k].pair) continue;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) turn(pos, freq_s[pair_number<VEC, INTER>(ch[k], i)], P.rope_scale, cs[k][i], sn[k][i]);
+      for (int i = 0; i < VEC; ++i) turn(pos, freq_s[i * np + lane + k * LPR], P.rope_scale, cs[k][i], sn[k][i]);
     }
 #pragma unroll 1
     for (int h = 0; h < per; ++h) {
@@ -266,8 +267,7 @@ template <bool F16>
 ffpa_status launch_bwd_rope(RopeParams& P, bool inter, int sms, int dev, cudaStream_t stream) {
   const int64_t tokens = (int64_t)P.B * P.N;
   for (int i = 0; i < 2; ++i) {
-    int per = 16;
-    while (per > 1 && tokens * ((P.t[i].H + per - 1) / per) < (int64_t)sms * 32) per /= 2;
+    const int per = rope_heads(P.D, P.rot, tokens, P.t[i].H, sms);
     P.chunks[i] = (P.t[i].H + per - 1) / per;
     P.heads_per[i] = (P.t[i].H + P.chunks[i] - 1) / P.chunks[i];
     P.items[i] = (unsigned)(tokens * P.chunks[i]);
