@@ -132,12 +132,12 @@ __device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place&
   if (++p.u < pairs) return;
   p.u = 0;
   do {
-    ++p.b;
-    if (p.b >= P.B) {
+    if (p.b + 1 >= P.B) {      // behind the last request: never used (one empty tile)
       p.len = 0;
-      p.tiles = 0;
+      p.tiles = 1;
       return;
     }
+    ++p.b;
     p.len = clamped_len(P, p.b);
   } while (p.len == 0);
   p.tiles = (p.len + T - 1) / T;
@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   __shared__ uint64_t full_k[DEC_RING_MAX], full_v[DEC_RING_MAX], empty_k[DEC_RING_MAX], empty_v[DEC_RING_MAX];
   __shared__ float2 ml_s[GROUPS][HEADS];
   __shared__ long long scan_s[DEC_THREADS / 32 + 1];
-  __shared__ int start_s;
+  __shared__ int start_s[2];
+  __shared__ Place next_s[2];
   __shared__ int abort_flag;
   char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -363,7 +364,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         if (lo < at + tiles * pairs) break;
         at += tiles * pairs;
       }
-      start_s = b;
+      start_s[0] = b;
+      start_s[1] = max(1, clamped_len(P, b));
       scan_s[DEC_THREADS / 32] = lo - at;
     }
     // Requests without keys have no tile: their rows are written here.
@@ -386,8 +388,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
                                   ((c16 ^ i) & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
-    cur.b = start_s;
-    cur.len = clamped_len(P, cur.b);
+    cur.b = start_s[0];
+    cur.len = start_s[1];
     cur.tiles = (cur.len + T - 1) / T;
     const long long r = scan_s[DEC_THREADS / 32];
     cur.u = (int)(r / cur.tiles);
@@ -440,9 +442,17 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   int buf = 0;
   constexpr int N = DEC_WARPS * 32;
 
-  for (int i0 = 0; i0 < n_tiles;) {
+  for (int i0 = 0, turn = 0; i0 < n_tiles; turn ^= 1) {
     // ---- one pair's tiles of this run: [i0, i1)
     const int i1 = min(n_tiles, i0 + cur.tiles - cur.t);
+    // One warp finds the pair after it; the others read that at the pair's end,
+    // behind one barrier at least, so that all warps agree on every pair.
+    if (warp == 0) {
+      Place next = cur;
+      next.t = next.tiles - 1;
+      advance(P, pairs, next, T);
+      if (lane == 0) next_s[turn] = next;
+    }
     const int hk = cur.u / P.head_tiles, ht = cur.u % P.head_tiles;
     const int hq0 = hk * P.group + ht * HEADS;
     const int rows = min(HEADS, P.group - ht * HEADS);
@@ -696,8 +706,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       P.meta[blockIdx.x] = make_int2(cur.b * pairs + cur.u, (int)(((last + 1) * runs - 1) / total));
     }
     i0 = i1;
-    cur.t = cur.tiles - 1;
-    advance(P, pairs, cur, T);
+    cur = next_s[turn];
   }
 }
 

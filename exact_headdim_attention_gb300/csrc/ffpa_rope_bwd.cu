@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
     }
   }
   copy_wait<0>();
+  dependents_launch();
   if (!t.w) return;
   // The block's sums, where the ring was.
   __syncthreads();
@@ -215,6 +216,7 @@ template <bool F16>
 __global__ void __launch_bounds__(1024) weight_sum_kernel(const RopeParams P) {
   const int wt = blockIdx.y;
   if (!P.dw[wt]) return;
+  dependency_wait();
   const int col = threadIdx.x % 32, row = threadIdx.x / 32, d = blockIdx.x * 32 + col;
   __shared__ float sums[32][33];
   float s = 0.0f;
@@ -257,8 +259,20 @@ ffpa_status launch_bwd_as(RopeParams& P, bool inter, int sms, int dev, cudaStrea
   fn<<<grid, RB_THREADS, smem, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
   if (P.dw[0] || P.dw[1]) {
-    weight_sum_kernel<F16><<<dim3((P.D + 31) / 32, 2), 1024, 0, stream>>>(P);
-    if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
+    // A dependent launch: its blocks are set up while the first kernel runs out.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((P.D + 31) / 32, 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, weight_sum_kernel<F16>, P) != cudaSuccess) {
+      cudaGetLastError();
+      return FFPA_ERR_CUDA;
+    }
   }
   return FFPA_OK;
 }

@@ -495,7 +495,8 @@ ffpa_status ffpa_bwd_noalloc(const void* q, const void* k, const void* v, const 
  * h / (Hq / Hkv).
  *
  *   q, o [B, Hq, D] (strides b, h, d); lse [B, Hq] fp32 contiguous or NULL.
- *   block_table: int32 [B, max_pages], rows table_str elements apart.
+ *   block_table: int32 [B, max_pages], rows table_str elements apart.  It and
+ *     seq_lens must not change while the call runs.
  *     Entries at and behind ceil(seq_lens[b] / page_size) are not read.
  *   seq_lens: int32 [B].  A request of length 0 gets o = 0 and lse = -inf.
  *     A negative length counts as 0, one above max_pages * page_size as that;
@@ -532,7 +533,8 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
  * columns from rot_dim on are not rotated.  fp32 arithmetic, rounded once;
  * an angle is off by at most 2^-31 turns and 2^-52 of its size, so positions
  * of millions lose nothing.  Scaled frequencies for long contexts come in through inv_freq and
- * rope_scale.
+ * rope_scale.  inv_freq is finite, and the sum of a row's squares stays in
+ * fp32's range.
  */
 typedef struct ffpa_rope {
   const void* positions;    /* device int32 or int64 [B, N], element strides position_str */
@@ -591,6 +593,7 @@ ffpa_status ffpa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const 
  *   q, q_out [T, Hq, D] (q NULL: there are no queries), k, v [T, Hkv, D],
  *     strides (t, h, d); k_cache, v_cache as above.  rope as above, with
  *     positions [1, T]; rot_dim = 0 and no weights store k as it is.
+ *     The cache must not overlap q, k or v.
  *   slots: int64 [T] contiguous.  A negative slot is padding: nothing is
  *     stored for that token (its queries are computed all the same).  One at or beyond
  *     num_pages * page_size is reported and not stored.  Slots are distinct:
@@ -644,7 +647,8 @@ const char* ffpa_status_string(ffpa_status status);
  * `stream`, then reads and clears the FALLBACK status word of the stream's
  * device (see "Thread safety and shared state" above: the word is shared
  * by every such call on that device, on every stream).  Returns FFPA_OK,
- * FFPA_ERR_DEVICE_TIMEOUT, or FFPA_ERR_CUDA if the synchronisation or the
+ * FFPA_ERR_DEVICE_TIMEOUT, FFPA_ERR_INVALID (a page, slot or length that a
+ * paged-cache call found out of range), or FFPA_ERR_CUDA if the synchronisation or the
  * read failed.
  */
 ffpa_status ffpa_last_device_error(ffpa_stream_t stream);
