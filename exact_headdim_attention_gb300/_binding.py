@@ -44,7 +44,7 @@ class Options(ctypes.Structure):
 
 class Rope(ctypes.Structure):
     """ffpa_rope of include/ffpa.h (norm weights, positions and frequencies of one call)."""
-    _fields_ = [("positions", ctypes.c_void_p), ("position_str", ctypes.c_int64 * 2),
+    _fields_ = [("positions", ctypes.c_void_p), ("position_str_b", ctypes.c_int64), ("position_str_n", ctypes.c_int64),
                 ("position_bits", ctypes.c_int), ("rot_dim", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
                 ("interleaved", ctypes.c_int), ("rope_scale", ctypes.c_float),
                 ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),

@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
 
 // Joins the partial sums of a pair cut between CTAs: block (c, row) the row of
 // the pair that CTA c began, over CTAs c .. last.  Their weights come first (a
-// thread each), then groups of threads add every n-th CTA's sums, with four
+// thread each), then groups of threads add every n-th CTA's sums, with eight
 // loads on the way, and the groups are added in their order.
 constexpr int JOIN_THREADS = 512;
 template <bool F16>
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const DecodeParams P
   float4 a = make_float4(0, 0, 0, 0);
   if (g < groups) {
     const float* from = P.part + row * P.D + col * 4;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = g; i < n; i += groups) {
       const float f = w_s[i];
       const float4 x = *reinterpret_cast<const float4*>(from + slot_of(i) * heads * P.D);

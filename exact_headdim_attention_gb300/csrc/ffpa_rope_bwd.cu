@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const RopeParams P) {
   __shared__ float sums[32][33];
   float s = 0.0f;
   if (d < P.D)
+#pragma unroll 8
     for (int i = row; i < P.blocks[wt]; i += 32) s += P.part[wt][(int64_t)i * P.D + d];
   sums[row][col] = s;
   __syncthreads();

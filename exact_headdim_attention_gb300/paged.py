@@ -80,10 +80,10 @@ def _rope_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, 
             raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
         shape = positions.shape
         if shape == (N,):
-            r.position_str[1] = positions.stride(0)
+            r.position_str_n = positions.stride(0)
         elif shape == (B, N) or shape == (1, N):
-            r.position_str[0] = positions.stride(0) if shape[0] == B else 0
-            r.position_str[1] = positions.stride(1)
+            r.position_str_b = positions.stride(0) if shape[0] == B else 0
+            r.position_str_n = positions.stride(1)
         else:
             shape = tuple(shape)
             raise ValueError(f"positions must have shape {(N,)} or {(B, N)}, got {shape}")
@@ -123,17 +123,12 @@ def _strides(*tensors):
     return keep, [None if x is None else base + x for x in at]
 
 
-def _bhnd(t):
-    """Strides of [B, H, N, D] or packed [T, H, D] rows as (b, h, n, d)."""
-    s = t.stride()
-    return s if len(s) == 4 else (0, s[1], s[0], s[2])
-
-
 def _strides4(*tensors):
     """As _strides, for [B, H, N, D] or packed [T, H, D] rows as (b, h, n, d)."""
     flat = []
     for t in tensors:
-        flat += _bhnd(t)
+        s = t.stride()
+        flat += s if len(s) == 4 else (0, s[1], s[0], s[2])
     keep = (ctypes.c_int64 * len(flat))(*flat)
     base = ctypes.addressof(keep)
     return keep, range(base, base + 32 * len(tensors), 32)
@@ -166,7 +161,7 @@ def _qk_shape(q, k):
 
 def _like(t, out, name):
     if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     _check_buffer(out, name, t.shape, t.dtype, t.device)
     return out
 
@@ -351,10 +346,7 @@ def ffpa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     if rows != B:
         raise ValueError(f"block_table has {rows} rows for {B} requests")
     _check_ints(seq_lens, "seq_lens", B, torch.int32)
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-    else:
-        _check_buffer(out, "out", q.shape, q.dtype, q.device)
+    out = _like(q, out, "out")
     if lse is not None:
         _check_buffer(lse, "lse", (B, Hq), torch.float32, q.device, contiguous=True)
     elif return_lse:

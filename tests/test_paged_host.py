@@ -38,7 +38,7 @@ def decode_call(lib, dt=0, B=2, Hq=4, Hkv=2, D=128, pages=8, page=16, width=4, q
 
 
 def rope_arg(**kw):
-    r = Rope(positions=FAKE, position_str=(ctypes.c_int64 * 2)(0, 1), position_bits=32, rot_dim=64, inv_freq=FAKE,
+    r = Rope(positions=FAKE, position_str_b=0, position_str_n=1, position_bits=32, rot_dim=64, inv_freq=FAKE,
              rope_scale=1.0, q_weight=FAKE, k_weight=FAKE, eps=1e-6)
     for n, x in kw.items():
         setattr(r, n, x)
