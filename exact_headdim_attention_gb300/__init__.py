@@ -1,4 +1,5 @@
-"""Exact scaled-dot-product attention (forward and backward) for large head dimensions on GB300.
+"""Exact scaled-dot-product attention (forward and backward) for large head dimensions on GB300,
+the head norm with rotation before it, and generation over a paged key/value cache.
 
 The compute path is libffpa.so (hand-written sm_103a CUDA kernels behind the
 C ABI in include/ffpa.h); this package only marshals torch tensors into that

@@ -1,6 +1,8 @@
 /*
- * ffpa.h -- C ABI of libffpa: exact scaled-dot-product attention forward for
- * large head dimensions (D = 64..1024) on NVIDIA GB300 (sm_103a).
+ * ffpa.h -- C ABI of libffpa: exact scaled-dot-product attention, forward and
+ * backward, for large head dimensions (D = 64..1024) on NVIDIA GB300 (sm_103a),
+ * with the head norm and rotation before it and a paged key/value cache
+ * behind it.
  *
  * The operation (FFPA API reference, "ffpa_attn.ffpa_attn_func", parameters
  * `query`, `key`, `value`, `attn_mask`, `is_causal`, `scale`, `enable_gqa`
