@@ -46,8 +46,9 @@ namespace {
 constexpr int DEC_WARPS = 8;          // that multiply
 constexpr int DEC_THREADS = (DEC_WARPS + 2) * 32;   // and one each that brings K and V
 constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
-// CTAs of any sm_103 part; the workspace is sized for them without asking a device.
-constexpr int DEC_GRID_MAX = 320;
+// SMs of any sm_103 part; the workspace is sized for them without asking a device.
+constexpr int DEC_SMS_MAX = 160;
+constexpr int DEC_GRID_MAX = 2 * DEC_SMS_MAX;
 
 struct DecodeParams {
   CUtensorMap map_k, map_v;
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         if (lo < at + tiles * pairs) break;
         at += tiles * pairs;
       }
+      b = min(b, P.B - 1);
       start_s[0] = b;
       start_s[1] = max(1, clamped_len(P, b));
       scan_s[DEC_THREADS / 32] = lo - at;
@@ -847,7 +849,8 @@ extern "C" {
 
 size_t ffpa_decode_paged_workspace_bytes(int Hq, int Hkv, int D) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 64 || D > 1024 || D % 8 != 0) return 0;
-  return ffpa::decode_space(ffpa::DEC_GRID_MAX, 8 * ffpa::decode_nt(Hq / Hkv), D).total;
+  const int nt = ffpa::decode_nt(Hq / Hkv);
+  return ffpa::decode_space(ffpa::DEC_SMS_MAX * ffpa::decode_ctas(nt), 8 * nt, D).total;
 }
 
 ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
@@ -879,7 +882,7 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   if (held && (!on_boundary(k_cache, 16) || !on_boundary(v_cache, 16) || !on_boundary(block_table, 4)))
     return FFPA_ERR_INVALID;
   const DecodePlan pl = decode_plan(D, Hq / Hkv);
-  if (workspace_bytes < decode_space(DEC_GRID_MAX, 8 * pl.nt, D).total) return FFPA_ERR_INVALID;
+  if (workspace_bytes < ffpa_decode_paged_workspace_bytes(Hq, Hkv, D)) return FFPA_ERR_INVALID;
   if ((long long)B * Hkv * pl.head_tiles > 0x7fffffffLL) return FFPA_ERR_INVALID;
   int dev = 0;
   ffpa_status st = call_device({q, o, lse, seq_lens, workspace, held ? k_cache : nullptr, held ? v_cache : nullptr,
@@ -891,7 +894,7 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   int* err = nullptr;
   int sms = 0;
   if ((st = call_status(dev, options, &err, &sms)) != FFPA_OK) return st;
-  const int grid = sms * pl.ctas < DEC_GRID_MAX ? sms * pl.ctas : DEC_GRID_MAX;
+  const int grid = (sms < DEC_SMS_MAX ? sms : DEC_SMS_MAX) * pl.ctas;
 
   DecodeParams P{};
   P.q = static_cast<const char*>(q);

@@ -20,8 +20,11 @@ namespace ffpa {
 namespace {
 
 constexpr int RB_THREADS = 256;
-constexpr int RB_DEPTH = 3;
 constexpr int RB_BLOCKS_MAX = 512;   // blocks of queries and keys together
+
+// Rows of the ring: more than three slow the one block of D > 512 down (T4096
+// D1024: 112 us, with four 115), four are best elsewhere.
+__host__ __device__ constexpr int rb_depth(int iter) { return iter == 1 ? 4 : 3; }
 
 template <int VEC, int ITER>
 __host__ __device__ constexpr int rb_row_bytes() {     // of one row and its gradient, for all threads of a block
@@ -31,7 +34,7 @@ __host__ __device__ constexpr int rb_row_bytes() {     // of one row and its gra
 template <bool F16, int VEC, int LPR, int ITER, bool INTER>
 __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel(const __grid_constant__ RopeParams P) {
   constexpr int GROUPS = RB_THREADS / LPR, COLS = LPR * 2 * VEC * ITER;
-  constexpr int ROW = rb_row_bytes<VEC, ITER>(), PIECE = RB_THREADS * VEC * 2;
+  constexpr int ROW = rb_row_bytes<VEC, ITER>(), PIECE = RB_THREADS * VEC * 2, RB_DEPTH = rb_depth(ITER);
   static_assert(RB_DEPTH * ROW >= GROUPS * COLS * 4, "the ring holds a block's sums");
   extern __shared__ __align__(16) char ring[];     // [RB_DEPTH][ITER][g, g, x, x][thread] vectors
   __shared__ long long freq_s[512];
@@ -169,17 +172,19 @@ __global__ void __launch_bounds__(RB_THREADS, ITER == 1 ? 2 : 1) rope_bwd_kernel
       }
       if (!on) continue;
       const float r = rsqrtf(sq * inv_d + P.eps);
-      const float back = r * r * dot * inv_d;      // r mean(w g' xn)
+      const float back = -r * dot * inv_d * r * r; // dx = (r g') w + back x
 #pragma unroll
       for (int k = 0; k < ITER; ++k) {
         if (!ch[k].live) continue;
         if (t.w) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
-            dw[k][i].x += g[k][i].x * (x[k][i].x * r);
-            dw[k][i].y += g[k][i].y * (x[k][i].y * r);
-            g[k][i].x = r * (w[k][i].x * g[k][i].x - x[k][i].x * back);
-            g[k][i].y = r * (w[k][i].y * g[k][i].y - x[k][i].y * back);
+            g[k][i].x *= r;
+            g[k][i].y *= r;
+            dw[k][i].x += g[k][i].x * x[k][i].x;
+            dw[k][i].y += g[k][i].y * x[k][i].y;
+            g[k][i].x = g[k][i].x * w[k][i].x + back * x[k][i].x;
+            g[k][i].y = g[k][i].y * w[k][i].y + back * x[k][i].y;
           }
         }
         *reinterpret_cast<Raw<VEC>*>(to + ch[k].a * 2) = narrow<F16, VEC>(g[k]);
@@ -253,7 +258,7 @@ ffpa_status launch_bwd_as(RopeParams& P, bool inter, int sms, int dev, cudaStrea
   }
   P.part[1] = P.part[0] + (int64_t)P.blocks[0] * P.D;
   const int grid = P.blocks[0] + P.blocks[1];
-  const int smem = RB_DEPTH * rb_row_bytes<VEC, ITER>();
+  const int smem = rb_depth(ITER) * rb_row_bytes<VEC, ITER>();
   auto fn = inter ? &rope_bwd_kernel<F16, VEC, LPR, ITER, true> : &rope_bwd_kernel<F16, VEC, LPR, ITER, false>;
   const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(fn), dev, smem);
   if (st != FFPA_OK) return st;
