@@ -1,4 +1,5 @@
-"""Compile libffpa.so (the CUDA kernels and their C ABI) in-tree for sm_103a.
+"""Compile libffpa.so (the CUDA kernels and their C ABI) in-tree for sm_103a, and the
+module that marshals torch tensors into the paged-cache calls (host C++).
 
     python -m exact_headdim_attention_gb300.build [--force]
 
@@ -28,6 +29,30 @@ DEPS = SOURCES + [CSRC / "ffpa_paged.cuh", CSRC / "ffpa_rope.cuh", CSRC / "ffpa_
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
+BINDING = CSRC / "paged_binding.cpp"
+
+
+def binding_path() -> Path:
+    """The marshalling module of this interpreter and torch (their C++ interfaces are compiled in)."""
+    import torch
+    tag = f"cp{sys.version_info[0]}{sys.version_info[1]}-torch{torch.__version__.replace('+', '-')}"
+    return OUT.parent / f"ffpa_paged_binding.{tag}.so"
+
+
+def binding_command(out: Path) -> list[str]:
+    import sysconfig
+
+    import torch
+    t = Path(torch.__file__).resolve().parent
+    cuda = Path(nvcc()).resolve().parent.parent
+    inc = [t / "include", t / "include" / "torch" / "csrc" / "api" / "include",
+           Path(sysconfig.get_paths()["include"]), cuda / "include"]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(x for i in inc for x in ("-isystem", str(i))), f"-I{INCLUDE}", str(BINDING), "-o", str(out),
+            f"-L{t / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def nvcc() -> str:
     cand = os.environ.get("NVCC") or "/usr/local/cuda/bin/nvcc"
     return cand if Path(cand).exists() else "nvcc"
@@ -39,7 +64,9 @@ def flags() -> list[str]:
 
 
 def stale() -> bool:
-    if not OUT.exists():
+    if not OUT.exists() or not binding_path().exists():
+        return True
+    if any(p.stat().st_mtime > binding_path().stat().st_mtime for p in (BINDING, INCLUDE / "ffpa.h")):
         return True
     t = OUT.stat().st_mtime
     return any(p.stat().st_mtime > t for p in DEPS)
@@ -52,6 +79,9 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     objdir.mkdir(parents=True, exist_ok=True)
     jobs = [[nvcc(), *flags(), "-c", str(src), "-o", str(objdir / (src.stem + ".o"))]
             for src in SOURCES]
+    module = binding_path()
+    module_tmp = module.with_suffix(".so.tmp")
+    jobs.append(binding_command(module_tmp))
     if verbose:
         for cmd in jobs:
             print(" ".join(cmd))
@@ -67,6 +97,7 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     if verbose:
         print(" ".join(link))
     subprocess.run(link, check=True)
+    os.replace(module_tmp, module)
     os.replace(tmp, OUT)
     return OUT
 
