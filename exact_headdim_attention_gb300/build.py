@@ -50,7 +50,7 @@ def binding_command(out: Path) -> list[str]:
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *(x for i in inc for x in ("-isystem", str(i))), f"-I{INCLUDE}", str(BINDING), "-o", str(out),
-            f"-L{t / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            f"-L{t / 'lib'}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def nvcc() -> str:
