@@ -48,7 +48,6 @@ constexpr int DEC_THREADS = (DEC_WARPS + 2) * 32;   // and one each that brings 
 constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
 // SMs of any sm_103 part; the workspace is sized for them without asking a device.
 constexpr int DEC_SMS_MAX = 160;
-constexpr int DEC_GRID_MAX = 2 * DEC_SMS_MAX;
 
 struct DecodeParams {
   CUtensorMap map_k, map_v;
@@ -59,7 +58,8 @@ struct DecodeParams {
   const int32_t* lens;
   float* part;      // [2 grid][8 NT][D] unnormalised partial outputs
   float2* part_ml;  // [2 grid][8 NT] (maximum in log2 units, sum)
-  int2* meta;       // [grid] (pair cut behind CTA c or -1, last CTA of that pair)
+  int4* cuts;       // [grid][2] the pairs that CTA c shares with earlier and with later CTAs:
+                    // (first CTA + 65536 x CTAs or 0, heads, request, first head)
   int* err;
   int64_t q_sb, q_sh, o_sb, o_sh;       // bytes
   int64_t k_sp, k_ss, k_sh, v_sp, v_ss, v_sh;
@@ -107,8 +107,9 @@ DecodePlan decode_plan(int D, int group) {
   p.chunks = (D + 63) / 64;
   const size_t fixed = decode_score_bytes(p.nt, p.tile);
   const size_t stage = (size_t)p.tile * p.chunks * 128;
-  // 4 KB a CTA stay for static shared memory, the alignment of the boxes and the system.
-  int n = static_cast<int>((SMEM_LIMIT / p.ctas - 4096 - fixed) / stage);
+  // 8 KB a CTA stay for static shared memory, the alignment of the boxes, the system,
+  // and a block of the joining kernel that is set up early (with 4 KB left 1 us more).
+  int n = static_cast<int>((SMEM_LIMIT / p.ctas - 8192 - fixed) / stage);
   if (n > 2 * DEC_RING_MAX) n = 2 * DEC_RING_MAX;
   p.ring_v = n / 2;
   p.ring_k = n - n / 2;
@@ -144,6 +145,24 @@ __device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place&
   p.tiles = (p.len + T - 1) / T;
 }
 
+// A run [lo, lo + n) of the line's `total` tiles, which are dealt to `runs` CTAs.
+struct Run {
+  long long lo, total, runs;
+  int n;
+  __device__ __forceinline__ int cta_of(long long tile) const { return (int)(((tile + 1) * runs - 1) / total); }
+};
+
+// Notes for the joining kernel that the pair of the run's tile i, the first one
+// here, goes over several CTAs.
+__device__ __forceinline__ void note_cut(const DecodeParams& P, const Place& p, const Run& run, int i, int heads) {
+  const int side = p.t == 0;
+  if (side ? i + p.tiles <= run.n : i != 0) return;
+  const long long begin = run.lo + i - p.t;
+  const int first = run.cta_of(begin), n = run.cta_of(begin + p.tiles - 1) - first + 1;
+  const int hk = p.u / P.head_tiles, ht = p.u % P.head_tiles;
+  P.cuts[2 * blockIdx.x + side] = make_int4(first + (n << 16), min(heads, P.group - ht * heads), p.b, hk * P.group + ht * heads);
+}
+
 // A whole warp's bounded wait; false for all its lanes when the limit expired for one.
 __device__ __forceinline__ bool all_waited(uint32_t bar, uint32_t parity, const DecodeParams& P, volatile int* abort_flag) {
   return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag, P.timeout_ns, P.err));
@@ -152,9 +171,9 @@ __device__ __forceinline__ bool all_waited(uint32_t bar, uint32_t parity, const 
 // K (or V) tiles of the run as tensor boxes, a box a lane, its page looked up
 // one tile ahead.  A page that does not exist, and rows that belong to no key,
 // have a coordinate behind the last page: the copy writes zeros there.
-__device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, bool is_v, Place at, int n_tiles, uint32_t ring,
-                                              int slots, uint64_t* full, uint64_t* empty, volatile int* abort_flag) {
-  const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles;
+__device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int heads, bool is_v, Place at, const Run& run,
+                                              uint32_t ring, int slots, uint64_t* full, uint64_t* empty, volatile int* abort_flag) {
+  const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles, n_tiles = run.n;
   const CUtensorMap* map = is_v ? &P.map_v : &P.map_k;
   const int per_row = P.chunks / P.box_chunks;          // boxes side by side (at most 32 boxes a tile)
   const int row = lane / per_row * P.box_rows, chunk = lane % per_row;
@@ -181,6 +200,7 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, bool
     const bool good = page >= 0 && page < P.num_pages;
     if (keyed && !good) report_invalid(P.err);
     const int y = good ? in_page : 0, z = good ? page : P.num_pages;
+    if (is_v && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
     advance(P, pairs, at, T);
     if (i + 1 < n_tiles) look_up(at);
     if (!all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) || P.drop) break;
@@ -215,10 +235,10 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, bool
 // one tile ahead, and copies them in pieces of 16 bytes, a power of two of
 // lanes to a row.  A row without a key, or of a page that does not exist,
 // becomes zeros.
-__device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, bool is_v, Place at, int n_tiles,
-                                               uint32_t ring, int slots, uint64_t* full, uint64_t* empty,
+__device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int heads, bool is_v, Place at,
+                                               const Run& run, uint32_t ring, int slots, uint64_t* full, uint64_t* empty,
                                                volatile int* abort_flag) {
-  const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles;
+  const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles, n_tiles = run.n;
   const int cpr = P.D / 8;                         // pieces of a row
   int wide = 8;                                    // lanes of a row
   while (wide < cpr && wide < 32) wide *= 2;
@@ -254,6 +274,7 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, boo
           report_invalid(P.err);
       }
     }
+    if (is_v && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
     advance(P, pairs, at, T);
     if (i + 1 < n_tiles) look_up(at);
     if (!all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) || P.drop) break;
@@ -343,7 +364,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         mbar_init(smem_u32(empty_v + i), DEC_WARPS);
       }
       fence_mbar_init();
-      P.meta[blockIdx.x] = make_int2(-1, 0);
+      P.cuts[2 * blockIdx.x] = P.cuts[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
     long long before = 0;
@@ -408,15 +429,15 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     uint64_t *full = is_v ? full_v : full_k, *empty = is_v ? empty_v : empty_k;
     const uint32_t ring = is_v ? ring_v : ring_k;
     const int slots = is_v ? P.ring_v : P.ring_k;
+    const Run run{lo, total, total < gridDim.x ? total : gridDim.x, n_tiles};
     if (P.boxed)
-      produce_boxes(P, T, is_v, cur, n_tiles, ring, slots, full, empty, &abort_flag);
+      produce_boxes(P, T, HEADS, is_v, cur, run, ring, slots, full, empty, &abort_flag);
     else
-      produce_pieces(P, T, is_v, cur, n_tiles, ring, slots, full, empty, &abort_flag);
+      produce_pieces(P, T, HEADS, is_v, cur, run, ring, slots, full, empty, &abort_flag);
     return;
   }
 
   // ---- the computing warps
-  const long long runs = total < gridDim.x ? total : gridDim.x;
   const int ksteps = (P.D + 15) / 16;
   // Shares of D are whole chunks, so that a chunk's swizzle is a constant of the code.
   const int part = warp / MT;                        // in the first product (0 when a warp has two key tiles)
@@ -702,100 +723,129 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       }
       named_bar_sync(1, N);                        // before the next pair's scores
     }
-    if (!done && cur.t == 0 && tid == 0) {
-      // The pair goes on in the next CTAs; its last tile says how far.
-      const long long last = lo + i0 + cur.tiles - 1;
-      P.meta[blockIdx.x] = make_int2(cur.b * pairs + cur.u, (int)(((last + 1) * runs - 1) / total));
-    }
     i0 = i1;
     cur = next_s[turn];
   }
 }
 
-// Joins the partial sums of a pair cut between CTAs: block (c, row) the row of
-// the pair that CTA c began, over CTAs c .. last.  Their weights come first (a
-// thread each), then groups of threads add every n-th CTA's sums, with eight
-// loads on the way, and the groups are added in their order.
-constexpr int JOIN_THREADS = 512;
-template <bool F16>
-__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const DecodeParams P, int heads) {
-  __shared__ float4 acc_s[JOIN_THREADS];
-  __shared__ float w_s[DEC_GRID_MAX];
-  __shared__ float red_s[JOIN_THREADS / 32];
-  dependency_wait();
-  const int2 m = P.meta[blockIdx.x];
-  if (m.x < 0) return;
-  const int pairs = P.Hkv * P.head_tiles;
-  const int b = m.x / pairs, u = m.x % pairs, row = blockIdx.y;
-  const int hk = u / P.head_tiles, ht = u % P.head_tiles;
-  if (row >= P.group - ht * heads) return;
-  const int hq = hk * P.group + ht * heads + row;
-  const int n = m.y - blockIdx.x + 1;              // at most DEC_GRID_MAX
-  const int tid = threadIdx.x;
-  // The first CTA's sums are its second partial pair, the others' their first.
-  const int64_t first = 2 * (int64_t)blockIdx.x + 1;
-  auto slot_of = [&](int i) { return i == 0 ? first : first - 1 + 2 * i; };
-  auto reduce = [&](float x, bool max) {           // over the block, in a fixed tree
+// Joins the partial sums of the pairs cut between CTAs.  A pair over n CTAs is
+// joined by n blocks, one for each of its CTAs, 128 columns of a head at a time:
+// by a warp each where n is small (most often 2), by the warps of a block, a
+// share of the CTAs each, where it is large.  The order of the sums is fixed.
+// The kernel is one chain of latencies (the cut, the sums, the store), so it has
+// no division and no sum over lanes: 2 us of one request of 777 keys, against 4 us
+// for a block of 512 threads a head, and 2 to 3 us of batches of 110 requests,
+// against 4 to 7 us.  With a warp for up to 16 CTAs, 5 requests of 104 keys, 16
+// heads of 1024, take 18.3 us, with up to 4 CTAs 22.7 us; for up to 32 CTAs the
+// request of 777 keys takes 11.7 us in place of 9.3.
+constexpr int JOIN_WARPS = 8, JOIN_FEW = 16;
+
+struct Joined {
+  float top, l;
+  float4 a;
+  __device__ __forceinline__ void rescale(float t) {
+    const float f = ex2_approx(top - (t == -INFINITY ? 0.0f : t));
+    top = t;
+    l *= f;
+    a.x *= f;
+    a.y *= f;
+    a.z *= f;
+    a.w *= f;
+  }
+  __device__ __forceinline__ void add(float2 ml, const float4& x) {   // (behind rescale)
+    const float f = ex2_approx(ml.x - (top == -INFINITY ? 0.0f : top));
+    l += f * ml.y;
+    a.x += f * x.x;
+    a.y += f * x.y;
+    a.z += f * x.z;
+    a.w += f * x.w;
+  }
+};
+
+// Sums i, i + stride, .. of the pair, at most N below n, heads rows apart.
+// The first CTA's sums are its second partial pair, the others' their first.
+template <int N>
+__device__ __forceinline__ void join_add(Joined& s, const float2* mls, const float* from, int heads, int D, int i, int stride, int n) {
+  mls += (2 * i + (i == 0)) * heads;
+  from += (2 * i + (i == 0)) * heads * D;
+  const int step = 2 * stride * heads, first = i == 0 ? heads : 0;
+  float2 ml[N];
+  float4 x[N];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const float y = __shfl_xor_sync(~0u, x, d);
-      x = max ? fmaxf(x, y) : x + y;
-    }
-    __syncthreads();
-    if (tid % 32 == 0) red_s[tid / 32] = x;
-    __syncthreads();
-    x = red_s[0];
-    for (int i = 1; i < JOIN_THREADS / 32; ++i) x = max ? fmaxf(x, red_s[i]) : x + red_s[i];
-    return x;
-  };
-  const float2 ml = tid < n ? P.part_ml[slot_of(tid) * heads + row] : make_float2(-INFINITY, 0.0f);
-  const float top = reduce(ml.x, true);
-  const float w = ex2_approx(ml.x - (top == -INFINITY ? 0.0f : top));
-  if (tid < n) w_s[tid] = w;
-  const float l = reduce(w * ml.y, false);         // (also: the weights are written)
-  const int cols = P.D / 4;                        // float4 columns
-  const int groups = JOIN_THREADS / cols;          // at least 2 (D <= 1024)
-  const int g = tid / cols, col = tid % cols;
-  float4 a = make_float4(0, 0, 0, 0);
-  if (g < groups) {
-    const float* from = P.part + row * P.D + col * 4;
-#pragma unroll 8
-    for (int i = g; i < n; i += groups) {
-      const float f = w_s[i];
-      const float4 x = *reinterpret_cast<const float4*>(from + slot_of(i) * heads * P.D);
-      a.x += f * x.x;
-      a.y += f * x.y;
-      a.z += f * x.z;
-      a.w += f * x.w;
+  for (int k = 0; k < N; ++k) {
+    ml[k] = make_float2(-INFINITY, 0.0f);
+    x[k] = make_float4(0, 0, 0, 0);
+    if (i + k * stride < n) {
+      const int at = k == 0 ? 0 : k * step - first;
+      ml[k] = mls[at];
+      x[k] = *reinterpret_cast<const float4*>(from + at * D);
     }
   }
-  acc_s[tid] = a;
-  __syncthreads();
-  if (g != 0) return;
-  for (int i = 1; i < groups; ++i) {
-    const float4 x = acc_s[i * cols + col];
-    a.x += x.x;
-    a.y += x.y;
-    a.z += x.z;
-    a.w += x.w;
+  float t = s.top;
+#pragma unroll
+  for (int k = 0; k < N; ++k) t = fmaxf(t, ml[k].x);
+  s.rescale(t);
+#pragma unroll
+  for (int k = 0; k < N; ++k) s.add(ml[k], x[k]);
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 4) join_kernel(const __grid_constant__ DecodeParams P, int heads, int log_rows) {
+  __shared__ float4 acc_s[JOIN_WARPS][32];
+  __shared__ float2 ml_s[JOIN_WARPS];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int tasks = (P.D + 127) / 128 << log_rows;
+  dependency_wait();
+  const int4 m = P.cuts[blockIdx.x];
+  const int n = m.x >> 16, first = m.x & 0xffff;   // CTAs of the pair
+  if (n == 0) return;
+  const bool few = n <= JOIN_FEW;
+  const int mine = blockIdx.x / 2 - first;
+  for (int task = few ? mine * JOIN_WARPS + warp : mine; task < tasks; task += few ? n * JOIN_WARPS : n) {
+    const int row = task & ((1 << log_rows) - 1), col = (task >> log_rows) * 128 + lane * 4;
+    if (row >= m.y) continue;
+    const float2* mls = P.part_ml + 2 * first * heads + row;
+    const float* from = P.part + (int64_t)(2 * first * heads + row) * P.D + min(col, P.D - 4);
+    Joined s{-INFINITY, 0.0f, make_float4(0, 0, 0, 0)};
+    if (n == 2) {
+      join_add<2>(s, mls, from, heads, P.D, 0, 1, n);
+    } else if (few) {
+      for (int i = 0; i < n; i += 4) join_add<4>(s, mls, from, heads, P.D, i, 1, n);
+    } else {
+      for (int i = warp; i < n; i += 4 * JOIN_WARPS) join_add<4>(s, mls, from, heads, P.D, i, JOIN_WARPS, n);
+      acc_s[warp][lane] = s.a;
+      if (lane == 0) ml_s[warp] = make_float2(s.top, s.l);
+      __syncthreads();
+      if (warp == 0) {
+        float t = s.top;
+        for (int w = 1; w < JOIN_WARPS; ++w) t = fmaxf(t, ml_s[w].x);
+        s.rescale(t);
+        for (int w = 1; w < JOIN_WARPS; ++w) s.add(ml_s[w], acc_s[w][lane]);
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    const int64_t hq = m.w + row;
+    const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+    if (col < P.D)
+      *reinterpret_cast<uint2*>(P.o + m.z * P.o_sb + hq * P.o_sh + col * 2) =
+          make_uint2(pack2<F16>(s.a.x * inv, s.a.y * inv), pack2<F16>(s.a.z * inv, s.a.w * inv));
+    if (P.lse && col == 0)
+      P.lse[(int64_t)m.z * P.Hq + hq] = s.l == 0.0f ? -INFINITY : (s.top + log2f(s.l)) * 0.69314718055994531f;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  *reinterpret_cast<uint2*>(P.o + b * P.o_sb + (int64_t)hq * P.o_sh + col * 8) =
-      make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-  if (P.lse && col == 0) P.lse[(int64_t)b * P.Hq + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
 }
 
 // Workspace: partial outputs, their maxima and sums, the cut pairs.
 struct DecodeSpace {
-  size_t part, ml, meta, total;
+  size_t part, ml, cuts, total;
 };
 DecodeSpace decode_space(int grid, int heads, int D) {
   DecodeSpace s;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   s.part = 0;
   s.ml = up((size_t)2 * grid * heads * D * 4);
-  s.meta = s.ml + up((size_t)2 * grid * heads * 8);
-  s.total = s.meta + up((size_t)grid * 8);
+  s.cuts = s.ml + up((size_t)2 * grid * heads * 8);
+  s.total = s.cuts + up((size_t)2 * grid * sizeof(int4));
   return s;
 }
 
@@ -807,18 +857,19 @@ ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int gr
   decode_kernel<F16, NT, T><<<grid, DEC_THREADS, pl.smem, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
   const int heads = 8 * NT;
-  const int rows = P.group < heads ? P.group : heads;
+  int log_rows = 0;
+  while ((1 << log_rows) < (P.group < heads ? P.group : heads)) ++log_rows;
   // A dependent launch: its blocks are set up while the first kernel runs out.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, rows);
-  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.gridDim = dim3(2 * grid);
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<F16>, P, heads) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, join_kernel<F16>, P, heads, log_rows) != cudaSuccess) {
     cudaGetLastError();
     return FFPA_ERR_CUDA;
   }
@@ -908,7 +959,7 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   char* ws = static_cast<char*>(workspace);
   P.part = reinterpret_cast<float*>(ws + sp.part);
   P.part_ml = reinterpret_cast<float2*>(ws + sp.ml);
-  P.meta = reinterpret_cast<int2*>(ws + sp.meta);
+  P.cuts = reinterpret_cast<int4*>(ws + sp.cuts);
   P.err = err;
   P.q_sb = q_str[0] * 2;
   P.q_sh = q_str[1] * 2;
