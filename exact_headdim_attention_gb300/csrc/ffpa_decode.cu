@@ -309,6 +309,32 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int
   copy_wait_all();
 }
 
+// Two column tiles of 8 heads, as the second product leaves them (a lane holds
+// heads c, c + 1 of columns r and r + 8 of a tile, c = lane % 4 * 2, r = lane / 4),
+// times f0 and f1, become 64 bytes of each head: 8 x 8 transpositions, then one of
+// pieces among four lanes, and 16 bytes a lane.  (Written as they lie, two bytes at a
+// time, the output took 3 us of a pair of D = 1024.)
+template <bool F16>
+__device__ __forceinline__ void write_columns(char* out, int64_t o_sh, int heads, int d0, int D, const float (&a)[4],
+                                              const float (&b)[4], float f0, float f1) {
+  const int q = threadIdx.x % 4, head = threadIdx.x % 32 / 4, d = d0 + q * 8;
+  uint32_t r0 = transpose8(pack2<F16>(a[0] * f0, a[1] * f1)), r1 = transpose8(pack2<F16>(a[2] * f0, a[3] * f1));
+  uint32_t r2 = transpose8(pack2<F16>(b[0] * f0, b[1] * f1)), r3 = transpose8(pack2<F16>(b[2] * f0, b[3] * f1));
+  auto trade = [&](uint32_t& x, uint32_t& y, int mask) {   // y of the lower lane for x of the upper
+    const bool up = q & mask;
+    const uint32_t got = __shfl_xor_sync(~0u, up ? x : y, mask);
+    if (up)
+      x = got;
+    else
+      y = got;
+  };
+  trade(r0, r1, 1);
+  trade(r2, r3, 1);
+  trade(r0, r2, 2);
+  trade(r1, r3, 2);
+  if (head < heads && d < D) *reinterpret_cast<uint4*>(out + head * o_sh + d * 2) = make_uint4(r0, r1, r2, r3);
+}
+
 template <bool F16, int NT, int T>
 __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(const __grid_constant__ DecodeParams P) {
   constexpr int HEADS = 8 * NT, THREADS = DEC_THREADS;
@@ -647,20 +673,23 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     if (GROUPS == 1) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float inv = whole ? (sum[n] == 0.0f ? 0.0f : 1.0f / sum[n]) : 1.0f;
+        if (whole) {
+          const float inv = sum[n] == 0.0f ? 0.0f : 1.0f / sum[n];
+          const float f0 = __shfl_sync(~0u, inv, c2 * 4), f1 = __shfl_sync(~0u, inv, c2 * 4 + 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int head = n * 8 + c2 + (j & 1);
-          const float f = __shfl_sync(~0u, inv, c2 * 4 + (j & 1) * 4);
-          if (head >= rows) continue;
+          for (int s = 0; s < DT; s += 2)
+            if (s < dn)
+              write_columns<F16>(out + n * 8 * P.o_sh, P.o_sh, rows - n * 8, (d0 + s) * 16, P.D, acc[s][n], acc[s + 1][n], f0, f1);
+        } else {
 #pragma unroll
-          for (int s = 0; s < DT; ++s) {
-            const int d = (d0 + s) * 16 + hq + (j >> 1) * 8;
-            if (s >= dn || d >= P.D) continue;
-            if (whole)
-              store16<F16>(out + head * P.o_sh + d * 2, acc[s][n][j] * f);
-            else
-              part_o[(int64_t)head * P.D + d] = acc[s][n][j];
+          for (int j = 0; j < 4; ++j) {
+            const int head = n * 8 + c2 + (j & 1), d = d0 * 16 + (j >> 1) * 8;
+            const int some = (P.D - d + 8) / 16;       // column tiles with these 8 columns
+            if (head >= rows) continue;
+            float* to = part_o + head * P.D + d + hq;
+#pragma unroll
+            for (int s = 0; s < DT; ++s)
+              if (s < some) to[s * 16] = acc[s][n][j];
           }
         }
         const int head = n * 8 + hq;

@@ -114,6 +114,14 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], con
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// Transposes an 8 x 8 matrix of 16-bit values, of which lane i holds row i / 4,
+// columns i % 4 * 2 and the next.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Dependent launch: let the next kernel of the stream start its blocks, and
 // wait (in that kernel) until this one's memory is visible.
 __device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
