@@ -122,9 +122,8 @@ struct Place {
   int b, u, t, tiles, len;
 };
 
-__device__ __forceinline__ int clamped_len(const DecodeParams& P, int b) {
+__device__ __forceinline__ int clamped_len(const DecodeParams& P, int n) {
   const long long cap = (long long)P.max_pages * P.page_size;
-  const int n = P.lens[b];
   return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
 
@@ -140,7 +139,7 @@ __device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place&
       return;
     }
     ++p.b;
-    p.len = clamped_len(P, p.b);
+    p.len = clamped_len(P, P.lens[p.b]);
   } while (p.len == 0);
   p.tiles = (p.len + T - 1) / T;
 }
@@ -166,6 +165,16 @@ __device__ __forceinline__ void note_cut(const DecodeParams& P, const Place& p, 
 // A whole warp's bounded wait; false for all its lanes when the limit expired for one.
 __device__ __forceinline__ bool all_waited(uint32_t bar, uint32_t parity, const DecodeParams& P, volatile int* abort_flag) {
   return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag, P.timeout_ns, P.err));
+}
+
+// The queries of the next pair on their way to L2, when its first values are asked
+// for: read by the pair itself they came 1 us late (B110 D512 of 1 to 87 keys 27.4 us
+// in place of 26.4).
+__device__ __forceinline__ void fetch_queries(const DecodeParams& P, const Place& p, int heads) {
+  const int hk = p.u / P.head_tiles, ht = p.u % P.head_tiles;
+  const int rows = min(heads, P.group - ht * heads), lines = (P.D * 2 + 127) / 128;
+  const char* q = P.q + p.b * P.q_sb + (int64_t)(hk * P.group + ht * heads) * P.q_sh;
+  for (int x = threadIdx.x % 32; x < rows * lines; x += 32) fetch_l2(q + x / lines * P.q_sh + x % lines * 128);
 }
 
 // K (or V) tiles of the run as tensor boxes, a box a lane, its page looked up
@@ -202,7 +211,10 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     const int y = good ? in_page : 0, z = good ? page : P.num_pages;
     if (is_v && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
     advance(P, pairs, at, T);
-    if (i + 1 < n_tiles) look_up(at);
+    if (i + 1 < n_tiles) {
+      look_up(at);
+      if (is_v && at.t == 0) fetch_queries(P, at, heads);
+    }
     if (!all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) || P.drop) break;
     const uint32_t bar = smem_u32(full + slot);
     if (lane == 0) mbar_arrive_expect_tx(bar, stage);
@@ -276,7 +288,10 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int
     }
     if (is_v && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
     advance(P, pairs, at, T);
-    if (i + 1 < n_tiles) look_up(at);
+    if (i + 1 < n_tiles) {
+      look_up(at);
+      if (is_v && at.t == 0) fetch_queries(P, at, heads);
+    }
     if (!all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) || P.drop) break;
     const uint32_t tile = ring + slot * stage;
 #pragma unroll
@@ -309,6 +324,23 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int
   copy_wait_all();
 }
 
+// Word i of lane q of each four lanes becomes word q of lane i.
+__device__ __forceinline__ void trade_words(uint32_t (&r)[4]) {
+  const int q = threadIdx.x % 4;
+  auto trade = [&](uint32_t& x, uint32_t& y, int mask) {   // y of the lower lane for x of the upper
+    const bool up = q & mask;
+    const uint32_t got = __shfl_xor_sync(~0u, up ? x : y, mask);
+    if (up)
+      x = got;
+    else
+      y = got;
+  };
+  trade(r[0], r[1], 1);
+  trade(r[2], r[3], 1);
+  trade(r[0], r[2], 2);
+  trade(r[1], r[3], 2);
+}
+
 // Two column tiles of 8 heads, as the second product leaves them (a lane holds
 // heads c, c + 1 of columns r and r + 8 of a tile, c = lane % 4 * 2, r = lane / 4),
 // times f0 and f1, become 64 bytes of each head: 8 x 8 transpositions, then one of
@@ -318,21 +350,10 @@ template <bool F16>
 __device__ __forceinline__ void write_columns(char* out, int64_t o_sh, int heads, int d0, int D, const float (&a)[4],
                                               const float (&b)[4], float f0, float f1) {
   const int q = threadIdx.x % 4, head = threadIdx.x % 32 / 4, d = d0 + q * 8;
-  uint32_t r0 = transpose8(pack2<F16>(a[0] * f0, a[1] * f1)), r1 = transpose8(pack2<F16>(a[2] * f0, a[3] * f1));
-  uint32_t r2 = transpose8(pack2<F16>(b[0] * f0, b[1] * f1)), r3 = transpose8(pack2<F16>(b[2] * f0, b[3] * f1));
-  auto trade = [&](uint32_t& x, uint32_t& y, int mask) {   // y of the lower lane for x of the upper
-    const bool up = q & mask;
-    const uint32_t got = __shfl_xor_sync(~0u, up ? x : y, mask);
-    if (up)
-      x = got;
-    else
-      y = got;
-  };
-  trade(r0, r1, 1);
-  trade(r2, r3, 1);
-  trade(r0, r2, 2);
-  trade(r1, r3, 2);
-  if (head < heads && d < D) *reinterpret_cast<uint4*>(out + head * o_sh + d * 2) = make_uint4(r0, r1, r2, r3);
+  uint32_t r[4] = {transpose8(pack2<F16>(a[0] * f0, a[1] * f1)), transpose8(pack2<F16>(a[2] * f0, a[3] * f1)),
+                   transpose8(pack2<F16>(b[0] * f0, b[1] * f1)), transpose8(pack2<F16>(b[2] * f0, b[3] * f1))};
+  trade_words(r);
+  if (head < heads && d < D) *reinterpret_cast<uint4*>(out + head * o_sh + d * 2) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <bool F16, int NT, int T>
@@ -362,10 +383,27 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   {
     const int per = (P.B + THREADS - 1) / THREADS;
     const int b0 = tid * per, b1 = min(P.B, b0 + per);
+    int n0 = b0 < b1 ? P.lens[b0] : 0;             // on its way while the barriers are made
+    if (P.boxed && tid == 32) {
+      prefetch_tmap(&P.map_k);
+      prefetch_tmap(&P.map_v);
+    }
+    if (tid < DEC_RING_MAX) {
+      const int arrivals = P.boxed ? 1 : 32;
+      mbar_init(smem_u32(full_k + tid), arrivals);
+      mbar_init(smem_u32(full_v + tid), arrivals);
+      mbar_init(smem_u32(empty_k + tid), DEC_WARPS);
+      mbar_init(smem_u32(empty_v + tid), DEC_WARPS);
+      fence_mbar_init();
+    }
+    if (tid == 64) {
+      abort_flag = 0;
+      P.cuts[2 * blockIdx.x] = P.cuts[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    }
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
-      const int n = P.lens[b];
-      const int len = clamped_len(P, b);
+      const int n = b == b0 ? n0 : P.lens[b];
+      const int len = clamped_len(P, n);
       if (n != len && blockIdx.x == 0) report_invalid(P.err);
       mine += (len + T - 1) / T;
     }
@@ -376,22 +414,6 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       if (lane >= d) incl += x;
     }
     if (lane == 31) scan_s[warp] = incl;
-    if (P.boxed && tid == 32) {
-      prefetch_tmap(&P.map_k);
-      prefetch_tmap(&P.map_v);
-    }
-    if (tid == 0) {
-      abort_flag = 0;
-      const int arrivals = P.boxed ? 1 : 32;
-      for (int i = 0; i < DEC_RING_MAX; ++i) {
-        mbar_init(smem_u32(full_k + i), arrivals);
-        mbar_init(smem_u32(full_v + i), arrivals);
-        mbar_init(smem_u32(empty_k + i), DEC_WARPS);
-        mbar_init(smem_u32(empty_v + i), DEC_WARPS);
-      }
-      fence_mbar_init();
-      P.cuts[2 * blockIdx.x] = P.cuts[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-    }
     __syncthreads();
     long long before = 0;
     total = 0;
@@ -403,23 +425,27 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     long long at = (before + incl - mine) * pairs;   // first tile of request b0
     const long long runs = total < gridDim.x ? total : gridDim.x;
     const long long c = blockIdx.x;
-    lo = c < runs ? c * total / runs : 0;
-    hi = c < runs ? (c + 1) * total / runs : 0;
+    // c total / runs by way of total = q runs + rest
+    const uint32_t cut = (uint32_t)max(runs, 1LL);
+    const long long q = total >> 32 ? total / cut : (uint32_t)total / cut;
+    const uint32_t rest = (uint32_t)(total - q * cut);
+    lo = c < runs ? c * q + (uint32_t)c * rest / cut : 0;
+    hi = c < runs ? (c + 1) * q + (uint32_t)(c + 1) * rest / cut : 0;
     if (c < runs && lo >= at && lo < at + mine * pairs) {
       int b = b0;
       for (; b < b1; ++b) {
-        const long long tiles = (clamped_len(P, b) + T - 1) / T;
+        const long long tiles = (clamped_len(P, b == b0 ? n0 : P.lens[b]) + T - 1) / T;
         if (lo < at + tiles * pairs) break;
         at += tiles * pairs;
       }
       b = min(b, P.B - 1);
       start_s[0] = b;
-      start_s[1] = max(1, clamped_len(P, b));
+      start_s[1] = max(1, clamped_len(P, b == b0 ? n0 : P.lens[b]));
       scan_s[DEC_THREADS / 32] = lo - at;
     }
     // Requests without keys have no tile: their rows are written here.
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
-      if (clamped_len(P, b) != 0) continue;
+      if (clamped_len(P, P.lens[b]) != 0) continue;
       for (int i = tid; i < P.Hq * (P.D / 8); i += THREADS) {
         const int h = i / (P.D / 8), d = i % (P.D / 8);
         *reinterpret_cast<uint4*>(P.o + b * P.o_sb + h * P.o_sh + d * 16) = make_uint4(0, 0, 0, 0);
@@ -441,8 +467,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     cur.len = start_s[1];
     cur.tiles = (cur.len + T - 1) / T;
     const long long r = scan_s[DEC_THREADS / 32];
-    cur.u = (int)(r / cur.tiles);
-    cur.t = (int)(r % cur.tiles);
+    cur.u = (int)(r >> 32 ? r / cur.tiles : (uint32_t)r / (uint32_t)cur.tiles);
+    cur.t = (int)(r - (long long)cur.u * cur.tiles);
   }
   dependents_launch();
   const int n_tiles = (int)(hi - lo);
@@ -510,12 +536,15 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       const int head = n * 8 + hq;
       const char* src = P.q + cur.b * P.q_sb + (int64_t)(hq0 + head) * P.q_sh;
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int d = (k0 + s) * 16 + j * 8 + c2;
-          qf[s][n][j] = head < rows && s < kn && d < P.D ? *reinterpret_cast<const uint32_t*>(src + d * 2) : 0u;
-        }
+      for (int s = 0; s < 8; s += 2) {             // 16 bytes a lane
+        const int d = (k0 + s) * 16 + lane % 4 * 8;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (head < rows && s < kn && d < P.D) x = *reinterpret_cast<const uint4*>(src + d * 2);
+        qf[s][n][0] = x.x;
+        qf[s][n][1] = x.y;
+        qf[s + 1][n][0] = x.z;
+        qf[s + 1][n][1] = x.w;
+      }
 #pragma unroll
       for (int s = 0; s < DT; ++s)
 #pragma unroll
@@ -531,6 +560,19 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
 
       // ---- scores of 16 keys over this warp's part of D
       if (alive) alive = all_waited(smem_u32(full_k + slot_k), lap_k, P, &abort_flag);
+      if (i == i0) {                               // Q is here too: dealt out to the four lanes of a head
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int s = 0; s < 8; s += 2) {
+            uint32_t r[4] = {qf[s][n][0], qf[s][n][1], qf[s + 1][n][0], qf[s + 1][n][1]};
+            trade_words(r);
+            qf[s][n][0] = r[0];
+            qf[s][n][1] = r[1];
+            qf[s + 1][n][0] = r[2];
+            qf[s + 1][n][1] = r[3];
+          }
+      }
 #pragma unroll
       for (int y = 0; y < (OWN ? 2 : 1); ++y) {
         const uint32_t a0 = (y ? k_at2 : k_at) + slot_k * stage;

@@ -114,6 +114,8 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], con
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+__device__ __forceinline__ void fetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Transposes an 8 x 8 matrix of 16-bit values, of which lane i holds row i / 4,
 // columns i % 4 * 2 and the next.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
