@@ -69,6 +69,7 @@ struct DecodeParams {
   int num_pages, page_size, max_pages;
   int chunks;       // 64-column chunks of a row
   int boxed;        // tiles arrive as tensor boxes
+  int page_tiles;   // tiles of a page where a tile ends with its page, else 0
   int box_rows;     // rows of a box (all T where not boxed), a power of two >= 8
   int box_chunks;   // chunks of a box: all, or 1 when D ends inside a chunk
   int ring_k, ring_v, drop;
@@ -127,6 +128,22 @@ __device__ __forceinline__ int clamped_len(const DecodeParams& P, int n) {
   return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
 
+// Tiles of a request, and a tile's first key.  (Tiles that end with their page are a
+// kernel of their own: with the other path's code beside it a call took 0.2 to 1 us more.)
+template <bool PAGED>
+__device__ __forceinline__ int tiles_of(const DecodeParams& P, int len, int T) {
+  if (!PAGED) return (len + T - 1) / T;
+  const int pages = len / P.page_size;
+  return pages * P.page_tiles + (len - pages * P.page_size + T - 1) / T;
+}
+template <bool PAGED>
+__device__ __forceinline__ int first_key(const DecodeParams& P, int t, int T) {
+  if (!PAGED) return t * T;
+  const int pages = t / P.page_tiles;
+  return pages * P.page_size + (t - pages * P.page_tiles) * T;
+}
+
+template <bool PAGED>
 __device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place& p, int T) {
   if (++p.t < p.tiles) return;
   p.t = 0;
@@ -141,7 +158,7 @@ __device__ __forceinline__ void advance(const DecodeParams& P, int pairs, Place&
     ++p.b;
     p.len = clamped_len(P, P.lens[p.b]);
   } while (p.len == 0);
-  p.tiles = (p.len + T - 1) / T;
+  p.tiles = tiles_of<PAGED>(P, p.len, T);
 }
 
 // A run [lo, lo + n) of the line's `total` tiles, which are dealt to `runs` CTAs.
@@ -180,6 +197,7 @@ __device__ __forceinline__ void fetch_queries(const DecodeParams& P, const Place
 // K (or V) tiles of the run as tensor boxes, a box a lane, its page looked up
 // one tile ahead.  A page that does not exist, and rows that belong to no key,
 // have a coordinate behind the last page: the copy writes zeros there.
+template <bool PAGED>
 __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int heads, bool is_v, Place at, const Run& run,
                                               uint32_t ring, int slots, uint64_t* full, uint64_t* empty, volatile int* abort_flag) {
   const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles, n_tiles = run.n;
@@ -192,7 +210,7 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
   int page = -1, in_page = 0;
   bool keyed = false;
   auto look_up = [&](const Place& p) {
-    const int key = p.t * T + row;
+    const int key = first_key<PAGED>(P, p.t, T) + row;
     keyed = mine && key < p.len;
     page = -1;
     if (keyed) {
@@ -210,7 +228,7 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     if (keyed && !good) report_invalid(P.err);
     const int y = good ? in_page : 0, z = good ? page : P.num_pages;
     if (is_v && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
-    advance(P, pairs, at, T);
+    advance<PAGED>(P, pairs, at, T);
     if (i + 1 < n_tiles) {
       look_up(at);
       if (is_v && at.t == 0) fetch_queries(P, at, heads);
@@ -287,7 +305,7 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int
       }
     }
     if (is_v && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
-    advance(P, pairs, at, T);
+    advance<false>(P, pairs, at, T);
     if (i + 1 < n_tiles) {
       look_up(at);
       if (is_v && at.t == 0) fetch_queries(P, at, heads);
@@ -356,7 +374,7 @@ __device__ __forceinline__ void write_columns(char* out, int64_t o_sh, int heads
   if (head < heads && d < D) *reinterpret_cast<uint4*>(out + head * o_sh + d * 2) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <bool F16, int NT, int T>
+template <bool F16, int NT, int T, bool PAGED>
 __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(const __grid_constant__ DecodeParams P) {
   constexpr int HEADS = 8 * NT, THREADS = DEC_THREADS;
   constexpr int PARTS = decode_parts(T), GROUPS = decode_groups(T), MT = T / 16;
@@ -405,7 +423,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       const int n = b == b0 ? n0 : P.lens[b];
       const int len = clamped_len(P, n);
       if (n != len && blockIdx.x == 0) report_invalid(P.err);
-      mine += (len + T - 1) / T;
+      mine += tiles_of<PAGED>(P, len, T);
     }
     long long incl = mine;
 #pragma unroll
@@ -434,7 +452,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     if (c < runs && lo >= at && lo < at + mine * pairs) {
       int b = b0;
       for (; b < b1; ++b) {
-        const long long tiles = (clamped_len(P, b == b0 ? n0 : P.lens[b]) + T - 1) / T;
+        const long long tiles = tiles_of<PAGED>(P, clamped_len(P, b == b0 ? n0 : P.lens[b]), T);
         if (lo < at + tiles * pairs) break;
         at += tiles * pairs;
       }
@@ -465,7 +483,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     __syncthreads();
     cur.b = start_s[0];
     cur.len = start_s[1];
-    cur.tiles = (cur.len + T - 1) / T;
+    cur.tiles = tiles_of<PAGED>(P, cur.len, T);
     const long long r = scan_s[DEC_THREADS / 32];
     cur.u = (int)(r >> 32 ? r / cur.tiles : (uint32_t)r / (uint32_t)cur.tiles);
     cur.t = (int)(r - (long long)cur.u * cur.tiles);
@@ -482,8 +500,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     const uint32_t ring = is_v ? ring_v : ring_k;
     const int slots = is_v ? P.ring_v : P.ring_k;
     const Run run{lo, total, total < gridDim.x ? total : gridDim.x, n_tiles};
-    if (P.boxed)
-      produce_boxes(P, T, HEADS, is_v, cur, run, ring, slots, full, empty, &abort_flag);
+    if (PAGED || P.boxed)
+      produce_boxes<PAGED>(P, T, HEADS, is_v, cur, run, ring, slots, full, empty, &abort_flag);
     else
       produce_pieces(P, T, HEADS, is_v, cur, run, ring, slots, full, empty, &abort_flag);
     return;
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     if (warp == 0) {
       Place next = cur;
       next.t = next.tiles - 1;
-      advance(P, pairs, next, T);
+      advance<PAGED>(P, pairs, next, T);
       if (lane == 0) next_s[turn] = next;
     }
     const int hk = cur.u / P.head_tiles, ht = cur.u % P.head_tiles;
@@ -552,8 +570,18 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       top[n] = -INFINITY;
       sum[n] = 0.0f;
     }
-    int left = cur.len - cur.t * T - wkey * 32;    // keys from this warp's first one on
-    for (int i = i0; i < i1; ++i, left -= T) {
+    int key = first_key<PAGED>(P, cur.t, T);              // of the tile
+    int in_page = PAGED ? P.page_size - key % P.page_size : 0;   // keys of its page from the tile on
+    for (int i = i0; i < i1; ++i) {
+      const int left = (PAGED ? min(in_page, cur.len - key) : cur.len - key) - wkey * 32;   // keys from this warp's first one on
+      if (!PAGED) {
+        key += T;
+      } else {
+        const int step = min(in_page, T);
+        key += step;
+        in_page -= step;
+        if (in_page == 0) in_page = P.page_size;
+      }
       float* sc = scores + (OWN ? 0 : buf) * SBUF;
       buf ^= 1;
       if (OWN) __syncwarp();
@@ -922,10 +950,10 @@ DecodeSpace decode_space(int grid, int heads, int D) {
 
 template <bool F16, int NT, int T>
 ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int grid, int dev, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(&decode_kernel<F16, NT, T>);
-  const ffpa_status st = set_smem_attr_once(fn, dev, (int)pl.smem);
+  const auto fn = P.page_tiles ? &decode_kernel<F16, NT, T, true> : &decode_kernel<F16, NT, T, false>;
+  const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(fn), dev, (int)pl.smem);
   if (st != FFPA_OK) return st;
-  decode_kernel<F16, NT, T><<<grid, DEC_THREADS, pl.smem, stream>>>(P);
+  fn<<<grid, DEC_THREADS, pl.smem, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
   const int heads = 8 * NT;
   int log_rows = 0;
@@ -1055,12 +1083,17 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   P.page_size = page_size;
   P.max_pages = held ? max_pages : 0;   // without pages every request is empty
   P.chunks = pl.chunks;
-  // Boxes of as many rows as divide a page, down to the 8 of the swizzle.
-  P.boxed = held && page_size % 8 == 0;
+  // Boxes of as many rows as divide a page, down to the 8 of the swizzle.  Where a
+  // page's size is no multiple of 8 but fills half a tile at least, a tile is one box
+  // that ends with its page (B32 Hkv8 D512 of 4096 keys, pages of 100: 317 us, in pieces
+  // 444); smaller pages of that kind come in pieces.
+  const bool by_page = page_size % 8 != 0 && 2 * page_size >= pl.tile;
+  P.boxed = held && (page_size % 8 == 0 || by_page);
+  P.page_tiles = by_page ? (page_size + pl.tile - 1) / pl.tile : 0;
   P.box_rows = pl.tile;
   P.box_chunks = D % 64 == 0 ? pl.chunks : 1;
   if (P.boxed) {
-    while (page_size % P.box_rows != 0) P.box_rows /= 2;
+    while (!by_page && page_size % P.box_rows != 0) P.box_rows /= 2;
     for (int i = 0; i < 2; ++i) {
       const int64_t* s = i ? v_str : k_str;
       CUtensorMap* map = i ? &P.map_v : &P.map_k;

@@ -64,6 +64,15 @@ def test_decode_groups(Hq, Hkv, D):
     check_decode(args, ref, f"Hq={Hq} Hkv={Hkv}")
 
 
+@pytest.mark.parametrize("page", [9, 20, 60, 130, 250, 999])
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 64), (2, 2, 200), (6, 1, 320), (40, 2, 512), (8, 2, 1000)])
+def test_decode_tiles_that_end_with_their_page(page, Hq, Hkv, D):
+    """Page sizes that are no multiple of 8: smaller than half a tile, than a tile, and of several."""
+    lens = [page - 1, page, page + 1, 0, 3 * page + 7, 1, 2 * page - 1, 1111, 5 * page]
+    args, ref = decode_case(lens, Hq, Hkv, D, page, HF if D == 320 else BF, seed=page + D)
+    check_decode(args, ref, f"page={page} D={D}")
+
+
 @pytest.mark.parametrize("page", [1, 3, 8, 16, 100, 256])
 @pytest.mark.parametrize("D", [64, 512])
 def test_decode_page_sizes_and_lengths(page, D):
