@@ -17,9 +17,10 @@
 //    but the tiles in work in flight), are kept full by warps of their own.
 //    Where pages hold a multiple of 8 keys a tile arrives as tensor boxes of
 //    up to T rows of one page, with the 128-byte swizzle that the matrix
-//    loads want; other page sizes take 16-byte asynchronous copies into the same
-//    layout.  (One bulk copy per row was slower: an SM starts one every 45 to 64
-//    cycles, 1.65 TB/s with the 256-byte rows of D = 128.)
+//    loads want.  Of other page sizes the larger ones have tiles that end with
+//    their page, one box each, and the smaller ones take 16-byte asynchronous
+//    copies into the same layout.  (One bulk copy per row was slower: an SM
+//    starts one every 45 to 64 cycles, 1.65 TB/s with the 256-byte rows of D = 128.)
 //  - Keys (then columns of V) are the 16 rows of mma.m16n8k16 and the heads its
 //    8 columns: K and V are the operands read once, and up to 8 heads cost one
 //    instruction per 256 elements.  For the scores each of eight warps takes 16
@@ -1084,10 +1085,12 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   P.max_pages = held ? max_pages : 0;   // without pages every request is empty
   P.chunks = pl.chunks;
   // Boxes of as many rows as divide a page, down to the 8 of the swizzle.  Where a
-  // page's size is no multiple of 8 but fills half a tile at least, a tile is one box
-  // that ends with its page (B32 Hkv8 D512 of 4096 keys, pages of 100: 317 us, in pieces
-  // 444); smaller pages of that kind come in pieces.
-  const bool by_page = page_size % 8 != 0 && 2 * page_size >= pl.tile;
+  // page's size is no multiple of 8 but fills enough of a tile, a tile is one box that
+  // ends with its page (B32 Hkv8 D512 of 4096 keys, pages of 100: 317 us, in pieces
+  // 444); smaller pages of that kind come in pieces.  "Enough" is where both cost the
+  // same: a half (D512, 12 of 32 keys: 136 us, in pieces 118), and a third of the tiles
+  // of 128 and 256 keys (D64, 100 of 256 keys: 32 us, in pieces 45; D128, 36 of 128: 47, 45).
+  const bool by_page = page_size % 8 != 0 && (pl.tile >= 128 ? 3 : 2) * page_size >= pl.tile;
   P.boxed = held && (page_size % 8 == 0 || by_page);
   P.page_tiles = by_page ? (page_size + pl.tile - 1) / pl.tile : 0;
   P.box_rows = pl.tile;
