@@ -835,9 +835,9 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
 // The kernel is one chain of latencies (the cut, the sums, the store), so it has
 // no division and no sum over lanes: 2 us of one request of 777 keys, against 4 us
 // for a block of 512 threads a head, and 2 to 3 us of batches of 110 requests,
-// against 4 to 7 us.  With a warp for up to 16 CTAs, 5 requests of 104 keys, 16
-// heads of 1024, take 18.3 us, with up to 4 CTAs 22.7 us; for up to 32 CTAs the
-// request of 777 keys takes 11.7 us in place of 9.3.
+// against 4 to 7 us.  With a warp for up to 16 CTAs, 5 requests of up to 208 keys,
+// 64 heads of 1024, take 4 us less than for up to 4; for up to 32 CTAs the request
+// of 777 keys takes 2.4 us more.
 constexpr int JOIN_WARPS = 8, JOIN_FEW = 16;
 
 struct Joined {
@@ -1090,7 +1090,7 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   // 444); smaller pages of that kind come in pieces.  "Enough" is where both cost the
   // same: a half (D512, 12 of 32 keys: 136 us, in pieces 118), and a third of the tiles
   // of 128 and 256 keys (D64, 100 of 256 keys: 32 us, in pieces 45; D128, 36 of 128: 47, 45).
-  const bool by_page = page_size % 8 != 0 && (pl.tile >= 128 ? 3 : 2) * page_size >= pl.tile;
+  const bool by_page = page_size % 8 != 0 && page_size > (pl.tile - 1) / (pl.tile >= 128 ? 3 : 2);
   P.boxed = held && (page_size % 8 == 0 || by_page);
   P.page_tiles = by_page ? (page_size + pl.tile - 1) / pl.tile : 0;
   P.box_rows = pl.tile;
