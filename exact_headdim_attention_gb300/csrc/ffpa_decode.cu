@@ -1098,17 +1098,20 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   if (P.boxed) {
     while (!by_page && page_size % P.box_rows != 0) P.box_rows /= 2;
     for (int i = 0; i < 2; ++i) {
-      const int64_t* s = i ? v_str : k_str;
+      // (bytes; a dimension of one entry may have any stride, a tensor map takes multiples of 16)
+      const int64_t* of = i ? v_str : k_str;
+      const uint64_t row = (uint64_t)of[1] * 2, one = (uint64_t)D * 2;
+      const uint64_t head = Hkv > 1 ? (uint64_t)of[2] * 2 : one, page = num_pages > 1 ? (uint64_t)of[0] * 2 : one;
       CUtensorMap* map = i ? &P.map_v : &P.map_k;
       const void* base = i ? v_cache : k_cache;
       if (P.box_chunks > 1) {
         const uint64_t dims[5] = {64, (uint64_t)page_size, (uint64_t)pl.chunks, (uint64_t)Hkv, (uint64_t)num_pages};
-        const uint64_t str[4] = {(uint64_t)s[1] * 2, 128, (uint64_t)s[2] * 2, (uint64_t)s[0] * 2};
+        const uint64_t str[4] = {row, 128, head, page};
         const uint32_t box[5] = {64, (uint32_t)P.box_rows, (uint32_t)pl.chunks, 1, 1};
         st = encode_rows(map, dt, 5, base, dims, str, box);
       } else {
         const uint64_t dims[4] = {(uint64_t)D, (uint64_t)page_size, (uint64_t)Hkv, (uint64_t)num_pages};
-        const uint64_t str[3] = {(uint64_t)s[1] * 2, (uint64_t)s[2] * 2, (uint64_t)s[0] * 2};
+        const uint64_t str[3] = {row, head, page};
         const uint32_t box[4] = {64, (uint32_t)P.box_rows, 1, 1};
         st = encode_rows(map, dt, 4, base, dims, str, box);
       }

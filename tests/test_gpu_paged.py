@@ -192,6 +192,17 @@ def test_decode_bad_pages_and_lengths_are_reported_and_not_followed():
     device_ok()
 
 
+@pytest.mark.parametrize("page", [16, 100])
+@pytest.mark.parametrize("D", [200, 512])
+def test_decode_strides_of_single_entries_are_free(page, D):
+    """One key head, and one page: their strides are never used and may be anything."""
+    args, ref = decode_case([page - 3], 4, 1, D, page, BF, seed=D + page)
+    q, kc, vc, table, n = args
+    kc, vc = (x[:1].contiguous() for x in (kc[table[0, 0]:], vc[table[0, 0]:]))
+    odd = [x.as_strided(x.shape, (5, D, 3, 1)) for x in (kc, vc)]
+    check_decode((q, *odd, torch.zeros_like(table), n), ref, f"page={page} D={D}")
+
+
 def test_decode_pages_beyond_32_bit_offsets():
     """A cache of 2^31 + elements whose used pages lie at its end."""
     Hkv, D, page = 2, 512, 16
