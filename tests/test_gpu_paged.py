@@ -192,6 +192,22 @@ def test_decode_bad_pages_and_lengths_are_reported_and_not_followed():
     device_ok()
 
 
+@pytest.mark.parametrize("page,D", [(100, 512), (20, 1000), (100, 64)])
+def test_decode_bad_pages_of_any_size(page, D):
+    """A page that does not exist counts as keys and values of zeros, and is reported."""
+    args, _ = decode_case([3 * page + 7, page, 2 * page - 1], 4, 2, D, page, BF, seed=D)
+    q, kc, vc, table, n = args
+    for b, bad in [(0, -1), (2, kc.shape[0]), (1, 2**31 - 1)]:
+        word = status_word()
+        broken, k0, v0 = table.clone(), kc.clone(), vc.clone()
+        broken[b, 0] = bad
+        k0[table[b, 0]] = 0
+        v0[table[b, 0]] = 0
+        got = pkg.ffpa_decode_paged(q, kc, vc, broken, n, enable_gqa=True, status=word)
+        assert word.item() == pkg.FFPA_ERR_INVALID
+        assert torch.equal(got, pkg.ffpa_decode_paged(q, k0, v0, table, n, enable_gqa=True))
+
+
 @pytest.mark.parametrize("page", [16, 100])
 @pytest.mark.parametrize("D", [200, 512])
 def test_decode_strides_of_single_entries_are_free(page, D):
