@@ -33,9 +33,11 @@
 //    so two CTAs share an SM where the registers allow it, each with half of
 //    the rings.
 //  - Maximum and sum are kept in fp32 by each group of warps that has keys of
-//    its own and joined at the pair's end in the order of the groups.  P is
-//    rounded to the input type, as in the forward kernels; the sum is of the
-//    unrounded values.
+//    its own and joined at the pair's end in the order of the groups.  P goes
+//    into the second product as two values of the input type (off by 2^-16 of
+//    P, fp16 2^-21), so that numerator and sum see the same weights.  (With P
+//    rounded once the error of O was 20 to 35 % larger; the second value costs
+//    0.3 to 2 %: B32 Hkv8 D512 201.3 -> 201.8 us, B2 Hq16 Hkv1 D256 107.7 -> 110.)
 //
 // Every wait on a copy has a time limit, after which the call's status word
 // receives FFPA_ERR_DEVICE_TIMEOUT and the CTA runs out without waiting.
@@ -47,6 +49,9 @@ namespace {
 constexpr int DEC_WARPS = 8;          // that multiply
 constexpr int DEC_THREADS = (DEC_WARPS + 2) * 32;   // and one each that brings K and V
 constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
+// Powers of two above the maximum at which fp16 forms its exponentials: the largest is
+// 2^15, and 2^-39 of it is the smallest that counts.
+constexpr float P_LIFT = 15.0f;
 // SMs of any sm_103 part; the workspace is sized for them without asking a device.
 constexpr int DEC_SMS_MAX = 160;
 
@@ -637,7 +642,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       if (!OWN) named_bar_sync(1, N);
 
       // ---- P of this warp's keys, as the operand of the second product
-      uint32_t pf[KSTEPS][NT][2];
+      uint32_t pf[KSTEPS][NT][2], pr[KSTEPS][NT][2];   // and the rest of it
       float fac[NT];
       bool moved = false;
 #pragma unroll
@@ -668,6 +673,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         for (int j = 0; j < 2 * KSTEPS; ++j) most = fmax3(most, x[j].x, x[j].y);
         most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
         most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+        if (F16) most -= P_LIFT;
         const float now = fmaxf(top[n], most);
         const float base = now == -INFINITY ? 0.0f : now;
         fac[n] = ex2_approx(top[n] - base);
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
           x[j].x = ex2_approx(x[j].x - base);
           x[j].y = ex2_approx(x[j].y - base);
           add += x[j].x + x[j].y;
-          pf[j >> 1][n][j & 1] = pack2<F16>(x[j].x, x[j].y);
+          split2<F16>(x[j].x, x[j].y, pf[j >> 1][n][j & 1], pr[j >> 1][n][j & 1]);
         }
         sum[n] = sum[n] * fac[n] + add;
       }
@@ -718,6 +724,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16<F16>(acc[s][n], a, pf[g][n]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16<F16>(acc[s][n], a, pr[g][n]);
         }
       }
       __syncwarp();
