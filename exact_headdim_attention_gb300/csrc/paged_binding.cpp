@@ -7,6 +7,7 @@
 // the device when they serve single tokens, and the marshalling in Python took
 // 14 to 27 us of the 26 to 44 us that a call took (now 7 to 13 us a call).
 #include <ATen/ATen.h>
+#include <ATen/FunctionalTensorWrapper.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -32,7 +33,13 @@ struct Abi {
 // ---- arguments
 const Tensor& tensor(PyObject* o, const char* name) {
   TORCH_CHECK_TYPE(THPVariable_Check(o), name, " must be a torch.Tensor");
-  return THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  // (Tracers' and transforms' tensors have no memory that a kernel could use: a pointer
+  // of theirs is null or anything.  They go through the torch operators.)
+  TORCH_CHECK_TYPE(!t.unsafeGetTensorImpl()->is_python_dispatch() && !at::functionalization::impl::isFunctionalTensor(t) &&
+                       t.layout() == at::kStrided && t.has_storage() && !t.is_meta(),
+                   name, " must be a tensor with memory of its own, not one that is traced or transformed");
+  return t;
 }
 const Tensor* maybe(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
 bool truth(PyObject* o) {
