@@ -15,7 +15,7 @@ the recomputed scores, but no gradient is formed for the mask itself), and
 the varlen operator through ``ffpa_bwd_varlen``.
 
 ``torch.ops.ffpa.qk_norm_rope`` (differentiable through
-``ffpa_qk_norm_rope_bwd``), ``kv_append``, ``decode_paged`` and
+``qk_norm_rope_bwd``, once), ``kv_append``, ``decode_paged`` and
 ``page_plan`` do the same for the calls around a paged key/value cache
 (paged.py); the last three serve and have no gradient, and ``kv_append`` and
 ``page_plan`` declare the cache and the block table that they write.  As with
@@ -30,6 +30,14 @@ from typing import Optional
 import torch
 
 from . import _binding, paged
+
+
+def _eager(*tensors) -> bool:
+    """Whether a backward may call the binding itself: no graph of the gradients is asked for, no
+    tracer or mode looks on, and every tensor is a plain one.  (A backward's operator is for the
+    rest: its dispatch takes 57 us of host time, of a step of 262 us.)"""
+    return (not torch.is_grad_enabled() and torch._C._len_torch_dispatch_stack() == 0 and
+            all(t is None or type(t) in (torch.Tensor, torch.nn.Parameter) for t in tensors))
 
 
 @torch.library.custom_op("ffpa::attn_fwd", mutates_args=())
@@ -165,6 +173,32 @@ def _qk_norm_rope_fake(q, k, positions, inv_freq, q_weight, k_weight, eps, inter
             torch.empty_like(k, memory_format=torch.contiguous_format))
 
 
+@torch.library.custom_op("ffpa::qk_norm_rope_bwd", mutates_args=())
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                     positions: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+                     q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], eps: float, interleaved: bool,
+                     rope_scale: float) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of q, k, q_weight and k_weight (no entries for a weight that is None)."""
+    dq, dk, dqw, dkw = paged.ffpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight,
+                                                   eps=eps, interleaved=interleaved, rope_scale=rope_scale)
+    return dq, dk, q.new_empty(0) if dqw is None else dqw, k.new_empty(0) if dkw is None else dkw
+
+
+@qk_norm_rope_bwd.register_fake
+def _qk_norm_rope_bwd_fake(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, rope_scale):
+    return (torch.empty_like(q, memory_format=torch.contiguous_format),
+            torch.empty_like(k, memory_format=torch.contiguous_format),
+            q.new_empty(0) if q_weight is None else torch.empty_like(q_weight),
+            k.new_empty(0) if k_weight is None else torch.empty_like(k_weight))
+
+
+def _no_second_derivative(ctx, *grads):
+    raise NotImplementedError("no second derivative is formed")
+
+
+qk_norm_rope_bwd.register_autograd(_no_second_derivative)
+
+
 def _qk_norm_rope_setup_context(ctx, inputs, output):
     q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, rope_scale = inputs
     ctx.save_for_backward(q, k, positions, inv_freq, q_weight, k_weight)
@@ -179,10 +213,13 @@ def _qk_norm_rope_backward(ctx, grad_q, grad_k):
     # An output that the loss does not use has no gradient: zeros for its rows.
     grad_q = torch.zeros_like(q, memory_format=torch.contiguous_format) if grad_q is None else grad_q.contiguous()
     grad_k = torch.zeros_like(k, memory_format=torch.contiguous_format) if grad_k is None else grad_k.contiguous()
-    dq, dk, dqw, dkw = paged.ffpa_qk_norm_rope_bwd(grad_q, grad_k, q, k, positions, inv_freq, q_weight, k_weight,
-                                                   eps=ctx.eps, interleaved=ctx.interleaved,
-                                                   rope_scale=ctx.rope_scale)
-    return dq, dk, None, None, dqw, dkw, None, None, None
+    how = (grad_q, grad_k, q, k, positions, inv_freq, q_weight, k_weight)
+    if _eager(*how):
+        dq, dk, dqw, dkw = paged.ffpa_qk_norm_rope_bwd(*how, eps=ctx.eps, interleaved=ctx.interleaved,
+                                                       rope_scale=ctx.rope_scale)
+    else:
+        dq, dk, dqw, dkw = torch.ops.ffpa.qk_norm_rope_bwd(*how, ctx.eps, ctx.interleaved, ctx.rope_scale)
+    return (dq, dk, None, None, None if q_weight is None else dqw, None if k_weight is None else dkw, None, None, None)
 
 
 qk_norm_rope.register_autograd(_qk_norm_rope_backward, setup_context=_qk_norm_rope_setup_context)
