@@ -12,7 +12,9 @@ replace that call for the supported cases: bf16/fp16 CUDA tensors,
 backward), no dropout.  The dense operator is
 differentiable through ``ffpa_bwd`` (the backward kernels; a mask enters
 the recomputed scores, but no gradient is formed for the mask itself), and
-the varlen operator through ``ffpa_bwd_varlen``.
+the varlen operator through ``ffpa_bwd_varlen``.  Both backwards are operators
+themselves (``attn_bwd``, ``attn_varlen_bwd``), so that a training step can be
+traced; second derivatives are refused.
 
 ``torch.ops.ffpa.qk_norm_rope`` (differentiable through
 ``qk_norm_rope_bwd``, once), ``kv_append``, ``decode_paged`` and
@@ -73,13 +75,43 @@ def _check_grads(grad_o, grad_lse):
         raise NotImplementedError("backward without a gradient for O")
 
 
+def _no_second_derivative(ctx, *grads):
+    raise NotImplementedError("no second derivative is formed")
+
+
+def _like_inputs(q, k, v):
+    return tuple(torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
+
+
+@torch.library.custom_op("ffpa::attn_bwd", mutates_args=())
+def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+             lse: torch.Tensor, attn_mask: Optional[torch.Tensor], is_causal: bool, scale: Optional[float],
+             enable_gqa: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of q, k and v."""
+    return _binding.ffpa_bwd(dout, q, k, v, out, lse, is_causal=is_causal, scale=scale, enable_gqa=enable_gqa,
+                             attn_mask=attn_mask)
+
+
+@attn_bwd.register_fake
+def _attn_bwd_fake(dout, q, k, v, out, lse, attn_mask, is_causal, scale, enable_gqa):
+    return _like_inputs(q, k, v)
+
+
+attn_bwd.register_autograd(_no_second_derivative)
+
+
 def _attn_fwd_backward(ctx, grad_o, grad_lse):
     if ctx.needs_input_grad[3]:
         raise NotImplementedError("no gradient is formed for attn_mask")
     _check_grads(grad_o, grad_lse)
     q, k, v, o, lse, attn_mask = ctx.saved_tensors
-    dq, dk, dv = _binding.ffpa_bwd(grad_o.contiguous(), q, k, v, o, lse, is_causal=ctx.is_causal,
-                                   scale=ctx.scale, enable_gqa=ctx.enable_gqa, attn_mask=attn_mask)
+    grad_o = grad_o.contiguous()
+    if _eager(grad_o, q, k, v, o, lse, attn_mask):
+        dq, dk, dv = _binding.ffpa_bwd(grad_o, q, k, v, o, lse, is_causal=ctx.is_causal, scale=ctx.scale,
+                                       enable_gqa=ctx.enable_gqa, attn_mask=attn_mask)
+    else:
+        dq, dk, dv = torch.ops.ffpa.attn_bwd(grad_o, q, k, v, o, lse, attn_mask, ctx.is_causal, ctx.scale,
+                                             ctx.enable_gqa)
     return dq, dk, dv, None, None, None, None
 
 
@@ -115,12 +147,35 @@ def _attn_varlen_setup_context(ctx, inputs, output):
     ctx.set_materialize_grads(False)
 
 
+@torch.library.custom_op("ffpa::attn_varlen_bwd", mutates_args=())
+def attn_varlen_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                    lse: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: Optional[torch.Tensor],
+                    max_seqlen_q: int, max_seqlen_k: int, causal: bool, softmax_scale: Optional[float],
+                    enable_gqa: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of packed q, k and v."""
+    return _binding.ffpa_bwd_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                    softmax_scale=softmax_scale, causal=causal, enable_gqa=enable_gqa)
+
+
+@attn_varlen_bwd.register_fake
+def _attn_varlen_bwd_fake(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
+                          softmax_scale, enable_gqa):
+    return _like_inputs(q, k, v)
+
+
+attn_varlen_bwd.register_autograd(_no_second_derivative)
+
+
 def _attn_varlen_backward(ctx, grad_o, grad_lse):
     _check_grads(grad_o, grad_lse)
     q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
-    dq, dk, dv = _binding.ffpa_bwd_varlen(grad_o.contiguous(), q, k, v, o, lse, cu_q, cu_k,
-                                          ctx.max_q, ctx.max_k, softmax_scale=ctx.scale,
-                                          causal=ctx.causal, enable_gqa=ctx.enable_gqa)
+    grad_o = grad_o.contiguous()
+    if _eager(grad_o, q, k, v, o, lse, cu_q, cu_k):
+        dq, dk, dv = _binding.ffpa_bwd_varlen(grad_o, q, k, v, o, lse, cu_q, cu_k, ctx.max_q, ctx.max_k,
+                                              softmax_scale=ctx.scale, causal=ctx.causal, enable_gqa=ctx.enable_gqa)
+    else:
+        dq, dk, dv = torch.ops.ffpa.attn_varlen_bwd(grad_o, q, k, v, o, lse, cu_q, cu_k, ctx.max_q, ctx.max_k,
+                                                    ctx.causal, ctx.scale, ctx.enable_gqa)
     return dq, dk, dv, None, None, None, None, None, None, None
 
 
@@ -190,10 +245,6 @@ def _qk_norm_rope_bwd_fake(dq_out, dk_out, q, k, positions, inv_freq, q_weight, 
             torch.empty_like(k, memory_format=torch.contiguous_format),
             q.new_empty(0) if q_weight is None else torch.empty_like(q_weight),
             k.new_empty(0) if k_weight is None else torch.empty_like(k_weight))
-
-
-def _no_second_derivative(ctx, *grads):
-    raise NotImplementedError("no second derivative is formed")
 
 
 qk_norm_rope_bwd.register_autograd(_no_second_derivative)
