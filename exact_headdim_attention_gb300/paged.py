@@ -80,7 +80,9 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str | None = 
                   fastest stays: base * factor ** (rot_dim / (rot_dim - 2));
       "by_parts"  pairs that turn more than beta_fast times within original_length positions stay,
                   pairs that turn less than beta_slow times are divided by factor, a linear ramp
-                  over the pair's number lies between; rope_scale = 0.1 ln(factor) + 1."""
+                  over the pair's number lies between (from whole pairs on either side: number 0
+                  at the earliest, rot_dim - 1 at the latest); rope_scale = 0.1 ln(factor) + 1.
+                  The published method is YaRN (arXiv 2309.00071)."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and at least 2")
     if not (base > 0 and math.isfinite(base)) or not (factor >= 1 and math.isfinite(factor)):
@@ -101,9 +103,10 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str | None = 
         def pair_turning(times):     # (real) number of the pair that turns `times` times
             return rot_dim * math.log(original_length / (times * 2 * math.pi)) / (2 * math.log(base))
 
+        # The ramp may end behind the last pair, which it then does not divide by the whole factor.
         lo = max(math.floor(pair_turning(beta_fast)), 0)
-        hi = min(math.ceil(pair_turning(beta_slow)), rot_dim // 2 - 1)
-        slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        hi = min(math.ceil(pair_turning(beta_slow)), rot_dim - 1)
+        slow = ((i - lo) / (hi - lo)).clamp(0, 1) if hi > lo else (i >= hi).double()
         inv = inv * (1 - slow) + inv / factor * slow
         scale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "base"):
