@@ -3,7 +3,7 @@
 //
 // Each row is read once and written once: the memory's bandwidth is the bound.
 //  - A work item is some heads of one token, so that the token's cosines and
-//    sines (one sincospif per pair) are shared by its heads; with the weights
+//    sines (two polynomials a pair) are shared by its heads; with the weights
 //    they make four factors a pair, and a row costs two products and the
 //    row's scale for each value.
 //  - Rows come through shared memory by asynchronous copies, DEPTH - 1 of them

@@ -13,8 +13,8 @@
 //
 // Angles are taken in turns, as 64-bit fixed-point fractions: position times
 // frequency wraps there as the angle does, so that far positions need neither
-// a table nor 64-bit floating point per angle (off by 2^-32 turns, and by the
-// rounding of the frequency itself to a double, 2^-52 of the angle).
+// a table nor 64-bit floating point per angle (off by 2^-34 turns, by the position times
+// the frequency's rounding to 2^-65 turns, and by that to a double, 2^-52 of the angle).
 #include "ffpa_paged.cuh"
 
 namespace ffpa {
@@ -148,16 +148,27 @@ __device__ __forceinline__ void load_freqs(const RopeParams& P, long long* freq_
   }
   __syncthreads();
 }
-// Cosine and sine of position times frequency.  The angle is within [-pi, pi),
-// where __cosf and __sinf are off by at most 2^-21 (the CUDA guide's bounds):
-// 2^-12 and less of the outputs' half steps, for a sixth of sincospif's
-// instructions, which took as long as the rows' own arithmetic.
+// Cosine and sine of position times frequency, times scale.  The angle in turns goes
+// to the nearest quarter (its two highest bits) and the rest, u quarters with |u| <= 1/2,
+// to fp32 from 2^-34 turns on.  On it two polynomials in w = u^2 (minimax fits by Remez exchange
+// of sin(pi u / 2) / u and (cos(pi u / 2) - 1) / w, off by 2^-28 and 2^-34) leave both
+// functions off by at most 2^-22 of themselves, however small.  (The hardware's, off by
+// 2^-21 of one, lost small sines and cosines; with them T8192 D512 took 107.6 us in place of
+// 109.9, its backward 88.2 in place of 90.4.)
 __device__ __forceinline__ void turn(long long pos, long long freq, float scale, float& c, float& s) {
   const unsigned long long t = static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(freq);
-  const int hi = static_cast<int>(static_cast<unsigned>(t >> 32));   // turns in [-1/2, 1/2), times 2^32
-  const float a = static_cast<float>(hi) * 1.4629180792671596e-9f;   // 2 pi / 2^32
-  c = __cosf(a) * scale;
-  s = __sinf(a) * scale;
+  const unsigned hi = static_cast<unsigned>(t >> 32), lo = static_cast<unsigned>(t), quarter = hi + 0x20000000u;
+  const float u = static_cast<float>(static_cast<int>(__funnelshift_l(lo, hi, 2))) * 0x1p-32f, w = u * u;
+  float sn = fmaf(w, -0x1.2d9278p-8f, 0x1.465e90p-4f), cs = fmaf(w, 0x1.d9f6ecp-11f, -0x1.55c662p-6f);
+  sn = fmaf(w, sn, -0x1.4abbb8p-1f);
+  cs = fmaf(w, cs, 0x1.03c1dep-2f);
+  sn = fmaf(w, sn, 0x1.921fb6p+0f);
+  cs = fmaf(w, cs, -0x1.3bd3ccp+0f);
+  sn = u * sn * scale;
+  cs = fmaf(w, cs, 1.0f) * scale;
+  const bool odd = quarter & 0x40000000u;          // a quarter on: (c, s) -> (-s, c)
+  c = __uint_as_float(__float_as_uint(odd ? sn : cs) ^ ((quarter + 0x40000000u) & 0x80000000u));
+  s = __uint_as_float(__float_as_uint(odd ? cs : sn) ^ (quarter & 0x80000000u));
 }
 
 __device__ __forceinline__ long long position_of(const RopeParams& P, int b, int n) {

@@ -532,11 +532,12 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
  *     (y_a, y_b) -> rope_scale * (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
  *
  * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved;
- * columns from rot_dim on are not rotated.  fp32 arithmetic, rounded once;
- * an angle is off by at most 2^-31 turns and 2^-52 of its size, so positions
- * of millions lose nothing.  Scaled frequencies for long contexts come in through inv_freq and
- * rope_scale.  inv_freq is finite, and the sum of a row's squares stays in
- * fp32's range.
+ * columns from rot_dim on are not rotated.  fp32 arithmetic, rounded once.
+ * An angle is off by at most 2^-33 turns (for |p| < 2^31; beyond, by |p| 2^-65
+ * turns more) and 2^-52 of its size, so positions of millions lose nothing; its
+ * cosine and sine by 2^-22 of themselves.  Scaled frequencies for long contexts
+ * come in through inv_freq and rope_scale.  inv_freq is finite, and the sum of a
+ * row's squares stays in fp32's range.
  */
 typedef struct ffpa_rope {
   const void* positions;    /* device int32 or int64 [B, N], element strides position_str */
