@@ -53,10 +53,13 @@ def _handle(stream):
 
 
 def _on_stream(workspace, need, t, stream):
-    """A workspace for a stream of the caller's is allocated in that stream's order (the module does so
-    for the current one)."""
-    if workspace is not None or not isinstance(stream, torch.cuda.Stream):
+    """A workspace for a stream of the caller's (torch's, or any object with its handle as cuda_stream) is
+    allocated in that stream's order (the module does so for the current one): it is free again for
+    what the stream runs after the call, and for nothing else."""
+    if workspace is not None or not t.is_cuda:
         return workspace
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=t.device)
     with torch.cuda.stream(stream):
         return torch.empty(max(need, 256), dtype=torch.uint8, device=t.device)
 
