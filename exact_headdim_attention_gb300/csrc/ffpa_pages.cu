@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32) plan_kernel(const PlanParams 
     for (unsigned i = from + lane; i < to; i += 32) {
       const unsigned pos = old + i, j = pos / page_size, in = pos - j * page_size;
       const long long at = before_t + i;
-      // New page: the free list's entry, or -1 when the list has run out or
-      // holds something that is no page (a page number is never negative).
+      // New page: the free list's entry, or -1 when the list has run out.  A page
+      // number is never negative, in the list and in what the table holds.
       int page = -1;
       if (j < held)
         page = table[j];
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32) plan_kernel(const PlanParams 
         if (j - held < got) page = P.free_pages[count - 1 - (before_p + (j - held))];
         if (in == 0) table[j] = page;
       }
+      if (page < 0) report_invalid(P.err);
       if (at < P.tokens) {
         P.slots[at] = page < 0 ? -1 : (long long)page * page_size + in;
         P.positions[at] = (int)pos;

@@ -221,7 +221,8 @@ def ffpa_page_plan(block_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: 
     Returns (slots int64 [num_tokens], positions int32 [num_tokens], cu_seqlens int32 [B+1],
     seq_lens int32 [B] with the new tokens, free_count int32 [1] without the pages taken); rows
     behind the last token have slot -1 and position 0.  Everything stays on the device.  Tokens for
-    which there is no page get slot -1; the status word (see ffpa_fwd) receives FFPA_ERR_INVALID.
+    which there is no page, or a negative one, get slot -1; the status word (see ffpa_fwd) receives
+    FFPA_ERR_INVALID.
 
     Pages of a finished request go back by the caller: written at free_pages[free_count:]."""
     keep, options = _call_options(block_table, status)

@@ -633,8 +633,11 @@ ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_
  * the tokens without a page get slot -1 (and new table entries -1),
  * seq_lens_out counts the tokens that have one, and the call is reported.  So
  * are more than `tokens` new tokens (those beyond are not written and
- * cu_seqlens stops there), negative lengths (taken as 0) and a free_count
- * outside [0, n_free].  One launch on `stream`.
+ * cu_seqlens stops there), negative lengths (taken as 0), a free_count
+ * outside [0, n_free], and a negative page that a new token falls on, whether
+ * the free list gave it or the table held it: the token's slot is -1, and
+ * seq_lens_out counts it (the page was taken, or is the request's).  One
+ * launch on `stream`.
  */
 ffpa_status ffpa_page_plan(int32_t* block_table, int64_t table_str, int B, int max_pages, const int32_t* seq_lens,
                            const int32_t* new_lens, const int32_t* free_pages, int n_free, const int32_t* free_count,

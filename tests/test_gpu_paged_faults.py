@@ -1,0 +1,48 @@
+"""Negative pages in what a plan is given: reported, and their tokens without a slot."""
+import pytest
+import torch
+
+import exact_headdim_attention_gb300 as pkg
+from tests.gpu_util import device_ok
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def plan(table, old, new, free, count, page, tokens):
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    t = torch.tensor(table, dtype=torch.int32, device=DEV)
+    got = pkg.ffpa_page_plan(t, ints(*old), ints(*new), ints(*free), ints(count), page, tokens, status=word)
+    return word.item(), t.tolist(), [x.tolist() for x in got]
+
+
+@pytest.mark.parametrize("bad", [-1, -7, -2 ** 31])
+def test_negative_page_of_the_free_list(bad):
+    """Pages come off the end: request 0 takes 9, the bad one and 8, request 1 takes 6."""
+    word, table, (slots, pos, cu, lens, left) = plan([[-1] * 4, [5, -1, -1, -1]], [0, 3], [9, 3], [7, 6, 8, bad, 9], 5, 4, 13)
+    assert word == pkg.FFPA_ERR_INVALID
+    assert table == [[9, bad, 8, -1], [5, 6, -1, -1]]
+    assert slots == [36, 37, 38, 39, -1, -1, -1, -1, 32, 23, 24, 25, -1]
+    assert pos == [0, 1, 2, 3, 4, 5, 6, 7, 8, 3, 4, 5, 0] and cu == [0, 9, 12] and lens == [9, 6] and left == [1]
+    device_ok()
+
+
+def test_negative_page_that_the_table_holds():
+    """In the page that the request goes on filling it is reported; where no new token falls it is not looked at."""
+    word, table, (slots, _, _, lens, left) = plan([[3, -1, -1, -1], [-1, 5, -1, -1]], [6, 6], [3, 1], [7, 8], 2, 4, 4)
+    assert word == pkg.FFPA_ERR_INVALID
+    assert table == [[3, -1, 8, -1], [-1, 5, -1, -1]] and slots == [-1, -1, 32, 22] and lens == [9, 7] and left == [1]
+    word, _, (slots, _, _, _, _) = plan([[3, -1, -1, -1], [-1, 5, -1, -1]], [6, 6], [0, 1], [7, 8], 2, 4, 1)
+    assert word == pkg.FFPA_OK and slots == [22]
+    device_ok()
+
+
+def test_negative_pages_are_not_reported_where_none_is_taken():
+    """Entries of the list behind free_count, and free pages that the step does not need, may be anything."""
+    word, _, (slots, _, _, _, left) = plan([[-1] * 2], [0], [4], [-1, -1, 2, -1], 3, 4, 4)
+    assert word == pkg.FFPA_OK and slots == [8, 9, 10, 11] and left == [2]
+    device_ok()
