@@ -1,9 +1,11 @@
-"""Negative pages in what a plan is given: reported, and their tokens without a slot."""
+"""What goes wrong in the paged calls is reported and ends: negative pages in what a plan is given, waits that
+run out in every way that decode brings its tiles."""
 import pytest
 import torch
 
 import exact_headdim_attention_gb300 as pkg
 from tests.gpu_util import device_ok
+from tests.test_gpu_paged import check_decode, decode_case
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -45,4 +47,18 @@ def test_negative_pages_are_not_reported_where_none_is_taken():
     """Entries of the list behind free_count, and free pages that the step does not need, may be anything."""
     word, _, (slots, _, _, _, left) = plan([[-1] * 2], [0], [4], [-1, -1, 2, -1], 3, 4, 4)
     assert word == pkg.FFPA_OK and slots == [8, 9, 10, 11] and left == [2]
+    device_ok()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (16, 1), (20, 1)])
+@pytest.mark.parametrize("D,page", [(64, 3), (512, 3), (512, 100), (1000, 20), (200, 16), (72, 100), (256, 16)])
+def test_decode_ends_when_a_wait_runs_out(D, page, Hq, Hkv):
+    """A copy that never starts, in pieces (pages of 3), in boxes that end with their page (100, 20), in boxes of
+    one chunk (D = 200, 72) and in whole ones: the timeout status after the call's limit, and a whole next call."""
+    args, ref = decode_case([300, 20, 0, 900], Hq, Hkv, D, page, torch.bfloat16, seed=D + page)
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkg.ffpa_decode_paged(*args, enable_gqa=True, status=word, wait_timeout_ns=3_000_000, test_drop_first_copy=True)
+    torch.cuda.synchronize()
+    assert word.item() == pkg.FFPA_ERR_DEVICE_TIMEOUT
+    check_decode(args, ref)
     device_ok()
