@@ -3,10 +3,12 @@
 One generation step of an attention layer:
 
     slots, positions, cu, lens, free_count = ffpa_page_plan(table, lens, new, free, free_count, page, tokens)
-    q = ffpa_kv_append(q, k, v, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight)
-    o = ffpa_decode_paged(q, k_cache, v_cache, table, lens)
+    q = ffpa_kv_append(q, k, v, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, rope_scale=scale)
+    last = (cu[1:] - 1).clamp(min=0)
+    o = ffpa_decode_paged(q[last], k_cache, v_cache, table, lens, enable_gqa=True)
 
-and of a training step: ``ffpa_qk_norm_rope_func`` (torch_ops.py; differentiable through
+with q, k, v the packed rows of the new tokens, (inv_freq, scale) those of training, and one row of
+o for each request: of its last new token (for a request without one it is of no use).  And of a training step: ``ffpa_qk_norm_rope_func`` (torch_ops.py; differentiable through
 ``ffpa_qk_norm_rope_bwd``), then ``ffpa_attn_func`` or ``ffpa_attn_varlen_func``.  The step's plan
 is shared by all layers.  As in _binding.py every computation runs in the CUDA kernels behind the C
 ABI (include/ffpa.h); tensors are checked, outputs allocated and the ABI called in
