@@ -13,8 +13,10 @@
 //    mix, and the host needs no lengths.  A pair that ends inside its CTA is
 //    written at once; a pair cut between CTAs leaves fp32 partial sums with
 //    their maximum and sum, which the second launch joins in the order of the CTAs.
-//  - Two rings of shared-memory tiles, one of K and one of V (some 200 KB an SM, all
-//    but the tiles in work in flight), are kept full by warps of their own.
+//  - Two rings of shared-memory tiles, one of K and one of V, are kept full by warps
+//    of their own.  They hold what fits of whole tiles: 192 KB an SM up to D = 256,
+//    and with two CTAs an SM 128 KB at D = 512 and 1024 (one K and one V tile of 32 KB
+//    a CTA; a third misses by 0.5 and 2.5 KB), 144 to 168 KB between.
 //    Where pages hold a multiple of 8 keys a tile arrives as tensor boxes of
 //    up to T rows of one page, with the 128-byte swizzle that the matrix
 //    loads want.  Of other page sizes the larger ones have tiles that end with
@@ -36,8 +38,9 @@
 //    its own and joined at the pair's end in the order of the groups.  P goes
 //    into the second product as two values of the input type (off by 2^-16 of
 //    P, fp16 2^-21), so that numerator and sum see the same weights.  (With P
-//    rounded once the error of O was 20 to 35 % larger; the second value costs
-//    0.3 to 2 %: B32 Hkv8 D512 201.3 -> 201.8 us, B2 Hq16 Hkv1 D256 107.7 -> 110.)
+//    rounded once the error of O was 20 to 35 % larger.  The second value costs
+//    0 to 4 % with up to 8 heads, B32 Hkv8 D512 201.3 -> 201.8 us, and 3 to 8 % with
+//    more: B2 Hq16 Hkv1 D256 104 -> 107, B32 Hq32 Hkv2 D512 98 -> 104.)
 //
 // Every wait on a copy has a time limit, after which the call's status word
 // receives FFPA_ERR_DEVICE_TIMEOUT and the CTA runs out without waiting.
@@ -90,11 +93,11 @@ struct DecodePlan {
 };
 
 // Heads of one pass: 8 NT.  A larger group is split over pairs that read the
-// same keys again (B64 Hq32 Hkv1 D512: 335 us in two passes of 16 heads; one
-// pass of 32 heads, whose accumulators leave the registers, 524).
+// same keys again (B64 Hq32 Hkv1 D512 of 4096 keys: 192 us in two passes of 16 heads; one
+// pass of 32 heads, whose accumulators leave the registers, took 1.56 times as long).
 __host__ __device__ constexpr int decode_nt(int group) { return group <= 8 ? 1 : 2; }
 // CTAs of an SM: two leave 96 registers a thread, too few for 16 heads (B32 Hq32
-// Hkv2 D512: 194 us with 8 computing warps an SM, 222 with 16).
+// Hkv2 D512 of 4096 keys: 104 us with 8 computing warps an SM; 16 took 1.14 times as long).
 __host__ __device__ constexpr int decode_ctas(int nt) { return nt == 1 ? 2 : 1; }
 // Parts of D in the first product, and groups of warps with keys of their own in the second.
 __host__ __device__ constexpr int decode_parts(int tile) { return tile >= 128 ? 1 : 128 / tile; }
@@ -191,8 +194,8 @@ __device__ __forceinline__ bool all_waited(uint32_t bar, uint32_t parity, const 
 }
 
 // The queries of the next pair on their way to L2, when its first values are asked
-// for: read by the pair itself they came 1 us late (B110 D512 of 1 to 87 keys 27.4 us
-// in place of 26.4).
+// for: read by the pair itself they came 1 us late (B110 D512 of 1 to 87 keys 28.6 us
+// in place of 27.4).
 __device__ __forceinline__ void fetch_queries(const DecodeParams& P, const Place& p, int heads) {
   const int hk = p.u / P.head_tiles, ht = p.u % P.head_tiles;
   const int rows = min(heads, P.group - ht * heads), lines = (P.D * 2 + 127) / 128;
@@ -1094,10 +1097,11 @@ ffpa_status ffpa_decode_paged(const void* q, const void* k_cache, const void* v_
   P.chunks = pl.chunks;
   // Boxes of as many rows as divide a page, down to the 8 of the swizzle.  Where a
   // page's size is no multiple of 8 but fills enough of a tile, a tile is one box that
-  // ends with its page (B32 Hkv8 D512 of 4096 keys, pages of 100: 317 us, in pieces
-  // 444); smaller pages of that kind come in pieces.  "Enough" is where both cost the
-  // same: a half (D512, 12 of 32 keys: 136 us, in pieces 118), and a third of the tiles
-  // of 128 and 256 keys (D64, 100 of 256 keys: 32 us, in pieces 45; D128, 36 of 128: 47, 45).
+  // ends with its page (B32 Hkv8 D512 of 4096 keys, pages of 100: 321 us, in pieces
+  // 454); smaller pages of that kind come in pieces.  "Enough" is where both cost the
+  // same: a half (that case with pages of 12, of 32 keys a tile: 580 us, in pieces 455), and a
+  // third of the tiles of 128 and 256 keys (B64 Hkv2 D64 of 3000 keys, pages of 100: 34 us, in
+  // pieces 45; D128 of 2000 keys, pages of 36: 51, 45).
   const bool by_page = page_size % 8 != 0 && page_size > (pl.tile - 1) / (pl.tile >= 128 ? 3 : 2);
   P.boxed = held && (page_size % 8 == 0 || by_page);
   P.page_tiles = by_page ? (page_size + pl.tile - 1) / pl.tile : 0;

@@ -61,11 +61,15 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
 // infinite): off by 2^-16, fp16 2^-21, of the value.
 template <bool F16>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& most, uint32_t& rest) {
-  if (F16)
+  float2 m;
+  if (F16) {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(most) : "f"(b), "f"(a));
-  else
-    most = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-  const float2 m = unpack2<F16>(most);
+    m = unpack2<F16>(most);
+  } else {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    most = __byte_perm(x, y, 0x7632);
+    m = make_float2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u));
+  }
   constexpr float more = 1.0f + 0x1p-23f;
   rest = pack2<F16>(fmaf(a, more, -m.x), fmaf(b, more, -m.y));
 }
