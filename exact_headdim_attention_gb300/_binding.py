@@ -43,7 +43,8 @@ class Options(ctypes.Structure):
 
 
 class Rope(ctypes.Structure):
-    """ffpa_rope of include/ffpa.h (norm weights, positions and frequencies of one call)."""
+    """ffpa_rope of include/ffpa.h (norm weights, positions and frequencies of one call), for programs that
+    call the C ABI through ctypes; the package's own calls are marshalled in csrc/paged_binding.cpp."""
     _fields_ = [("positions", ctypes.c_void_p), ("position_str_b", ctypes.c_int64), ("position_str_n", ctypes.c_int64),
                 ("position_bits", ctypes.c_int), ("rot_dim", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
                 ("interleaved", ctypes.c_int), ("rope_scale", ctypes.c_float),
@@ -130,6 +131,7 @@ def load_library(path: str | Path | None = None) -> ctypes.CDLL:
     lib.ffpa_bwd_noalloc.argtypes = sigs["ffpa_bwd"][:9] + sigs["ffpa_bwd"][10:]
     lib.ffpa_bwd_noalloc.restype = I
     L, Z, R = ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(Rope)
+    # (likewise; what paged.py calls itself are the workspace sizes)
     paged = {
         "ffpa_decode_paged": [P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P, L, P, P, I, P, Z, P, O],
         "ffpa_qk_norm_rope": [P, P, P, P, I, I, I, I, I, I, P, P, P, P, R, P],

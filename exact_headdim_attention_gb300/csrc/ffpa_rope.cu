@@ -52,9 +52,9 @@ __host__ __device__ constexpr int rope_row_bytes() {   // of one row, for all th
   return ROPE_THREADS * ITER * 2 * VEC * 2;
 }
 
-// Resident blocks an SM.  The 4-wide vectors fit three (T16384 D120: 62 us, with
-// two 74); more rows on their way than those of two blocks of 8-wide vectors
-// only slow the memory down (T8192 D512: 115 us, with three blocks 123).
+// Resident blocks an SM.  The 4-wide vectors fit three (T16384 D120: 54 us, with
+// two 64); more rows on their way than those of two blocks of 8-wide vectors
+// only slow the memory down (T8192 D512: 110 us, with three blocks 112).
 template <int VEC, int ITER>
 __host__ __device__ constexpr int rope_blocks() {
   return VEC == 4 && ITER == 1 ? 3 : 2;

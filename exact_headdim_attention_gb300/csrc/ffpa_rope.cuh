@@ -57,8 +57,8 @@ struct RopeParams {
 inline int rope_vec(int D, int rot) { return D % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
 // Heads that share a token's cosines and sines: 8 where the rows fill their
 // lanes (a power of two of chunks) and the memory is the bound, 16 where lanes
-// idle and the arithmetic weighs more (T8192 D512: 108 us with 8 and 120 with
-// 16; T8192 D320: 59 and 55; T16384 D120: 58 and 53); fewer where that would leave
+// idle and the arithmetic weighs more (T8192 D512: 110 us with 8 and 118 with
+// 16; T8192 D320: 61 and 55; T16384 D120: 60 and 54); fewer where that would leave
 // SMs without work.
 inline int rope_heads(int D, int rot, int64_t tokens, int H, int sms) {
   const int n = D / (2 * rope_vec(D, rot));

@@ -23,7 +23,7 @@ constexpr int RB_THREADS = 256;
 constexpr int RB_BLOCKS_MAX = 512;   // blocks of queries and keys together
 
 // Rows of the ring: more than three slow the one block of D > 512 down (T4096
-// D1024: 112 us, with four 115), four are best elsewhere.
+// D1024: 115 us, with four 119); elsewhere four are as good or better to 2 % (T8192 D512 92, 92).
 __host__ __device__ constexpr int rb_depth(int iter) { return iter == 1 ? 4 : 3; }
 
 template <int VEC, int ITER>
