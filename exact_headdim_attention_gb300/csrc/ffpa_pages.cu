@@ -126,28 +126,34 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32) plan_kernel(const PlanParams 
     P.cu_seqlens[b] = (int)(before_t < P.tokens ? before_t : P.tokens);
     P.lens_out[b] = (int)max(old, min(old + add, room));
   }
-  // This warp's stretch of the request's new tokens, and the pages that begin in it.
-  const unsigned step = gridDim.y * PLAN_STRETCH;
-  for (unsigned from = blockIdx.y * PLAN_STRETCH; from < add; from += step) {
-    const unsigned to = min(from + PLAN_STRETCH, add);
+  // New page j: the free list's entry, or -1 when the list has run out.  A page
+  // number is never negative, in the list and in what the table holds.
+  auto fresh = [&](unsigned j) { return j - held < got ? P.free_pages[count - 1 - (before_p + (j - held))] : -1; };
+  // This warp's stretch of the request's new tokens that have a row, and the pages that begin in it.
+  const long long rows = P.tokens - before_t;
+  const unsigned end = rows <= 0 ? 0 : rows < add ? (unsigned)rows : add, step = gridDim.y * PLAN_STRETCH;
+  for (unsigned from = blockIdx.y * PLAN_STRETCH; from < end; from += step) {
+    const unsigned to = min(from + PLAN_STRETCH, end);
     for (unsigned i = from + lane; i < to; i += 32) {
       const unsigned pos = old + i, j = pos / page_size, in = pos - j * page_size;
       const long long at = before_t + i;
-      // New page: the free list's entry, or -1 when the list has run out.  A page
-      // number is never negative, in the list and in what the table holds.
       int page = -1;
       if (j < held)
         page = table[j];
       else if (j < held + need) {
-        if (j - held < got) page = P.free_pages[count - 1 - (before_p + (j - held))];
+        page = fresh(j);
         if (in == 0) table[j] = page;
       }
       if (page < 0) report_invalid(P.err);
-      if (at < P.tokens) {
-        P.slots[at] = page < 0 ? -1 : (long long)page * page_size + in;
-        P.positions[at] = (int)pos;
-      }
+      P.slots[at] = page < 0 ? -1 : (long long)page * page_size + in;
+      P.positions[at] = (int)pos;
     }
+  }
+  // Pages that begin behind the last row (the call is reported): as many as the table takes,
+  // however many tokens the lengths name.
+  if (blockIdx.y == 0 && end < add) {
+    const unsigned next = old + end, j0 = next / page_size + (next % page_size != 0);
+    for (unsigned j = max(held, j0) + lane; j < held + need; j += 32) table[j] = fresh(j);
   }
 }
 

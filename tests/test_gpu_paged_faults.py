@@ -50,6 +50,41 @@ def test_negative_pages_are_not_reported_where_none_is_taken():
     device_ok()
 
 
+MOST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("new", [(MOST, 3), (MOST, MOST), (9, MOST)])
+def test_plan_of_lengths_beyond_any_table_is_short(new):
+    """The work goes by the step's rows and the table's pages, not by what the lengths name (a loop over
+    2^31 tokens would take seconds)."""
+    start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    plan([[7, -1, -1], [-1] * 3], [2, 0], [1, 1], [1, 2, 3, 4, 5], 5, 4, 6)          # (the kernel is loaded)
+    start.record()
+    word, table, (slots, pos, cu, lens, left) = plan([[7, -1, -1], [-1] * 3], [2, 0], new, [1, 2, 3, 4, 5], 5, 4, 6)
+    stop.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(stop) < 100
+    assert word == pkg.FFPA_ERR_INVALID
+    assert slots == [30, 31, 20, 21, 22, 23] and pos == [2, 3, 4, 5, 6, 7] and cu == [0, 6, 6]
+    pages = {3: 1, MOST: 3}[new[1]]                       # of request 1, from what request 0 left
+    assert table == [[7, 5, 4], [3, 2, 1][:pages] + [-1] * (3 - pages)]
+    assert lens == [12 if new[0] == MOST else 11, min(new[1], 4 * pages)] and left == [3 - pages]
+    device_ok()
+
+
+def test_plan_with_fewer_rows_than_tokens_still_enters_every_page():
+    """Pages that begin behind the last row, of requests in and behind it, each once."""
+    word, table, (slots, _, cu, lens, left) = plan([[-1] * 40, [6] + [-1] * 39, [-1] * 40], [0, 3, 0], [70, 50, 9],
+                                                   list(range(100, 200)), 100, 2, 21)
+    assert word == pkg.FFPA_ERR_INVALID and cu == [0, 21, 21, 21] and lens == [70, 53, 9]
+    free = list(range(199, 99, -1))
+    want = [free[:35], [6, -1] + free[35:60], free[60:65]]
+    for row, pages in zip(table, want):
+        assert row == pages + [-1] * (40 - len(pages))
+    assert slots == [free[t // 2] * 2 + t % 2 for t in range(21)] and left == [35]
+    device_ok()
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(4, 2), (16, 1), (20, 1)])
 @pytest.mark.parametrize("D,page", [(64, 3), (512, 3), (512, 100), (1000, 20), (200, 16), (72, 100), (256, 16)])
 def test_decode_ends_when_a_wait_runs_out(D, page, Hq, Hkv):
