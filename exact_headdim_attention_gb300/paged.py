@@ -13,6 +13,9 @@ o for each request: of its last new token (for a request without one it is of no
 is shared by all layers.  As in _binding.py every computation runs in the CUDA kernels behind the C
 ABI (include/ffpa.h); tensors are checked, outputs allocated and the ABI called in
 csrc/paged_binding.cpp, because calls that serve single tokens are as short as a few microseconds.
+
+A call on a stream of the caller's (stream=) makes its outputs in the current stream's memory, as the
+attention calls do: the caller orders the two streams and keeps the outputs until the call is done.
 """
 from __future__ import annotations
 

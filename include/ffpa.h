@@ -511,7 +511,8 @@ ffpa_status ffpa_bwd_noalloc(const void* q, const void* k, const void* v, const 
  *
  * D a multiple of 8 from 64 to 1024 (else FFPA_ERR_UNSUPPORTED); max_pages *
  * page_size at most 0x7fff0000.  Other checks and error codes as for
- * ffpa_fwd.  The result does not depend on the order in which the GPU runs
+ * ffpa_fwd.  Sums are fp32; a softmax weight enters them to 2^-16 of itself
+ * (fp16 2^-21, down to 2^-39 of the largest).  The result does not depend on the order in which the GPU runs
  * the blocks.  Two launches on `stream`; no allocation, no synchronisation.
  */
 size_t ffpa_decode_paged_workspace_bytes(int Hq, int Hkv, int D);
@@ -616,7 +617,7 @@ ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_
  * ceil(seq_lens[b] / page_size) pages of row b of block_table, and gets
  * new_lens[b] more (0: it waits).  Pages for them come off the end of the free
  * list free_pages[0 .. free_count[0]), in the order of the requests and then
- * of their pages, and are entered in the table.
+ * of their pages, and are entered in the table.  B and max_pages are at least 1.
  *
  *   block_table: int32 [B, max_pages], rows table_str apart; only the entries
  *     of new pages are written.
