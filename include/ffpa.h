@@ -512,7 +512,7 @@ ffpa_status ffpa_bwd_noalloc(const void* q, const void* k, const void* v, const 
  * D a multiple of 8 from 64 to 1024 (else FFPA_ERR_UNSUPPORTED); max_pages *
  * page_size at most 0x7fff0000.  Other checks and error codes as for
  * ffpa_fwd.  Sums are fp32; a softmax weight enters them to 2^-16 of itself
- * (fp16 2^-21, down to 2^-39 of the largest).  The result does not depend on the order in which the GPU runs
+ * (fp16: to 2^-21, or to 2^-40 of the largest).  The result does not depend on the order in which the GPU runs
  * the blocks.  Two launches on `stream`; no allocation, no synchronisation.
  */
 size_t ffpa_decode_paged_workspace_bytes(int Hq, int Hkv, int D);
