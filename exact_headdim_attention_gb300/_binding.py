@@ -29,7 +29,9 @@ EXPORTED = ("ffpa_fwd", "ffpa_fwd_ex", "ffpa_fwd_varlen", "ffpa_fwd_varlen_ex", 
             "ffpa_bwd_ws_ex", "ffpa_bwd_workspace_bytes", "ffpa_bwd_varlen_ws", "ffpa_bwd_varlen_ws_ex",
             "ffpa_bwd_varlen_workspace_bytes", "ffpa_decode_paged", "ffpa_decode_paged_workspace_bytes",
             "ffpa_qk_norm_rope", "ffpa_qk_norm_rope_bwd", "ffpa_qk_norm_rope_bwd_workspace_bytes",
-            "ffpa_kv_append", "ffpa_page_plan")
+            "ffpa_kv_append", "ffpa_page_plan", "ffpa_kv_append_fp8", "ffpa_decode_paged_fp8",
+            "ffpa_decode_paged_fp8_workspace_bytes", "ffpa_kv_read", "ffpa_decode_shared",
+            "ffpa_decode_shared_workspace_bytes")
 
 KERNEL_VARIANTS = {"auto": 0, "single": 1, "pair": 2, "split": 3, "dual": 4}
 
@@ -138,12 +140,20 @@ def load_library(path: str | Path | None = None) -> ctypes.CDLL:
         "ffpa_qk_norm_rope_bwd": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, P, P, R, P, Z, P],
         "ffpa_kv_append": [P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P, P, P, P, R, P, O],
         "ffpa_page_plan": [P, L, I, I, P, P, P, I, P, I, I, P, P, P, P, P, P, O],
+        "ffpa_kv_append_fp8": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P, P, P, P, P, P, R, P, O],
+        "ffpa_decode_paged_fp8": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P, P, P, L, P, P, I, P, Z, P, O],
+        "ffpa_kv_read": [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P, P, P, L, P, P, O],
+        "ffpa_decode_shared": [P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P, P, P, P, P, P, L, P, P, I, P, Z, P, O],
     }
     for name, args in paged.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
     lib.ffpa_decode_paged_workspace_bytes.argtypes = [I, I, I]
     lib.ffpa_decode_paged_workspace_bytes.restype = Z
+    lib.ffpa_decode_paged_fp8_workspace_bytes.argtypes = [I, I, I]
+    lib.ffpa_decode_paged_fp8_workspace_bytes.restype = Z
+    lib.ffpa_decode_shared_workspace_bytes.argtypes = [I, I, I, I]
+    lib.ffpa_decode_shared_workspace_bytes.restype = Z
     lib.ffpa_qk_norm_rope_bwd_workspace_bytes.argtypes = [I]
     lib.ffpa_qk_norm_rope_bwd_workspace_bytes.restype = Z
     lib.ffpa_status_string.argtypes = [I]

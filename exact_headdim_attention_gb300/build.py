@@ -24,8 +24,12 @@ OUT = PKG / "_build" / "libffpa.so"
 SOURCES = [CSRC / n for n in ("ffpa_cluster.cu", "ffpa_split.cu", "ffpa_bwd.cu", "ffpa_bwd_tiles.cu",
                               "ffpa_pair.cu", "ffpa_fp8.cu", "ffpa_fp8_split.cu", "ffpa_single.cu",
                               "ffpa_dual.cu", "ffpa_api.cu", "ffpa_noalloc.cu", "ffpa_decode.cu",
-                              "ffpa_rope.cu", "ffpa_rope_bwd.cu", "ffpa_pages.cu")]
-DEPS = SOURCES + [CSRC / "ffpa_paged.cuh", CSRC / "ffpa_rope.cuh", CSRC / "ffpa_common.cuh", CSRC / "ffpa_bwd_common.cuh", CSRC / "ptx.cuh", INCLUDE / "ffpa.h"]
+                              "ffpa_decode_fp8.cu",
+                              "ffpa_shared.cu", "ffpa_rope.cu", "ffpa_append_fp8.cu", "ffpa_rope_bwd.cu",
+                              "ffpa_pages.cu", "ffpa_read.cu")]
+DEPS = SOURCES + [CSRC / "ffpa_paged.cuh", CSRC / "ffpa_decode.cuh", CSRC / "ffpa_rope_fwd.cuh",
+                   CSRC / "ffpa_rope.cuh", CSRC / "ffpa_common.cuh", CSRC / "ffpa_bwd_common.cuh",
+                  CSRC / "ptx.cuh", INCLUDE / "ffpa.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -593,6 +593,11 @@ ffpa_status encode_rows(CUtensorMap* map, ffpa_dtype dt, int rank, const void* b
                     base, dims, stride_bytes, box);
 }
 
+ffpa_status encode_codes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* stride_bytes,
+                         const uint32_t* box) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, base, dims, stride_bytes, box);
+}
+
 // Kernels whose shared-memory limit was raised, per device (set-once facts).
 ffpa_status set_smem_attr_once(const void* fn, int device, int bytes) {
   struct Entry {

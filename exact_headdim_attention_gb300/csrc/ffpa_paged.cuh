@@ -1,6 +1,6 @@
 #pragma once
-// Shared by the operators around a paged key/value cache (ffpa_decode.cu,
-// ffpa_rope.cu, ffpa_rope_bwd.cu, ffpa_pages.cu): the host checks they have
+// Shared by the operators around a paged key/value cache (ffpa_decode.cuh,
+// ffpa_rope.cuh, ffpa_rope_bwd.cu, ffpa_pages.cu): the host checks they have
 // in common with the attention entry points, and small device helpers.
 #include <initializer_list>
 
@@ -22,19 +22,28 @@ ffpa_status call_status(int dev, const ffpa_options* options, int** err, int* sm
 ffpa_status encode_rows(CUtensorMap* map, ffpa_dtype dt, int rank, const void* base, const uint64_t* dims,
                         const uint64_t* stride_bytes, const uint32_t* box);
 
+// The same of boxes of 128 8-bit values.
+ffpa_status encode_codes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* stride_bytes,
+                         const uint32_t* box);
+
 inline bool on_boundary(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // As for the attention inputs: unit last stride, every other stride of a
-// dimension longer than 1 positive and a multiple of 16 bytes.
-inline bool rows_ok(const int64_t* str, std::initializer_list<int64_t> sizes) {
+// dimension longer than 1 positive and a multiple of 16 bytes (`unit` values).
+inline bool rows_ok(const int64_t* str, std::initializer_list<int64_t> sizes, int unit = 8) {
   int i = 0;
   const int rank = static_cast<int>(sizes.size());
   for (int64_t n : sizes) {
     if (i == rank - 1) return str[i] == 1;
-    if (n > 1 && (str[i] <= 0 || str[i] % 8 != 0)) return false;
+    if (n > 1 && (str[i] <= 0 || str[i] % unit != 0)) return false;
     ++i;
   }
   return true;
+}
+
+// Strides (page, head, slot) of rows' scales: the slots of a page adjacent.
+inline bool scales_ok(const int64_t* str, int pages, int heads, int page_size) {
+  return (pages <= 1 || str[0] > 0) && (heads <= 1 || str[1] > 0) && (page_size <= 1 || str[2] == 1);
 }
 
 // ---- device
@@ -85,6 +94,10 @@ __device__ __forceinline__ void store16(void* p, float x) {
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes));
 }
+// Four bytes likewise.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes));
+}
 // N (8 or 16) bytes, for the copying thread's own use.
 template <int N>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
@@ -115,6 +128,15 @@ __device__ __forceinline__ void ldm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// Four e4m3 codes as fp16 (which holds every one of them): the lower two, the upper two.
+__device__ __forceinline__ void widen_e4m3(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 // C [16 x 8] += A [16 x 16] B [16 x 8], 16-bit operands, fp32 accumulators.
 template <bool F16>

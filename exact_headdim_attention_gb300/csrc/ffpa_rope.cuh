@@ -44,6 +44,8 @@ struct RopeParams {
   const char* v;
   int64_t vs[2], kcs[3], vcs[3];   // byte strides (h, n); (page, slot, h)
   unsigned items_v;    // and of values
+  float *k_scale, *v_scale;        // of e4m3 rows; element strides (page, head)
+  int64_t k_scale_s[2], v_scale_s[2];
   int* err;
   // backward
   const char* g[2];    // gradients of the outputs

@@ -10,6 +10,7 @@
 #include <ATen/FunctionalTensorWrapper.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -28,6 +29,11 @@ struct Abi {
   decltype(&ffpa_qk_norm_rope_bwd_workspace_bytes) rope_bwd_bytes = nullptr;
   decltype(&ffpa_kv_append) append = nullptr;
   decltype(&ffpa_page_plan) plan = nullptr;
+  decltype(&ffpa_kv_append_fp8) append_fp8 = nullptr;
+  decltype(&ffpa_decode_paged_fp8) decode_fp8 = nullptr;
+  decltype(&ffpa_kv_read) read = nullptr;
+  decltype(&ffpa_decode_shared) shared = nullptr;
+  decltype(&ffpa_decode_shared_workspace_bytes) shared_bytes = nullptr;
 } abi;
 
 // ---- arguments
@@ -125,6 +131,16 @@ void check_cache(const Tensor& kc, const Tensor& vc, at::ScalarType type, int64_
   TORCH_CHECK_TYPE(kc.scalar_type() == type && vc.scalar_type() == type, "the cache must be ", type, ", got ",
                    kc.scalar_type(), " and ", vc.scalar_type());
   TORCH_CHECK_VALUE(kc.size(3) == D, "the cache has head dim ", kc.size(3), ", the call ", D);
+}
+
+// Scales of e4m3 rows, for the caches they belong to.
+void check_scales(const Tensor& ks, const Tensor& vs, const Tensor& cache) {
+  TORCH_CHECK_TYPE(ks.scalar_type() == at::kFloat && vs.scalar_type() == at::kFloat, "k_scale and v_scale must be float32, got ",
+                   ks.scalar_type(), " and ", vs.scalar_type());
+  const int64_t want[3] = {cache.size(0), cache.size(2), cache.size(1)};
+  TORCH_CHECK_VALUE(ks.sizes() == at::IntArrayRef(want, 3) && vs.sizes() == ks.sizes(),
+                    "k_scale and v_scale must have shape [num_pages, Hkv, page_size] = ", at::IntArrayRef(want, 3), ", got ",
+                    ks.sizes(), " and ", vs.sizes());
 }
 
 // Queries and keys [B, H, N, D] or packed [T, H, D].  (That every tensor of a
@@ -271,64 +287,156 @@ PyObject* py_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (q, k, v, k_cache, v_cache, slots, <rope: 7>, q_out, stream, options)
-PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  count(n, 16);
+// (q, k, v, k_cache, v_cache, [k_scale, v_scale,] slots, <rope: 7>, q_out, stream, options)
+PyObject* append(PyObject* const* a, Py_ssize_t n, bool fp8) {
+  count(n, fp8 ? 18 : 16);
   const Tensor* q = maybe(a[0], "q");
   const Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache");
+  const Tensor *ks = fp8 ? &tensor(a[5], "k_scale") : nullptr, *vs = fp8 ? &tensor(a[6], "v_scale") : nullptr;
+  PyObject* const* r = a + (fp8 ? 7 : 5);          // slots and what follows
   TORCH_CHECK_VALUE(k.dim() == 3 && v.sizes() == k.sizes(), "k and v must be 3-D [T, Hkv, D] of one shape");
   TORCH_CHECK_TYPE(v.scalar_type() == k.scalar_type(), "k and v must share one dtype");
   const Shape s = qk_shape(q ? *q : k, k);
-  TORCH_CHECK_VALUE(q || (a[13] == Py_None && a[8] == Py_None), "q_out and q_weight need q");
-  check_cache(kc, vc, k.scalar_type(), s.D);
+  TORCH_CHECK_VALUE(q || (r[8] == Py_None && r[3] == Py_None), "q_out and q_weight need q");
+  check_cache(kc, vc, fp8 ? at::kFloat8_e4m3fn : k.scalar_type(), s.D);
   TORCH_CHECK_VALUE(kc.size(2) == s.Hkv, "the cache has ", kc.size(2), " key heads, the keys have ", s.Hkv);
-  const Tensor& slots = integers(a[5], "slots", s.N, at::kLong);
-  const ffpa_rope r = rope_of(a + 6, k, s);
+  if (fp8) check_scales(*ks, *vs, kc);
+  const Tensor& slots = integers(r[0], "slots", s.N, at::kLong);
+  const ffpa_rope rope = rope_of(r + 1, k, s);
   Tensor qo;
-  if (q) qo = output(a[13], "q_out", q->sizes(), q->scalar_type(), *q);
+  if (q) qo = output(r[8], "q_out", q->sizes(), q->scalar_type(), *q);
   const int pages = small(kc.size(0), "num_pages"), page = small(kc.size(1), "page_size");
-  const ffpa_stream_t stream = stream_of(a[14], k);
-  const ffpa_options* opt = options(a[15]);
+  const ffpa_stream_t stream = stream_of(r[9], k);
+  const ffpa_options* opt = options(r[10]);
+  const int64_t *qs = q ? q->strides().data() : nullptr, *qos = q ? qo.strides().data() : nullptr;
+  void* qp = q ? qo.data_ptr() : nullptr;
+  const int64_t* at = static_cast<const int64_t*>(slots.const_data_ptr());
   const ffpa_status st = call([&] {
-    return abi.append(ptr(q), k.const_data_ptr(), v.const_data_ptr(), q ? qo.data_ptr() : nullptr, kc.data_ptr(),
-                      vc.data_ptr(), dtype_of(k), s.N, s.Hq, s.Hkv, s.D, pages, page, q ? q->strides().data() : nullptr,
-                      k.strides().data(), v.strides().data(), q ? qo.strides().data() : nullptr, kc.strides().data(),
-                      vc.strides().data(), static_cast<const int64_t*>(slots.const_data_ptr()), &r, stream, opt);
+    if (fp8)
+      return abi.append_fp8(ptr(q), k.const_data_ptr(), v.const_data_ptr(), qp, kc.data_ptr(), vc.data_ptr(),
+                            static_cast<float*>(ks->data_ptr()), static_cast<float*>(vs->data_ptr()), dtype_of(k), s.N, s.Hq,
+                            s.Hkv, s.D, pages, page, qs, k.strides().data(), v.strides().data(), qos, kc.strides().data(),
+                            vc.strides().data(), ks->strides().data(), vs->strides().data(), at, &rope, stream, opt);
+    return abi.append(ptr(q), k.const_data_ptr(), v.const_data_ptr(), qp, kc.data_ptr(), vc.data_ptr(), dtype_of(k), s.N,
+                      s.Hq, s.Hkv, s.D, pages, page, qs, k.strides().data(), v.strides().data(), qos, kc.strides().data(),
+                      vc.strides().data(), at, &rope, stream, opt);
   });
   return st == FFPA_OK ? wrap(qo) : status(st);
+}
+PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return append(a, n, false);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* py_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return append(a, n, true);
   END_HANDLE_TH_ERRORS
 }
 
-// (q, k_cache, v_cache, block_table, seq_lens, scale, enable_gqa, return_lse, out, lse, workspace, stream, options)
-PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  count(n, 13);
+// (q, k_cache, v_cache, [k_scale, v_scale | shared_pages, shared_len,] block_table, seq_lens, scale, enable_gqa,
+// return_lse, out, lse, workspace, stream, options)
+enum class Decode { plain, fp8, shared };
+PyObject* decode(PyObject* const* a, Py_ssize_t n, Decode kind) {
+  const bool fp8 = kind == Decode::fp8, shared = kind == Decode::shared;
+  count(n, fp8 || shared ? 15 : 13);
   const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
+  const Tensor *ks = fp8 ? &tensor(a[3], "k_scale") : nullptr, *vs = fp8 ? &tensor(a[4], "v_scale") : nullptr;
+  const Tensor *sp = shared ? &integers(a[3], "shared_pages", -1, at::kInt) : nullptr;
+  const Tensor *sl = shared ? &integers(a[4], "shared_len", 1, at::kInt) : nullptr;
+  PyObject* const* r = a + (fp8 || shared ? 5 : 3);   // block_table and what follows
   TORCH_CHECK_VALUE(q.dim() == 3, "q must be 3-D [B, Hq, D]");
   const int B = small(q.size(0), "B"), Hq = small(q.size(1), "Hq"), D = small(q.size(2), "D");
-  check_cache(kc, vc, q.scalar_type(), D);
-  const Tensor& table = table_of(a[3]);
+  check_cache(kc, vc, fp8 ? at::kFloat8_e4m3fn : q.scalar_type(), D);
+  if (fp8) check_scales(*ks, *vs, kc);
+  const Tensor& table = table_of(r[0]);
   TORCH_CHECK_VALUE(table.size(0) == B, "block_table has ", table.size(0), " rows for ", B, " requests");
-  const Tensor& lens = integers(a[4], "seq_lens", B, at::kInt);
+  const Tensor& lens = integers(r[1], "seq_lens", B, at::kInt);
   const int pages = small(kc.size(0), "num_pages"), page = small(kc.size(1), "page_size"), Hkv = small(kc.size(2), "Hkv");
-  const bool scaled = a[5] != Py_None, gqa = truth(a[6]), want = truth(a[7]);
-  const float scale = scaled ? number(a[5]) : 0.0f;
-  const Tensor out = output(a[8], "out", q.sizes(), q.scalar_type(), q);
+  const bool scaled = r[2] != Py_None, gqa = truth(r[3]), want = truth(r[4]);
+  const float scale = scaled ? number(r[2]) : 0.0f;
+  const Tensor out = output(r[5], "out", q.sizes(), q.scalar_type(), q);
   Tensor lse;
-  if (want || a[9] != Py_None) lse = output(a[9], "lse", {B, Hq}, at::kFloat, q, true);
-  const Tensor ws = workspace(a[10], abi.decode_bytes(Hq, Hkv, D), q);
-  const ffpa_stream_t stream = stream_of(a[11], q);
-  const ffpa_options* opt = options(a[12]);
+  if (want || r[6] != Py_None) lse = output(r[6], "lse", {B, Hq}, at::kFloat, q, true);
+  const Tensor ws = workspace(r[7], shared ? abi.shared_bytes(B, Hq, Hkv, D) : abi.decode_bytes(Hq, Hkv, D), q);
+  const ffpa_stream_t stream = stream_of(r[8], q);
+  const ffpa_options* opt = options(r[9]);
+  float* lp = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
+  const int width = small(table.size(1), "max_pages");
+  auto ints = [](const Tensor& t) { return static_cast<const int32_t*>(t.const_data_ptr()); };
+  const int64_t *qs = q.strides().data(), *kcs = kc.strides().data(), *vcs = vc.strides().data(), *os = out.strides().data();
   const ffpa_status st = call([&] {
-    return abi.decode(q.const_data_ptr(), kc.const_data_ptr(), vc.const_data_ptr(), out.data_ptr(),
-                      lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, dtype_of(q), B, Hq, Hkv, D, pages,
-                      page, static_cast<int>(table.size(1)), q.strides().data(), kc.strides().data(),
-                      vc.strides().data(), out.strides().data(), static_cast<const int32_t*>(table.const_data_ptr()),
-                      table.stride(0), static_cast<const int32_t*>(lens.const_data_ptr()), scaled ? &scale : nullptr, gqa,
-                      ws.data_ptr(), static_cast<size_t>(ws.numel()), stream, opt);
+    if (fp8)
+      return abi.decode_fp8(q.const_data_ptr(), kc.const_data_ptr(), vc.const_data_ptr(),
+                            static_cast<const float*>(ks->const_data_ptr()), static_cast<const float*>(vs->const_data_ptr()),
+                            out.data_ptr(), lp, dtype_of(q), B, Hq, Hkv, D, pages, page, width, qs, kcs, vcs,
+                            ks->strides().data(), vs->strides().data(), os, ints(table), table.stride(0), ints(lens),
+                            scaled ? &scale : nullptr, gqa, ws.data_ptr(), static_cast<size_t>(ws.numel()), stream, opt);
+    if (shared)
+      return abi.shared(q.const_data_ptr(), kc.const_data_ptr(), vc.const_data_ptr(), out.data_ptr(), lp, dtype_of(q), B, Hq,
+                        Hkv, D, pages, page, width, small(sp->size(0), "shared_pages"), qs, kcs, vcs, os, ints(*sp), ints(*sl),
+                        ints(table), table.stride(0), ints(lens), scaled ? &scale : nullptr, gqa, ws.data_ptr(),
+                        static_cast<size_t>(ws.numel()), stream, opt);
+    return abi.decode(q.const_data_ptr(), kc.const_data_ptr(), vc.const_data_ptr(), out.data_ptr(), lp, dtype_of(q), B, Hq,
+                      Hkv, D, pages, page, width, qs, kcs, vcs, os, ints(table), table.stride(0), ints(lens),
+                      scaled ? &scale : nullptr, gqa, ws.data_ptr(), static_cast<size_t>(ws.numel()), stream, opt);
   });
   return st != FFPA_OK ? status(st) : want ? tuple({out, lse}) : wrap(out);
+}
+PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return decode(a, n, Decode::plain);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* py_decode_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return decode(a, n, Decode::fp8);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* py_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return decode(a, n, Decode::shared);
+  END_HANDLE_TH_ERRORS
+}
+
+// (k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, num_tokens, dtype, k_out, v_out, stream, options)
+PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 12);
+  const Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache");
+  const Tensor *ks = maybe(a[2], "k_scale"), *vs = maybe(a[3], "v_scale");
+  const Tensor& table = table_of(a[4]);
+  const Tensor& cu = integers(a[5], "cu_seqlens", table.size(0) + 1, at::kInt);
+  const int T = small(integer(a[6]), "num_tokens");
+  TORCH_CHECK_VALUE(T >= 0, "num_tokens must not be negative");
+  TORCH_CHECK_VALUE(kc.dim() == 4, "k_cache and v_cache must be 4-D [num_pages, page_size, Hkv, D]");
+  const bool codes = kc.scalar_type() == at::kFloat8_e4m3fn;
+  check_cache(kc, vc, kc.scalar_type(), kc.size(3));
+  TORCH_CHECK_VALUE(codes == (ks != nullptr) && codes == (vs != nullptr),
+                    "k_scale and v_scale belong to a float8_e4m3fn cache, and it to them");
+  if (codes) check_scales(*ks, *vs, kc);
+  at::ScalarType type = codes ? at::kBFloat16 : kc.scalar_type();
+  if (a[7] != Py_None) {
+    TORCH_CHECK_TYPE(THPDtype_Check(a[7]), "dtype must be a torch.dtype");
+    type = reinterpret_cast<THPDtype*>(a[7])->scalar_type;
+  }
+  TORCH_CHECK_TYPE(type == at::kBFloat16 || type == at::kHalf, "rows are read as bfloat16 or float16, got ", type);
+  TORCH_CHECK_TYPE(codes || type == kc.scalar_type(), "a 16-bit cache is read as what it holds, ", kc.scalar_type());
+  const int Hkv = small(kc.size(2), "Hkv"), D = small(kc.size(3), "D");
+  const int pages = small(kc.size(0), "num_pages"), page = small(kc.size(1), "page_size"), B = small(table.size(0), "B");
+  const Tensor k = output(a[8], "k_out", {T, Hkv, D}, type, kc), v = output(a[9], "v_out", {T, Hkv, D}, type, kc);
+  const int width = small(table.size(1), "max_pages");
+  const ffpa_stream_t stream = stream_of(a[10], kc);
+  const ffpa_options* opt = options(a[11]);
+  const ffpa_status st = call([&] {
+    return abi.read(kc.const_data_ptr(), vc.const_data_ptr(), static_cast<const float*>(ptr(ks)),
+                    static_cast<const float*>(ptr(vs)), k.data_ptr(), v.data_ptr(), dtype_of(k), T, B, Hkv, D, pages, page,
+                    width, kc.strides().data(), vc.strides().data(), ks ? ks->strides().data() : nullptr,
+                    vs ? vs->strides().data() : nullptr, k.strides().data(), v.strides().data(),
+                    static_cast<const int32_t*>(table.const_data_ptr()), table.stride(0),
+                    static_cast<const int32_t*>(cu.const_data_ptr()), stream, opt);
+  });
+  return st == FFPA_OK ? tuple({k, v}) : status(st);
   END_HANDLE_TH_ERRORS
 }
 
@@ -360,9 +468,9 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // The addresses of the library's functions, in the order of Abi.
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  count(n, 7);
-  void* p[7];
-  for (int i = 0; i < 7; ++i) p[i] = reinterpret_cast<void*>(integer(a[i]));
+  count(n, 12);
+  void* p[12];
+  for (int i = 0; i < 12; ++i) p[i] = reinterpret_cast<void*>(integer(a[i]));
   abi.decode = reinterpret_cast<decltype(abi.decode)>(p[0]);
   abi.decode_bytes = reinterpret_cast<decltype(abi.decode_bytes)>(p[1]);
   abi.rope = reinterpret_cast<decltype(abi.rope)>(p[2]);
@@ -370,6 +478,11 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   abi.rope_bwd_bytes = reinterpret_cast<decltype(abi.rope_bwd_bytes)>(p[4]);
   abi.append = reinterpret_cast<decltype(abi.append)>(p[5]);
   abi.plan = reinterpret_cast<decltype(abi.plan)>(p[6]);
+  abi.append_fp8 = reinterpret_cast<decltype(abi.append_fp8)>(p[7]);
+  abi.decode_fp8 = reinterpret_cast<decltype(abi.decode_fp8)>(p[8]);
+  abi.read = reinterpret_cast<decltype(abi.read)>(p[9]);
+  abi.shared = reinterpret_cast<decltype(abi.shared)>(p[10]);
+  abi.shared_bytes = reinterpret_cast<decltype(abi.shared_bytes)>(p[11]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -378,6 +491,8 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {FFPA_PY("bind", py_bind),         FFPA_PY("qk_norm_rope", py_rope),
                          FFPA_PY("qk_norm_rope_bwd", py_rope_bwd), FFPA_PY("kv_append", py_append),
                          FFPA_PY("decode_paged", py_decode), FFPA_PY("page_plan", py_plan),
+                         FFPA_PY("kv_append_fp8", py_append_fp8), FFPA_PY("decode_paged_fp8", py_decode_fp8),
+                         FFPA_PY("kv_read", py_read), FFPA_PY("decode_shared", py_shared),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "ffpa_paged_binding", nullptr, -1, methods,
                           nullptr,               nullptr,              nullptr, nullptr};

@@ -30,7 +30,8 @@ from . import build as _build
 from ._binding import _options, _raise, load_library
 
 _BOUND = ("ffpa_decode_paged", "ffpa_decode_paged_workspace_bytes", "ffpa_qk_norm_rope", "ffpa_qk_norm_rope_bwd",
-          "ffpa_qk_norm_rope_bwd_workspace_bytes", "ffpa_kv_append", "ffpa_page_plan")
+          "ffpa_qk_norm_rope_bwd_workspace_bytes", "ffpa_kv_append", "ffpa_page_plan", "ffpa_kv_append_fp8",
+          "ffpa_decode_paged_fp8", "ffpa_kv_read", "ffpa_decode_shared", "ffpa_decode_shared_workspace_bytes")
 _module = _bound_to = None
 
 
@@ -212,6 +213,93 @@ def ffpa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                                workspace, _handle(stream), options)
     if type(r) is int:
         _raise(r, "ffpa_decode_paged")
+    return r
+
+
+def ffpa_kv_append_fp8(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_scale: torch.Tensor, v_scale: torch.Tensor, slots: torch.Tensor, positions=None, inv_freq=None,
+                       q_weight=None, k_weight=None, *, eps: float = 1e-6, interleaved: bool = False,
+                       rope_scale: float = 1.0, q_out=None, stream=None, status=None):
+    """ffpa_kv_append into a cache of 8 bits a value, through ``ffpa_kv_append_fp8``.
+
+    k_cache, v_cache float8_e4m3fn [num_pages,page_size,Hkv,D] (D a multiple of 16); k_scale, v_scale
+    float32 [num_pages,Hkv,page_size] (a page's slots adjacent).  Each row (a key head, normed and
+    rotated in fp32, or a value head) is stored as e4m3(y * (448 / max|y|)) with the scale max|y| / 448,
+    a row of zeros with scale 1.  Other arguments and the result as for ffpa_kv_append."""
+    keep, options = _call_options(k, status)
+    r = _native().kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positions, inv_freq, q_weight,
+                                k_weight, eps, interleaved, rope_scale, q_out, _handle(stream), options)
+    if type(r) is int:
+        _raise(r, "ffpa_kv_append_fp8")
+    return r
+
+
+def ffpa_decode_paged_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                          v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *,
+                          scale: float | None = None, enable_gqa: bool = False, return_lse: bool = False, out=None,
+                          lse=None, workspace=None, stream=None, status=None, wait_timeout_ns=None,
+                          test_drop_first_copy=False):
+    """ffpa_decode_paged over the cache that ffpa_kv_append_fp8 writes, through ``ffpa_decode_paged_fp8``.
+
+    The attention of codes times scales; q and the result bf16 or fp16.  Scales are not negative.  Other
+    arguments, workspace and the result as for ffpa_decode_paged."""
+    if stream is not None:
+        workspace = _on_stream(workspace, decode_paged_workspace_bytes(q.shape[1], k_cache.shape[2], q.shape[2]), q,
+                               stream)
+    keep, options = _call_options(q, status, wait_timeout_ns, test_drop_first_copy)
+    r = _native().decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale, enable_gqa,
+                                   return_lse, out, lse, workspace, _handle(stream), options)
+    if type(r) is int:
+        _raise(r, "ffpa_decode_paged_fp8")
+    return r
+
+
+def ffpa_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                 num_tokens: int, *, k_scale=None, v_scale=None, dtype=None, k_out=None, v_out=None, stream=None,
+                 status=None):
+    """The cached rows of a batch, packed: (k, v) [num_tokens,Hkv,D], through ``ffpa_kv_read``.
+
+    Row cu_seqlens[b] + i is key (value) i of request b; cu_seqlens int32 [B+1] on the device.  With them a
+    prompt behind a cached context attends: ffpa_attn_varlen_func(q, k, v, cu_q, cu_seqlens, ...,
+    causal=True).  A float8_e4m3fn cache comes with its scales and is read as dtype (bf16 when None, or
+    fp16): code times scale, rounded once; a 16-bit cache is copied as it is.  num_tokens: rows of the
+    result; those behind cu_seqlens[B] are left as they are (k_out, v_out).  Lengths and pages out of
+    range are not followed; the status word (see ffpa_fwd) receives FFPA_ERR_INVALID, and a key without a page is
+    zeros."""
+    keep, options = _call_options(k_cache, status)
+    r = _native().kv_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, num_tokens, dtype, k_out, v_out,
+                          _handle(stream), options)
+    if type(r) is int:
+        _raise(r, "ffpa_kv_read")
+    return r
+
+
+def decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of the workspace of ffpa_decode_shared, for any lengths (0 for unsupported heads)."""
+    return int(load_library().ffpa_decode_shared_workspace_bytes(B, Hq, Hkv, D))
+
+
+def ffpa_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, shared_pages: torch.Tensor,
+                       shared_len: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *,
+                       scale: float | None = None, enable_gqa: bool = False, return_lse: bool = False, out=None,
+                       lse=None, workspace=None, stream=None, status=None, wait_timeout_ns=None,
+                       test_drop_first_copy=False):
+    """ffpa_decode_paged for requests that begin with the same tokens, through ``ffpa_decode_shared``.
+
+    The first shared_len[0] keys (int32 [1]; whole pages of them count) of every request lie in shared_pages
+    (int32 [n], in order), which are read and multiplied once for the whole batch.  block_table and
+    seq_lens are those of ffpa_decode_paged, the shared keys included; the entries of the shared pages in
+    block_table are not read, and a request of fewer keys sees that many.  D a multiple of 64, page_size
+    of 8.  Other arguments and the result as for ffpa_decode_paged; workspace: of
+    decode_shared_workspace_bytes(...) bytes."""
+    if stream is not None:
+        need = decode_shared_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2])
+        workspace = _on_stream(workspace, need, q, stream)
+    keep, options = _call_options(q, status, wait_timeout_ns, test_drop_first_copy)
+    r = _native().decode_shared(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale, enable_gqa,
+                                return_lse, out, lse, workspace, _handle(stream), options)
+    if type(r) is int:
+        _raise(r, "ffpa_decode_shared")
     return r
 
 

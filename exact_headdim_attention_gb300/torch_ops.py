@@ -356,6 +356,107 @@ def ffpa_attn_decode_func(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     return (o, lse) if return_lse else o
 
 
+@torch.library.custom_op("ffpa::kv_append_fp8", mutates_args=("k_cache", "v_cache", "k_scale", "v_scale"))
+def kv_append_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, slots: torch.Tensor,
+                  positions: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                  k_weight: Optional[torch.Tensor], eps: float, interleaved: bool, rope_scale: float) -> torch.Tensor:
+    """Keys and values into cache slots as codes and scales; the normed and rotated queries (no rows without q)."""
+    out = paged.ffpa_kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positions, inv_freq, q_weight,
+                                   k_weight, eps=eps, interleaved=interleaved, rope_scale=rope_scale)
+    return k.new_empty((0,) + tuple(k.shape[1:])) if out is None else out
+
+
+@kv_append_fp8.register_fake
+def _kv_append_fp8_fake(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positions, inv_freq, q_weight, k_weight,
+                        eps, interleaved, rope_scale):
+    return _kv_append_fake(q, k, v, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps, interleaved,
+                           rope_scale)
+
+
+@torch.library.custom_op("ffpa::decode_paged_fp8", mutates_args=())
+def decode_paged_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                     v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, scale: Optional[float],
+                     enable_gqa: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    """O [B,Hq,D] and LSE [B,Hq] (fp32) of one new token per request over a paged cache of codes."""
+    return paged.ffpa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale=scale,
+                                       enable_gqa=enable_gqa, return_lse=True)
+
+
+@decode_paged_fp8.register_fake
+def _decode_paged_fp8_fake(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale, enable_gqa):
+    return _decode_paged_fake(q, k_cache, v_cache, block_table, seq_lens, scale, enable_gqa)
+
+
+@torch.library.custom_op("ffpa::decode_shared", mutates_args=())
+def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, shared_pages: torch.Tensor,
+                  shared_len: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, scale: Optional[float],
+                  enable_gqa: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    """O [B,Hq,D] and LSE [B,Hq] (fp32) of one new token per request behind shared pages."""
+    return paged.ffpa_decode_shared(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale=scale,
+                                    enable_gqa=enable_gqa, return_lse=True)
+
+
+@decode_shared.register_fake
+def _decode_shared_fake(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale, enable_gqa):
+    return _decode_paged_fake(q, k_cache, v_cache, block_table, seq_lens, scale, enable_gqa)
+
+
+@torch.library.custom_op("ffpa::kv_read", mutates_args=())
+def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+            num_tokens: int, k_scale: Optional[torch.Tensor], v_scale: Optional[torch.Tensor],
+            dtype: Optional[torch.dtype]) -> tuple[torch.Tensor, torch.Tensor]:
+    """Packed cached rows k, v [num_tokens,Hkv,D]."""
+    return paged.ffpa_kv_read(k_cache, v_cache, block_table, cu_seqlens, num_tokens, k_scale=k_scale, v_scale=v_scale,
+                              dtype=dtype)
+
+
+@kv_read.register_fake
+def _kv_read_fake(k_cache, v_cache, block_table, cu_seqlens, num_tokens, k_scale, v_scale, dtype):
+    if dtype is None:
+        dtype = torch.bfloat16 if k_cache.dtype == torch.float8_e4m3fn else k_cache.dtype
+    shape = (num_tokens, k_cache.shape[2], k_cache.shape[3])
+    return k_cache.new_empty(shape, dtype=dtype), k_cache.new_empty(shape, dtype=dtype)
+
+
+def ffpa_kv_append_fp8_func(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, slots: torch.Tensor,
+                            positions: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                            q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, *,
+                            eps: float = 1e-6, interleaved: bool = False, rope_scale: float = 1.0):
+    """Keys (normed and rotated) and values into a cache of 8 bits a value (see paged.ffpa_kv_append_fp8).
+    Returns the queries, or None without q."""
+    out = torch.ops.ffpa.kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positions, inv_freq, q_weight,
+                                       k_weight, float(eps), bool(interleaved), float(rope_scale))
+    return None if q is None else out
+
+
+def ffpa_attn_decode_fp8_func(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                              v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                              scale: Optional[float] = None, enable_gqa: bool = False, *, return_lse: bool = False):
+    """Attention of one new token per request over a paged cache of codes (see paged.ffpa_decode_paged_fp8)."""
+    o, lse = torch.ops.ffpa.decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
+                                             bool(enable_gqa))
+    return (o, lse) if return_lse else o
+
+
+def ffpa_attn_decode_shared_func(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 shared_pages: torch.Tensor, shared_len: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, scale: Optional[float] = None, enable_gqa: bool = False, *,
+                                 return_lse: bool = False):
+    """Attention of one new token per request behind shared pages (see paged.ffpa_decode_shared)."""
+    o, lse = torch.ops.ffpa.decode_shared(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale,
+                                          bool(enable_gqa))
+    return (o, lse) if return_lse else o
+
+
+def ffpa_kv_read_func(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                      num_tokens: int, *, k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                      dtype: Optional[torch.dtype] = None):
+    """Packed cached rows (k, v) [num_tokens,Hkv,D] (see paged.ffpa_kv_read)."""
+    return torch.ops.ffpa.kv_read(k_cache, v_cache, block_table, cu_seqlens, int(num_tokens), k_scale, v_scale, dtype)
+
+
 def ffpa_page_plan_func(block_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor,
                         free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, num_tokens: int):
     """Pages, slots and positions of one step's new tokens (see paged.ffpa_page_plan)."""

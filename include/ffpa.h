@@ -613,6 +613,107 @@ ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_
                            const ffpa_options* options);
 
 /*
+ * The paged cache in 8 bits.  k_cache and v_cache hold e4m3 codes (one byte
+ * each, [num_pages, page_size, Hkv, D] with strides as above, in bytes: every
+ * one but the last a multiple of 16), k_scale and v_scale an fp32 scale for
+ * each token and head: [num_pages, Hkv, page_size], strides (page, head, slot)
+ * in elements with the slots of a page adjacent.  A value is its code times its row's scale.
+ * D a multiple of 16 from 64 to 1024 (else FFPA_ERR_UNSUPPORTED).
+ */
+
+/*
+ * ffpa_kv_append into such a cache.  A row y (a key head, normed and rotated in
+ * fp32, or a value head) with a = max |y| is stored as
+ *
+ *     scale = a / 448,   codes = e4m3(y * (448 / a))
+ *
+ * in fp32, codes rounded to nearest even (a row of zeros: scale 1; a row with an
+ * infinity or a NaN: codes and scale that are not finite).  Each code is off by at
+ * most 2^-4 of its value, or 2^-10 scales.  The rows are not rounded to 16 bits
+ * before.  Arguments and checks otherwise as for ffpa_kv_append.
+ */
+ffpa_status ffpa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, ffpa_dtype dt, int T, int Hq, int Hkv, int D,
+                               int num_pages, int page_size, const int64_t q_str[3], const int64_t k_str[3],
+                               const int64_t v_str[3], const int64_t qo_str[3], const int64_t kc_str[4],
+                               const int64_t vc_str[4], const int64_t ks_str[3], const int64_t vs_str[3],
+                               const int64_t* slots, const ffpa_rope* rope, ffpa_stream_t stream,
+                               const ffpa_options* options);
+
+/*
+ * ffpa_decode_paged over such a cache: the attention of the values that the codes
+ * stand for.  Scales are not negative; any size of them is taken (a weight times a
+ * scale enters the sums to 2^-21 of itself, or to 2^-40 of the largest; scales below
+ * 2^-105 lose some of that).  q enters the scores exactly, or (bf16) to 2^-40 of
+ * the largest of 128 of its columns.
+ * Arguments, checks and workspace otherwise as for ffpa_decode_paged (the workspace
+ * sizes are the same).
+ */
+size_t ffpa_decode_paged_fp8_workspace_bytes(int Hq, int Hkv, int D);
+ffpa_status ffpa_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                  const float* v_scale, void* o, float* lse, ffpa_dtype dt, int B, int Hq, int Hkv,
+                                  int D, int num_pages, int page_size, int max_pages, const int64_t q_str[3],
+                                  const int64_t k_str[4], const int64_t v_str[4], const int64_t ks_str[3],
+                                  const int64_t vs_str[3], const int64_t o_str[3], const int32_t* block_table,
+                                  int64_t table_str, const int32_t* seq_lens, const float* scale, int enable_gqa,
+                                  void* workspace, size_t workspace_bytes, ffpa_stream_t stream,
+                                  const ffpa_options* options);
+
+/*
+ * The cached keys and values of a batch as packed rows, for the attention of its
+ * next tokens (ffpa_fwd_varlen with cu_seqlens as cu_seqlens_k):
+ *
+ *     k[cu_seqlens[b] + i], v[cu_seqlens[b] + i] = key and value i of request b,
+ *     0 <= i < cu_seqlens[b + 1] - cu_seqlens[b]
+ *
+ * from slot i % page_size of page block_table[b][i / page_size].
+ *
+ *   k_scale, v_scale NULL: the cache holds values of `dt` (D % 8 == 0), copied as they
+ *     are.  Otherwise it holds codes (D % 16 == 0): code times scale, rounded once.
+ *   k, v [T, Hkv, D] of `dt`, strides (t, h, d).  Rows at and behind cu_seqlens[B] are
+ *     left as they are; they must not overlap the cache.
+ *   cu_seqlens: int32 [B + 1] on the device.  What lies outside [0, T], a decrease, and a
+ *     request of more than max_pages * page_size rows is reported (rows beyond either are not
+ *     written).  A key whose page is not in [0, num_pages) is reported and becomes zeros.
+ *
+ * Other arguments as for ffpa_decode_paged.  One launch on `stream`.
+ */
+ffpa_status ffpa_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, void* k,
+                         void* v, ffpa_dtype dt, int T, int B, int Hkv, int D, int num_pages, int page_size,
+                         int max_pages, const int64_t kc_str[4], const int64_t vc_str[4], const int64_t ks_str[3],
+                         const int64_t vs_str[3], const int64_t k_str[3], const int64_t v_str[3],
+                         const int32_t* block_table, int64_t table_str, const int32_t* cu_seqlens,
+                         ffpa_stream_t stream, const ffpa_options* options);
+
+/*
+ * ffpa_decode_paged for a batch whose requests begin with the same tokens: the
+ * first shared_len[0] keys of every request (as many as it has) lie in the same
+ * pages, whose keys and values are read and multiplied once for all requests.
+ *
+ *   shared_pages: int32 [n_shared], the pages of those keys in order; shared_len:
+ *     int32 [1], on the device.  Only whole pages count as shared: S =
+ *     min(shared_len[0] / page_size, n_shared) * page_size keys.  (0: as ffpa_decode_paged.)
+ *   block_table, seq_lens: as for ffpa_decode_paged, over ALL keys of a request, the
+ *     shared ones among them; the first S / page_size entries of a row are not read.
+ *     A request of fewer than S keys sees that many of the shared ones.
+ *   workspace: of at least ffpa_decode_shared_workspace_bytes(B, Hq, Hkv, D) bytes.
+ *
+ * The result is that of ffpa_decode_paged with the shared pages in every row of the table,
+ * up to the order of the sums; a softmax weight of a shared key enters them as a 16-bit
+ * value (2^-9 of itself, fp16 2^-12 and 2^-24 of the largest) and all else in fp32.
+ * D a multiple of 64 from 64 to 1024, page_size a multiple of 8 (else FFPA_ERR_UNSUPPORTED).
+ * Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
+ */
+size_t ffpa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D);
+ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                               ffpa_dtype dt, int B, int Hq, int Hkv, int D, int num_pages, int page_size,
+                               int max_pages, int n_shared, const int64_t q_str[3], const int64_t k_str[4],
+                               const int64_t v_str[4], const int64_t o_str[3], const int32_t* shared_pages,
+                               const int32_t* shared_len, const int32_t* block_table, int64_t table_str,
+                               const int32_t* seq_lens, const float* scale, int enable_gqa, void* workspace,
+                               size_t workspace_bytes, ffpa_stream_t stream, const ffpa_options* options);
+
+/*
  * The page plan of one step.  Request b holds seq_lens[b] tokens, in the first
  * ceil(seq_lens[b] / page_size) pages of row b of block_table, and gets
  * new_lens[b] more (0: it waits).  Pages for them come off the end of the free
