@@ -593,6 +593,17 @@ ffpa_status encode_rows(CUtensorMap* map, ffpa_dtype dt, int rank, const void* b
                     base, dims, stride_bytes, box);
 }
 
+// Which kernel takes a decode batch's shared keys, and its plan.  As choose_kernel, but that
+// the dual-tile kernel needs more rows than one tile has.
+SharedKernel shared_kernel(int D, bool two_tiles) {
+  if (D > 256) return split_ways(D) == 2 ? SharedKernel::SPLIT : SharedKernel::CLUSTER;
+  return two_tiles && dual_eligible(D, false) ? SharedKernel::DUAL : SharedKernel::SINGLE;
+}
+int shared_ctas(SharedKernel k, int D) { return k == SharedKernel::SPLIT || k == SharedKernel::CLUSTER ? split_ways(D) : 1; }
+size_t plan_shared(SharedKernel k, int D, Params* P) {
+  return k == SharedKernel::DUAL ? plan_dual(D, P) : k == SharedKernel::SINGLE ? plan(D, P) : plan_split(D, P);
+}
+
 ffpa_status encode_codes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* stride_bytes,
                          const uint32_t* box) {
   return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, base, dims, stride_bytes, box);

@@ -53,13 +53,17 @@ __device__ __forceinline__ float max_from_bits(uint32_t h) { return __uint_as_fl
 // compile-time trip count and is fully unrolled: the tensor pipe's
 // instruction queue is shallow, and loop overhead between MMAs leaves it
 // idle (measured: a runtime-count loop of 8 MMAs runs at about half rate).
-template <bool VARLEN, int NCH, bool UMASK, int C>
+template <int LAYOUT, int NCH, bool UMASK, int C>
 __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
     ffpa_fwd_cluster_kernel(const __grid_constant__ Params p) {
   static_assert(C >= 2 && C <= 4 && NCH % C == 0 && NCH % 2 == 0, "unsupported split");
   const uint32_t rank = cluster_ctarank();
+  constexpr bool VARLEN = LAYOUT == LAYOUT_PACKED, SHARED = LAYOUT == LAYOUT_SHARED;
   Item it;
-  if (!decode_item(p, VARLEN, blockIdx.x / C, it)) return;    // same answer in every CTA
+  if (SHARED)
+    decode_item_shared(p, blockIdx.x / C, 1, it);
+  else if (!decode_item(p, VARLEN, blockIdx.x / C, it))
+    return;    // same answer in every CTA
   constexpr int VCH = NCH / C;                                  // V / O chunks per CTA
   static_assert(VCH * DK <= DV_MAX, "O must fit beside S in TMEM");
   it.dv = VCH * DK;
@@ -139,7 +143,54 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
     // Q pairs before the K pairs they meet when Q is streamed) of the first
     // own tile, then per round i: QK^T stages of the own tile of round i+1,
     // V (this CTA's columns) of the round's tiles in the MMA thread's order.
-    if (lane == 0 && T > 0) {
+    if (SHARED) {
+      if (T > 0) {
+        if (lane == 0) {
+          prefetch_tmap(&p.tm_q);
+          prefetch_tmap(&p.tm_k);
+          prefetch_tmap(&p.tm_v);
+        }
+        SharedCopy copy{p, it, ring_u32, SLOT_BYTES, bar_full, bar_empty, NS, lane, 0, 0, 0u, inject != 0 && rank == 0, &abort_flag};
+        const uint32_t qb = smem_u32(&bar_q);
+        if (lane == 0) mbar_arrive_expect_tx(qb, copy.q_bytes(QRES ? NCH : qt));
+        __syncwarp();
+        copy.queries(pbuf_u32, qb, 0, qt, it.q0);
+        if (QRES) copy.queries(qs_u32, qb, qt, NCH - qt, it.q0);
+        auto load_qk = [&](int j) -> bool {
+          for (int c = 0; c < NCH; c += 2) {
+            uint32_t fb = 0;
+            if (!QRES && c >= qt) {
+              const uint32_t dq = copy.acquire(copy.q_bytes(2), fb);
+              if (dq == ~0u) return false;
+              if (dq) copy.queries(dq, fb, c, 2, it.q0);
+            }
+            const uint32_t dst = copy.acquire(2 * CHUNK_BYTES, fb);
+            if (dst == ~0u) return false;
+            if (dst) copy.rows(&p.tm_k, dst, fb, (it.tile0 + j) * BN, BN, c, 2);
+          }
+          return true;
+        };
+        auto load_v = [&](int j) -> bool {
+          for (int h = 0; h < BN / vk; ++h) {
+            uint32_t fb = 0;
+            const uint32_t dst = copy.acquire(vslot, fb);
+            if (dst == ~0u) return false;
+            if (dst) copy.rows(&p.tm_v, dst, fb, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH);
+          }
+          return true;
+        };
+        bool ok = own0 >= T || load_qk(own0);
+        for (int i = 0; i < R && ok; ++i) {
+          if (C * (i + 1) + own0 < T && !(ok = load_qk(C * (i + 1) + own0))) break;
+          for (int k = 0; k < C; ++k) {
+            const int j = (own0 + k) % C;
+            if (ok && C * i + j < T) ok = load_v(C * i + j);
+          }
+        }
+        wait_drain(qb, 0, tmo, err);
+        copy.drain(inject != 0 && rank == 0);
+      }
+    } else if (lane == 0 && T > 0) {
       prefetch_tmap(&p.tm_q);
       prefetch_tmap(&p.tm_k);
       prefetch_tmap(&p.tm_v);
@@ -352,7 +403,9 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
     const int r = warp * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int row = it.q0 + r;
-    const bool row_valid = row < it.q_len;
+    const bool row_valid = row < it.q_len && (!SHARED || r < p.sh.tile_rows);
+    const int seen = SHARED ? shared_limit(p, it, it.q0, r) : 0, all_see = SHARED ? __reduce_min_sync(0xffffffffu, seen) : 0;
+    const float lift = SHARED ? p.sh.lift : 0.f;
     const long long row_limit = (long long)row + (it.kv_len - it.q_len);
     const long long first_limit = (long long)it.q0 + (it.kv_len - it.q_len);
     const uint8_t* mrow = nullptr;
@@ -416,10 +469,10 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_addr = lane_base + S_COL;
-        const int kbase = kv_tile(it, C * i + own0) * BN;
-        const bool need_mask = (kbase + BN > it.kv_len) ||
-                               (causal && (long long)kbase + BN - 1 > first_limit) ||
-                               mask_kind != FFPA_MASK_NONE;
+        const int kbase = SHARED ? (it.tile0 + C * i + own0) * BN : kv_tile(it, C * i + own0) * BN;
+        const bool need_mask = SHARED ? kbase + BN > all_see
+                                      : (kbase + BN > it.kv_len) || (causal && (long long)kbase + BN - 1 > first_limit) ||
+                                            mask_kind != FFPA_MASK_NONE;
         {
           uint32_t r0[32], r1[32], r2[32], r3[32];
           tmem_ld32(s_addr, r0);
@@ -446,7 +499,8 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
             for (int c = 0; c < BN; ++c) x[c] *= ld_scale;
           }
         }
-        if (need_mask) {
+        if (SHARED && need_mask) mask_tail(x, kbase, seen);
+        if (!SHARED && need_mask) {
 #pragma unroll
           for (int q4 = 0; q4 < BN / 32; ++q4) {
             apply_mask32<UMASK>(x + 32 * q4, kbase + 32 * q4, it.kv_len, causal, row_limit, mrow,
@@ -494,7 +548,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
       l_sum *= alpha;
       uint32_t pk[BN / 2];
       if (own) {
-        const float base = m_ref == -INFINITY ? 0.f : m_ref;
+        const float base = m_ref == -INFINITY ? 0.f : SHARED ? m_ref - lift : m_ref;
         // One branch per tile, not per element: the unrolled loop then holds
         // a single conversion per pair.
         l_sum += fp16 ? form_p<true, BN>(x, xs, base, pk) : form_p<false, BN>(x, xs, base, pk);
@@ -587,7 +641,12 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
         }
       }
     }
-    if (ok || T == 0) store_output<VARLEN>(p, it, T > 0, lane_base, row, row_valid, l_sum, m_ref);
+    if (ok || T == 0) {
+      if (SHARED)
+        store_part(p, it, 0, T > 0, lane_base, r, row_valid, l_sum, m_ref);
+      else
+        store_output<VARLEN>(p, it, T > 0, lane_base, row, row_valid, l_sum, m_ref);
+    }
   }
 
   tc_fence_before();
@@ -600,9 +659,9 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
   }
 }
 
-template <bool VARLEN, bool UMASK, int NCH, int C>
+template <int LAYOUT, bool UMASK, int NCH, int C>
 static ffpa_status launch_cluster_nc(const Params& P, int items, size_t smem, cudaStream_t stream) {
-  auto kern = ffpa_fwd_cluster_kernel<VARLEN, NCH, UMASK, C>;
+  auto kern = ffpa_fwd_cluster_kernel<LAYOUT, NCH, UMASK, C>;
   const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(kern), P.device,
                                             static_cast<int>(SMEM_LIMIT - SPLIT_STATIC_RESERVE));
   if (st != FFPA_OK) return st;
@@ -610,20 +669,24 @@ static ffpa_status launch_cluster_nc(const Params& P, int items, size_t smem, cu
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
-template <bool VARLEN, bool UMASK>
+template <int LAYOUT, bool UMASK>
 static ffpa_status launch_cluster_t(const Params& P, int items, size_t smem, cudaStream_t stream) {
-  if (!VARLEN && P.nchunks == 8 && P.split_c == 2 && P.q_res == 0)
-    return launch_cluster_nc<false, UMASK, 8, 2>(P, items, smem, stream);
-  if (P.nchunks == 12 && P.split_c == 3) return launch_cluster_nc<VARLEN, UMASK, 12, 3>(P, items, smem, stream);
-  if (P.nchunks == 16 && P.split_c == 4) return launch_cluster_nc<VARLEN, UMASK, 16, 4>(P, items, smem, stream);
+  if (LAYOUT == LAYOUT_DENSE && P.nchunks == 8 && P.split_c == 2 && P.q_res == 0)
+    return launch_cluster_nc<LAYOUT_DENSE, UMASK, 8, 2>(P, items, smem, stream);
+  if (P.nchunks == 12 && P.split_c == 3) return launch_cluster_nc<LAYOUT, UMASK, 12, 3>(P, items, smem, stream);
+  if (P.nchunks == 16 && P.split_c == 4) return launch_cluster_nc<LAYOUT, UMASK, 16, 4>(P, items, smem, stream);
   return FFPA_ERR_UNSUPPORTED;
 }
 
 ffpa_status launch_cluster(bool varlen, bool umask, const Params& P, int items, size_t smem,
                            cudaStream_t stream) {
-  return varlen  ? launch_cluster_t<true, false>(P, items, smem, stream)
-         : umask ? launch_cluster_t<false, true>(P, items, smem, stream)
-                 : launch_cluster_t<false, false>(P, items, smem, stream);
+  return varlen  ? launch_cluster_t<LAYOUT_PACKED, false>(P, items, smem, stream)
+         : umask ? launch_cluster_t<LAYOUT_DENSE, true>(P, items, smem, stream)
+                 : launch_cluster_t<LAYOUT_DENSE, false>(P, items, smem, stream);
+}
+
+ffpa_status launch_cluster_shared(const Params& P, int items, size_t smem, cudaStream_t stream) {
+  return launch_cluster_t<LAYOUT_SHARED, false>(P, items, smem, stream);
 }
 
 }  // namespace ffpa

@@ -77,6 +77,13 @@ constexpr size_t SPLIT_STATIC_RESERVE = 2048;    // static shared memory of the 
 // Launches of the forward kernels (one translation unit each; the column
 // split has a pair kernel and a kernel for clusters of 3 or 4 CTAs).
 struct Params;
+// How a launch finds its rows: dense tensors, packed sequences, or the keys of
+// pages that all requests of a decode batch share (Params::sh).
+enum Layout { LAYOUT_DENSE = 0, LAYOUT_PACKED = 1, LAYOUT_SHARED = 2 };
+ffpa_status launch_single_shared(const Params& P, int items, size_t smem, cudaStream_t stream);
+ffpa_status launch_dual_shared(const Params& P, int items, size_t smem, cudaStream_t stream);
+ffpa_status launch_split_shared(const Params& P, int items, size_t smem, cudaStream_t stream);
+ffpa_status launch_cluster_shared(const Params& P, int items, size_t smem, cudaStream_t stream);
 ffpa_status launch_single(bool varlen, bool umask, const Params& P, int items, size_t smem, cudaStream_t stream);
 ffpa_status launch_pair(bool varlen, bool umask, const Params& P, int items, size_t smem, cudaStream_t stream);
 ffpa_status launch_split(bool varlen, bool umask, const Params& P, int items, size_t smem, cudaStream_t stream);
@@ -239,6 +246,22 @@ struct BwdParams {
   int n_dq_items, n_kv_items;   // contraction kernel: dQ items, and dV (= dK) items
 };
 
+// Shared pages (LAYOUT_SHARED): the rows of a key head are the queries of its group of
+// heads, request by request; the keys lie in pages, and an item takes a part of them.
+// It leaves unnormalised fp32 sums with their maximum and sum for the merge.
+struct SharedKeys {
+  const int32_t* pages;      // [n_pages], of the keys in order
+  const int32_t* len;        // device: keys shared (whole pages of them count)
+  const int32_t* lens;       // [B]: a request sees so many of its keys
+  float* part;               // [item][128 rows][D]
+  float2* part_ml;           // [item][128 rows] (maximum in log2 units, sum)
+  int n_pages, num_pages, page_size;
+  int box_rows;              // keys of a box: a power of two of 8 .. 128 that divides page_size
+  int tile_rows;             // rows of a query tile: whole requests, at most 128
+  int splits;                // parts of the keys
+  float lift;                // log2 of the factor on P (fp16: small weights stay in its range)
+};
+
 struct Params {
   // Views with D split as (64, D/64): dense (64, N, D/64, H, B); varlen
   // (64, T, D/64, H).  Q and K boxes: 64 x 128 rows x min(2, D/64) chunks;
@@ -281,6 +304,7 @@ struct Params {
   const float* sk;
   const float* sv;
   int n_kb;
+  SharedKeys sh;
 };
 
 struct Item {
@@ -288,6 +312,7 @@ struct Item {
   int q0, q_len, kv_len, q_row0, kv_row0;
   int col_lo, dv, ntiles;
   int rot;   // first key tile visited; tiles are visited rot, rot+1, ... (mod ntiles)
+  int tile0, part;   // LAYOUT_SHARED: the first key tile of the item's part; its place in SharedKeys::part
 };
 
 // Key tile visited at step j.  Work items of one head start at different
@@ -347,6 +372,49 @@ __device__ __forceinline__ bool decode_item(const Params& p, bool varlen, int L,
   it.col_lo = c_lo * DK;
   it.dv = (c_hi - c_lo) * DK;
   return true;
+}
+
+// Item L of LAYOUT_SHARED: key head, part of the keys, query tile (of 128 rows, `per` of
+// them an item), output slice; the query tiles of a part are neighbours (they read the same keys).
+// The part's place is that of its first tile.
+__device__ __forceinline__ void decode_item_shared(const Params& p, int L, int per, Item& it) {
+  const SharedKeys& s = p.sh;
+  it.slice = L % p.n_slices;
+  L /= p.n_slices;
+  const int qt = L % p.n_qt;
+  L /= p.n_qt;
+  const int split = L % s.splits;
+  it.hkv = L / s.splits;
+  it.b = 0;
+  it.hq = it.hkv * p.group;
+  it.q_row0 = it.kv_row0 = 0;
+  it.q0 = qt * per * s.tile_rows;
+  it.q_len = p.B * p.group;
+  const int n = *s.len;
+  it.kv_len = n < 0 ? 0 : min(n / s.page_size, s.n_pages) * s.page_size;
+  const long long tiles = (it.kv_len + BN - 1) / BN;
+  it.tile0 = (int)(tiles * split / s.splits);
+  it.ntiles = (int)(tiles * (split + 1) / s.splits) - it.tile0;
+  it.part = ((it.hkv * s.splits + split) * p.n_qt + qt) * per;
+  it.rot = 0;
+  const int c_lo = it.slice * p.nchunks / p.n_slices;
+  const int c_hi = (it.slice + 1) * p.nchunks / p.n_slices;
+  it.col_lo = c_lo * DK;
+  it.dv = (c_hi - c_lo) * DK;
+}
+
+// Keys that row r of a query tile (whose first row is row0) sees; all for rows that are not stored.
+__device__ __forceinline__ int shared_limit(const Params& p, const Item& it, int row0, int r) {
+  const int row = row0 + r;
+  if (r >= p.sh.tile_rows || row >= it.q_len) return it.kv_len;
+  return min(max(p.sh.lens[row / p.group], 0), it.kv_len);
+}
+
+// Masks 128 scores of a row that sees `limit` keys.
+__device__ __forceinline__ void mask_tail(float* x, int key0, int limit) {
+#pragma unroll
+  for (int c = 0; c < BN; ++c)
+    if (key0 + c >= limit) x[c] = -INFINITY;
 }
 
 // Bounded wait on an mbarrier phase.  Returns false when this CTA has been
@@ -601,6 +669,100 @@ __device__ __forceinline__ void store_output_boxes(const Params& p, const Item& 
   }
 }
 
+// One row of an item of LAYOUT_SHARED: the columns [col_lo, col_lo + dv) of its sums (TMEM), and
+// from slice 0 their maximum and sum.
+__device__ __forceinline__ void store_part(const Params& p, const Item& it, int tile, bool have_o, uint32_t lane_base, int r,
+                                           bool row_valid, float l_sum, float m_ref) {
+  const int64_t at = (int64_t)(it.part + tile) * BM + r;
+  if (row_valid && it.slice == 0)
+    p.sh.part_ml[at] = make_float2(have_o ? m_ref - p.sh.lift : -INFINITY, have_o ? l_sum : 0.f);
+  if (!have_o) return;
+  float* out = p.sh.part + at * p.D + it.col_lo;
+  const int dcols = min(it.dv, p.D - it.col_lo);
+  for (int c0 = 0; c0 < it.dv; c0 += 32) {
+    uint32_t o[32];
+    tmem_ld32(lane_base + c0, o);
+    tmem_wait_ld();
+    reg_fence(o);
+    if (row_valid && c0 < dcols) {
+#pragma unroll
+      for (int v = 0; v < 8; ++v)
+        reinterpret_cast<uint4*>(out + c0)[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+    }
+  }
+}
+
+// The copying warp of LAYOUT_SHARED: all its lanes, a box of a stage each.
+struct SharedCopy {
+  const Params& p;
+  const Item& it;
+  uint32_t ring, stride;
+  uint64_t *full, *empty;
+  int slots, lane, slot = 0, issued = 0;
+  uint32_t lap = 0;
+  bool drop;
+  volatile int* abort_flag;
+
+  // The next stage, armed for `bytes`: its address, 0 where the test hook drops it, ~0 on abort.
+  __device__ __forceinline__ uint32_t acquire(uint32_t bytes, uint32_t& fb) {
+    const uint32_t eb = smem_u32(&empty[slot]);
+    const bool w = mbar_try_wait(eb, lap ^ 1u) || wait_bounded_inl(eb, lap ^ 1u, abort_flag, p.timeout_ns, p.err);
+    if (!__all_sync(0xffffffffu, w)) return ~0u;
+    fb = smem_u32(&full[slot]);
+    const uint32_t dst = ring + slot * stride;
+    ++issued;
+    if (++slot == slots) {
+      slot = 0;
+      lap ^= 1u;
+    }
+    if (drop) {
+      drop = false;
+      return 0u;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
+    __syncwarp();
+    return dst;
+  }
+  // `chunks` chunks from chunk0 of the queries of a tile, each of tile_rows rows, 16 KB apart.
+  __device__ __forceinline__ uint32_t q_bytes(int chunks) const { return (uint32_t)chunks * p.sh.tile_rows * 128u; }
+  __device__ __forceinline__ void queries(uint32_t dst, uint32_t bar, int chunk0, int chunks, int row0) {
+    if (lane < chunks) tma_load_5d(dst + lane * CHUNK_BYTES, &p.tm_q, bar, 0, 0, row0 / p.group, chunk0 + lane, it.hkv);
+  }
+  // `keys` keys from key0 on (the first a multiple of the box), `chunks` chunks from chunk0, each
+  // `keys` rows.  What lies behind the last key, and a page that does not exist, becomes zeros.
+  __device__ __forceinline__ void rows(const CUtensorMap* map, uint32_t dst, uint32_t bar, int key0, int keys, int chunk0, int chunks) {
+    const SharedKeys& s = p.sh;
+    const int boxes = keys / s.box_rows, c = lane / boxes, i = lane - c * boxes;
+    if (c >= chunks) return;
+    const int key = key0 + i * s.box_rows;
+    int y = 0, z = s.num_pages;
+    if (key < it.kv_len) {
+      const int j = key / s.page_size, page = __ldg(s.pages + j);
+      if (page >= 0 && page < s.num_pages) {
+        y = key - j * s.page_size;
+        z = page;
+      } else {
+        atomicCAS(p.err, 0, static_cast<int>(FFPA_ERR_INVALID));
+      }
+    }
+    tma_load_5d(dst + (uint32_t)(c * keys + i * s.box_rows) * 128u, map, bar, 0, y, chunk0 + c, it.hkv, z);
+  }
+  // Every copy lands before the CTA ends (a dropped stage, the first, was never armed).
+  __device__ __forceinline__ void drain(bool dropped) {
+    const int n = issued < slots ? issued : slots;
+    int s = slot;
+    uint32_t lp = lap;
+    for (int i = 0; i < n; ++i) {
+      if (--s < 0) {
+        s = slots - 1;
+        lp ^= 1u;
+      }
+      if (dropped && issued - 1 - i == 0) continue;
+      wait_drain_inl(smem_u32(&full[s]), lp, p.timeout_ns, p.err);
+    }
+  }
+};
+
 // Maximum of n scores (n a multiple of 16): eight independent chains of
 // three-input maxima, then a small tree.
 template <int N>
@@ -664,7 +826,7 @@ __device__ __forceinline__ void arrive_to(uint32_t addr) {
 
 // Softmax warps 0-3 and the epilogue: thread r owns query row it.q0 + r,
 // which is TMEM lane r of this CTA.
-template <bool VARLEN, bool PAIR, bool UMASK>
+template <int LAYOUT, bool PAIR, bool UMASK>
 __device__ __forceinline__ void softmax_role(const Params& p, const Item& it, int T, uint32_t tmem,
                                              int warp, int lane, const SoftmaxBars bars,
                                              volatile int* abort_flag, unsigned long long tmo,
@@ -676,9 +838,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Item& it, in
   const int r = warp * 32 + lane;                 // row within the tile = TMEM lane
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const int row = it.q0 + r;                      // row within the sequence
-  const bool row_valid = row < it.q_len;
+  constexpr bool VARLEN = LAYOUT == LAYOUT_PACKED, SHARED = LAYOUT == LAYOUT_SHARED;
+  const bool row_valid = row < it.q_len && (!SHARED || r < p.sh.tile_rows);
   const long long row_limit = (long long)row + (it.kv_len - it.q_len);   // causal
   const long long first_limit = (long long)it.q0 + (it.kv_len - it.q_len);
+  const int seen = SHARED ? shared_limit(p, it, it.q0, r) : 0, all_see = SHARED ? __reduce_min_sync(0xffffffffu, seen) : 0;
+  const float lift = SHARED ? p.sh.lift : 0.f;
   const uint8_t* mrow = nullptr;
   if (UMASK && mask_kind != FFPA_MASK_NONE && row_valid) {
     const size_t esz = mask_kind == FFPA_MASK_BOOL ? 1 : mask_kind == FFPA_MASK_ADD_F32 ? 4 : 2;
@@ -705,10 +870,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Item& it, in
     tc_fence_after();
     const uint32_t s_addr = lane_base + S_COL;
     const uint32_t p_addr = lane_base + P_COL0 + 64 * b;
-    const int kbase = kv_tile(it, j) * BN;
-    const bool need_mask = (kbase + BN > it.kv_len) ||
-                           (causal && (long long)kbase + BN - 1 > first_limit) ||
-                           mask_kind != FFPA_MASK_NONE;
+    const int kbase = SHARED ? (it.tile0 + j) * BN : kv_tile(it, j) * BN;
+    const bool need_mask = SHARED ? kbase + BN > all_see
+                                  : (kbase + BN > it.kv_len) || (causal && (long long)kbase + BN - 1 > first_limit) ||
+                                        mask_kind != FFPA_MASK_NONE;
     float x[BN];
     {
       uint32_t r0[32], r1[32], r2[32], r3[32];
@@ -737,7 +902,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Item& it, in
         for (int c = 0; c < BN; ++c) x[c] *= ld_scale;
       }
     }
-    if (need_mask) {
+    if (SHARED && need_mask) mask_tail(x, kbase, seen);
+    if (!SHARED && need_mask) {
 #pragma unroll
       for (int q4 = 0; q4 < BN / 32; ++q4) {
         apply_mask32<UMASK>(x + 32 * q4, kbase + 32 * q4, it.kv_len, causal, row_limit, mrow, mk,
@@ -780,7 +946,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Item& it, in
       tc_fence_after();
     }
     // P = exp2(x - m_ref) in 16-bit, into P buffer b.
-    const float base = m_ref == -INFINITY ? 0.f : m_ref;
+    const float base = m_ref == -INFINITY ? 0.f : SHARED ? m_ref - lift : m_ref;
     float psum = 0.f;
 #pragma unroll
     for (int g = 0; g < BN / 32; ++g) {
@@ -802,7 +968,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Item& it, in
     ok = __all_sync(0xffffffffu, w);
     if (ok) tc_fence_after();
   }
-  if (ok || T == 0) store_output<VARLEN>(p, it, T > 0, lane_base, row, row_valid, l_sum, m_ref);
+  if (ok || T == 0) {
+    if (SHARED)
+      store_part(p, it, 0, T > 0, lane_base, r, row_valid, l_sum, m_ref);
+    else
+      store_output<VARLEN>(p, it, T > 0, lane_base, row, row_valid, l_sum, m_ref);
+  }
 }
 
 }  // namespace ffpa

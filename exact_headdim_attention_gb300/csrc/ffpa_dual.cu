@@ -79,10 +79,13 @@ __device__ __forceinline__ bool decode_dual(const Params& p, int L, Item& it) {
 
 // No caller's mask here (its loads need more registers than the softmax
 // warps have); masked calls at these head dims run on the single-CTA kernel.
-template <int NCH>
+template <int NCH, bool SHARED>
 __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __grid_constant__ Params p) {
   Item it;
-  if (!decode_dual(p, blockIdx.x, it)) return;   // uniform across the CTA
+  if (SHARED)
+    decode_item_shared(p, blockIdx.x, 2, it);
+  else if (!decode_dual(p, blockIdx.x, it))
+    return;   // uniform across the CTA
 
   constexpr uint32_t TILE_BYTES = NCH * CHUNK_BYTES;   // one Q, K or V tile
   const int inject = p.inject;
@@ -138,7 +141,35 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
       // ------------------------------------------------------------ producer
       // Q_A and Q_B once, then the ring in the MMA thread's order: K_0; per
       // key tile j: K_{j+1}, V_j.
-      if (lane == 0 && T > 0) {
+      if (SHARED) {
+        if (T > 0) {
+          if (lane == 0) {
+            prefetch_tmap(&p.tm_q);
+            prefetch_tmap(&p.tm_k);
+            prefetch_tmap(&p.tm_v);
+          }
+          SharedCopy copy{p, it, ring_u32, TILE_BYTES, bar_full, bar_empty, NS, lane, 0, 0, 0u, inject != 0, &abort_flag};
+          const uint32_t qb = smem_u32(&bar_q);
+          if (lane == 0) mbar_arrive_expect_tx(qb, 2 * copy.q_bytes(NCH));
+          __syncwarp();
+          copy.queries(q_u32, qb, 0, NCH, it.q0);
+          copy.queries(q_u32 + TILE_BYTES, qb, 0, NCH, it.q0 + p.sh.tile_rows);
+          auto load = [&](const CUtensorMap* m, int j) -> bool {
+            uint32_t fb = 0;
+            const uint32_t dst = copy.acquire(TILE_BYTES, fb);
+            if (dst == ~0u) return false;
+            if (dst) copy.rows(m, dst, fb, (it.tile0 + j) * BN, BN, 0, NCH);
+            return true;
+          };
+          bool ok = load(&p.tm_k, 0);
+          for (int j = 0; j < T && ok; ++j) {
+            if (j + 1 < T && !(ok = load(&p.tm_k, j + 1))) break;
+            ok = load(&p.tm_v, j);
+          }
+          wait_drain_inl(qb, 0, tmo, err);
+          copy.drain(inject != 0);
+        }
+      } else if (lane == 0 && T > 0) {
         prefetch_tmap(&p.tm_q);
         prefetch_tmap(&p.tm_k);
         prefetch_tmap(&p.tm_v);
@@ -285,8 +316,10 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t s_addr = lane_base + DUAL_S_COL + 128u * g;
     const uint32_t o_base = lane_base + DUAL_O_STRIDE * g;
-    const int row = it.q0 + BM * g + r;
-    const bool row_valid = row < it.q_len;
+    const int row0 = it.q0 + (SHARED ? p.sh.tile_rows : BM) * g, row = row0 + r;
+    const bool row_valid = row < it.q_len && (!SHARED || r < p.sh.tile_rows);
+    const int seen = SHARED ? shared_limit(p, it, row0, r) : 0, all_see = SHARED ? __reduce_min_sync(0xffffffffu, seen) : 0;
+    const float lift = SHARED ? p.sh.lift : 0.f;
     const long long row_limit = (long long)row + (it.kv_len - it.q_len);
     const long long first_limit = (long long)it.q0 + BM * g + (it.kv_len - it.q_len);
     // Scores stay unscaled (x = q.k) so that the exponent is one FFMA, unless
@@ -307,9 +340,9 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
       ok = __all_sync(0xffffffffu, w);
       if (!ok) break;
       tc_fence_after();
-      const int kbase = kv_tile(it, j) * BN;
-      const bool need_mask = (kbase + BN > it.kv_len) ||
-                             (causal && (long long)kbase + BN - 1 > first_limit);
+      const int kbase = SHARED ? (it.tile0 + j) * BN : kv_tile(it, j) * BN;
+      const bool need_mask = SHARED ? kbase + BN > all_see
+                                    : (kbase + BN > it.kv_len) || (causal && (long long)kbase + BN - 1 > first_limit);
       float x[BN];
       {
         uint32_t r0[32], r1[32], r2[32], r3[32];
@@ -337,7 +370,8 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
           for (int c = 0; c < BN; ++c) x[c] *= ld_scale;
         }
       }
-      if (need_mask) {
+      if (SHARED && need_mask) mask_tail(x, kbase, seen);
+      if (!SHARED && need_mask) {
 #pragma unroll
         for (int q4 = 0; q4 < BN / 32; ++q4) {
           apply_mask32<false>(x + 32 * q4, kbase + 32 * q4, it.kv_len, causal, row_limit, nullptr, 0,
@@ -378,7 +412,7 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
       }
       // P = exp2(x - m) in 16-bit; row r of P_g: 16 units of 8 keys,
       // 128-byte swizzle, 64-key chunks.
-      const float base = m_ref == -INFINITY ? 0.f : m_ref;
+      const float base = m_ref == -INFINITY ? 0.f : SHARED ? m_ref - lift : m_ref;
       float psum = 0.f;
 #pragma unroll
       for (int q4 = 0; q4 < BN / 32; ++q4) {
@@ -404,7 +438,12 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
       ok = __all_sync(0xffffffffu, w);
       if (ok) tc_fence_after();
     }
-    if (ok || T == 0) store_output<false>(p, it, T > 0, o_base, row, row_valid, l_sum, m_ref);
+    if (ok || T == 0) {
+      if (SHARED)
+        store_part(p, it, g, T > 0, o_base, r, row_valid, l_sum, m_ref);
+      else
+        store_output<false>(p, it, T > 0, o_base, row, row_valid, l_sum, m_ref);
+    }
   }
 
   tc_fence_before();
@@ -416,11 +455,11 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
   }
 }
 
-ffpa_status launch_dual(bool umask, const Params& P, int items, size_t smem, cudaStream_t stream) {
-  if (umask) return FFPA_ERR_UNSUPPORTED;                              // see the kernel
+template <bool SHARED>
+static ffpa_status launch_dual_t(const Params& P, int items, size_t smem, cudaStream_t stream) {
   if (P.nchunks != 1 && P.nchunks != 2) return FFPA_ERR_UNSUPPORTED;   // only the instantiated shapes
   if (P.nslot < 2 || P.nslot > DUAL_NSLOT_MAX) return FFPA_ERR_UNSUPPORTED;
-  auto kern = P.nchunks == 2 ? ffpa_fwd_dual_kernel<2> : ffpa_fwd_dual_kernel<1>;
+  auto kern = P.nchunks == 2 ? ffpa_fwd_dual_kernel<2, SHARED> : ffpa_fwd_dual_kernel<1, SHARED>;
   const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(kern), P.device,
                                             static_cast<int>(SMEM_LIMIT - SMEM_STATIC_RESERVE));
   if (st != FFPA_OK) return st;
@@ -430,8 +469,8 @@ ffpa_status launch_dual(bool umask, const Params& P, int items, size_t smem, cud
   static const bool regs_ok = [] {
     cudaFuncAttributes a1{}, a2{};
     const bool ok =
-        cudaFuncGetAttributes(&a1, reinterpret_cast<const void*>(ffpa_fwd_dual_kernel<1>)) == cudaSuccess &&
-        cudaFuncGetAttributes(&a2, reinterpret_cast<const void*>(ffpa_fwd_dual_kernel<2>)) == cudaSuccess &&
+        cudaFuncGetAttributes(&a1, reinterpret_cast<const void*>(ffpa_fwd_dual_kernel<1, SHARED>)) == cudaSuccess &&
+        cudaFuncGetAttributes(&a2, reinterpret_cast<const void*>(ffpa_fwd_dual_kernel<2, SHARED>)) == cudaSuccess &&
         a1.numRegs == DUAL_REGS_LAUNCH && a2.numRegs == DUAL_REGS_LAUNCH;
     cudaGetLastError();
     return ok;
@@ -439,6 +478,14 @@ ffpa_status launch_dual(bool umask, const Params& P, int items, size_t smem, cud
   if (!regs_ok) return FFPA_ERR_UNSUPPORTED;
   kern<<<items, DUAL_THREADS, smem, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
+}
+
+ffpa_status launch_dual(bool umask, const Params& P, int items, size_t smem, cudaStream_t stream) {
+  return umask ? FFPA_ERR_UNSUPPORTED : launch_dual_t<false>(P, items, smem, stream);   // see the kernel
+}
+
+ffpa_status launch_dual_shared(const Params& P, int items, size_t smem, cudaStream_t stream) {
+  return launch_dual_t<true>(P, items, smem, stream);
 }
 
 }  // namespace ffpa

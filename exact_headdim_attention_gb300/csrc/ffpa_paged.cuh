@@ -26,6 +26,13 @@ ffpa_status encode_rows(CUtensorMap* map, ffpa_dtype dt, int rank, const void* b
 ffpa_status encode_codes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* stride_bytes,
                          const uint32_t* box);
 
+// Kernels that take the keys which a decode batch shares: which one, its CTAs an item, its plan
+// (sizes in *P; the dynamic shared memory is returned).
+enum class SharedKernel { SINGLE, DUAL, SPLIT, CLUSTER };
+SharedKernel shared_kernel(int D, bool two_tiles);
+int shared_ctas(SharedKernel k, int D);
+size_t plan_shared(SharedKernel k, int D, Params* P);
+
 inline bool on_boundary(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // As for the attention inputs: unit last stride, every other stride of a

@@ -4,10 +4,14 @@
 namespace ffpa {
 
 // UMASK: launched with a caller's mask (mask-loading code present).
-template <bool VARLEN, bool UMASK>
+template <int LAYOUT, bool UMASK>
 __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_constant__ Params p) {
+  constexpr bool VARLEN = LAYOUT == LAYOUT_PACKED, SHARED = LAYOUT == LAYOUT_SHARED;
   Item it;
-  if (!decode_item(p, VARLEN, blockIdx.x, it)) return;   // uniform across the CTA
+  if (SHARED)
+    decode_item_shared(p, blockIdx.x, 1, it);
+  else if (!decode_item(p, VARLEN, blockIdx.x, it))
+    return;   // uniform across the CTA
 
   // Scalars copied out of the parameter block once: the hot loops below run
   // between asm statements with memory clobbers, which would otherwise force
@@ -76,7 +80,45 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
     // resident, then K pairs, per key tile), warp 7 the V ring (V stages per
     // key tile).  Separate rings keep every mbarrier phase observed by its
     // only consumer, which parity-based waits require.
-    if (lane == 0 && T > 0) {
+    if (SHARED) {
+      if (T > 0) {
+        const bool k_role = warp == PRODUCER_WARP;
+        if (lane == 0) {
+          if (k_role) prefetch_tmap(&p.tm_q);
+          prefetch_tmap(k_role ? &p.tm_k : &p.tm_v);
+        }
+        SharedCopy copy{p, it, k_role ? ring_u32 : vring_u32, k_role ? SLOT_BYTES : vslot, k_role ? bar_full : bar_vfull,
+                        k_role ? bar_empty : bar_vempty, k_role ? NS : NSV, lane, 0, 0, 0u, k_role && inject != 0, &abort_flag};
+        bool ok = true;
+        const uint32_t qb = smem_u32(&bar_q);
+        if (k_role && q_res) {
+          if (lane == 0) mbar_arrive_expect_tx(qb, copy.q_bytes(nchunks));
+          __syncwarp();
+          copy.queries(qreg_u32, qb, 0, nchunks, it.q0);
+        }
+        for (int j = 0; j < T && ok; ++j) {
+          const int key0 = (it.tile0 + j) * BN;
+          uint32_t fb = 0, dst;
+          for (int pr = 0; k_role && pr < qpairs && ok; ++pr) {
+            if (!q_res) {
+              dst = copy.acquire(copy.q_bytes(kchunks), fb);
+              if (!(ok = dst != ~0u)) break;
+              if (dst) copy.queries(dst, fb, 2 * pr, kchunks, it.q0);
+            }
+            dst = copy.acquire((uint32_t)kchunks * CHUNK_BYTES, fb);
+            if (!(ok = dst != ~0u)) break;
+            if (dst) copy.rows(&p.tm_k, dst, fb, key0, BN, 2 * pr, kchunks);
+          }
+          for (int h = 0; !k_role && h < BN / vk && ok; ++h) {
+            dst = copy.acquire(vslot, fb);
+            if (!(ok = dst != ~0u)) break;
+            copy.rows(&p.tm_v, dst, fb, key0 + h * vk, vk, it.col_lo / DK, p.vchunks);
+          }
+        }
+        if (k_role && q_res) wait_drain(qb, 0, tmo, err);
+        copy.drain(k_role && inject != 0);
+      }
+    } else if (lane == 0 && T > 0) {
       const bool k_role = warp == PRODUCER_WARP;
       const int nslots = k_role ? NS : NSV;
       const uint32_t base = k_role ? ring_u32 : vring_u32;
@@ -291,7 +333,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
     bars.s_free_arrive = smem_u32(&bar_s_free);
     bars.p_full_arrive = smem_u32(&bar_p_full[0]);
     bars.pv_done = smem_u32(&bar_pv_done[0]);
-    softmax_role<VARLEN, false, UMASK>(p, it, T, tmem, warp, lane, bars, &abort_flag, tmo, err);
+    softmax_role<LAYOUT, false, UMASK>(p, it, T, tmem, warp, lane, bars, &abort_flag, tmo, err);
   }
 
   tc_fence_before();
@@ -305,9 +347,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
 
 ffpa_status launch_single(bool varlen, bool umask, const Params& P, int items, size_t smem,
                           cudaStream_t stream) {
-  auto kern = varlen  ? ffpa_fwd_kernel<true, false>
-              : umask ? ffpa_fwd_kernel<false, true>
-                      : ffpa_fwd_kernel<false, false>;
+  auto kern = varlen  ? ffpa_fwd_kernel<LAYOUT_PACKED, false>
+              : umask ? ffpa_fwd_kernel<LAYOUT_DENSE, true>
+                      : ffpa_fwd_kernel<LAYOUT_DENSE, false>;
   const ffpa_status st =
       set_smem_attr_once(reinterpret_cast<const void*>(kern), P.device, static_cast<int>(SMEM_LIMIT - SMEM_STATIC_RESERVE));
   if (st != FFPA_OK) return st;
@@ -315,5 +357,13 @@ ffpa_status launch_single(bool varlen, bool umask, const Params& P, int items, s
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
+ffpa_status launch_single_shared(const Params& P, int items, size_t smem, cudaStream_t stream) {
+  auto kern = ffpa_fwd_kernel<LAYOUT_SHARED, false>;
+  const ffpa_status st =
+      set_smem_attr_once(reinterpret_cast<const void*>(kern), P.device, static_cast<int>(SMEM_LIMIT - SMEM_STATIC_RESERVE));
+  if (st != FFPA_OK) return st;
+  kern<<<items, NTHREADS, smem, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
+}
 
 }  // namespace ffpa

@@ -31,13 +31,17 @@ namespace ffpa {
 // compile-time trip count and is fully unrolled: the tensor pipe's
 // instruction queue is shallow, and loop overhead between MMAs leaves it
 // idle (measured: a runtime-count loop of 8 MMAs runs at about half rate).
-template <bool VARLEN, int NCH, bool UMASK>
+template <int LAYOUT, int NCH, bool UMASK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
     ffpa_fwd_split_kernel(const __grid_constant__ Params p) {
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
+  constexpr bool VARLEN = LAYOUT == LAYOUT_PACKED, SHARED = LAYOUT == LAYOUT_SHARED;
   Item it;
-  if (!decode_item(p, VARLEN, blockIdx.x >> 1, it)) return;   // same answer in both CTAs
+  if (SHARED)
+    decode_item_shared(p, blockIdx.x >> 1, 1, it);
+  else if (!decode_item(p, VARLEN, blockIdx.x >> 1, it))
+    return;   // same answer in both CTAs
   it.dv = NCH * DK / 2;                                        // padded D: see split_chunks
   it.col_lo = it.dv * (int)rank;
   it.slice = (int)rank;                                        // rank 0 writes the LSE
@@ -109,7 +113,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
     // One ring, filled in the MMA thread's order: K of the first own tile,
     // then per round i: K of the own tile of round i+1, V (this CTA's
     // columns) of the own tile, V of the peer's tile.
-    if (lane == 0 && T > 0) {
+    if (SHARED) {
+      if (T > 0) {
+        if (lane == 0) {
+          prefetch_tmap(&p.tm_q);
+          prefetch_tmap(&p.tm_k);
+          prefetch_tmap(&p.tm_v);
+        }
+        SharedCopy copy{p, it, ring_u32, SLOT_BYTES, bar_full, bar_empty, NS, lane, 0, 0, 0u, inject != 0 && rank == 0, &abort_flag};
+        const uint32_t qb = smem_u32(&bar_q);
+        if (lane == 0) mbar_arrive_expect_tx(qb, copy.q_bytes(nchunks));
+        __syncwarp();
+        copy.queries(pown_u32, qb, 0, qt, it.q0);
+        copy.queries(qs_u32, qb, qt, nchunks - qt, it.q0);
+        auto load_k = [&](int j) -> bool {
+          for (int c = 0; c < nchunks; c += 2) {
+            uint32_t fb = 0;
+            const uint32_t dst = copy.acquire(2 * CHUNK_BYTES, fb);
+            if (dst == ~0u) return false;
+            if (dst) copy.rows(&p.tm_k, dst, fb, (it.tile0 + j) * BN, BN, c, 2);
+          }
+          return true;
+        };
+        auto load_v = [&](int j) -> bool {
+          for (int h = 0; h < BN / vk; ++h) {
+            uint32_t fb = 0;
+            const uint32_t dst = copy.acquire(vslot, fb);
+            if (dst == ~0u) return false;
+            copy.rows(&p.tm_v, dst, fb, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH);
+          }
+          return true;
+        };
+        bool ok = own0 >= T || load_k(own0);
+        for (int i = 0; i < R && ok; ++i) {
+          if (2 * i + 2 + own0 < T && !(ok = load_k(2 * i + 2 + own0))) break;
+          if (2 * i + own0 < T && !(ok = load_v(2 * i + own0))) break;
+          if (2 * i + peer0 < T && !(ok = load_v(2 * i + peer0))) break;
+        }
+        wait_drain(qb, 0, tmo, err);
+        copy.drain(inject != 0 && rank == 0);
+      }
+    } else if (lane == 0 && T > 0) {
       prefetch_tmap(&p.tm_q);
       prefetch_tmap(&p.tm_k);
       prefetch_tmap(&p.tm_v);
@@ -300,7 +344,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
     const int r = warp * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int row = it.q0 + r;
-    const bool row_valid = row < it.q_len;
+    const bool row_valid = row < it.q_len && (!SHARED || r < p.sh.tile_rows);
+    const int seen = SHARED ? shared_limit(p, it, it.q0, r) : 0, all_see = SHARED ? __reduce_min_sync(0xffffffffu, seen) : 0;
+    const float lift = SHARED ? p.sh.lift : 0.f;
     const long long row_limit = (long long)row + (it.kv_len - it.q_len);
     const long long first_limit = (long long)it.q0 + (it.kv_len - it.q_len);
     const uint8_t* mrow = nullptr;
@@ -364,10 +410,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_addr = lane_base + S_COL;
-        const int kbase = kv_tile(it, 2 * i + own0) * BN;
-        const bool need_mask = (kbase + BN > it.kv_len) ||
-                               (causal && (long long)kbase + BN - 1 > first_limit) ||
-                               mask_kind != FFPA_MASK_NONE;
+        const int kbase = SHARED ? (it.tile0 + 2 * i + own0) * BN : kv_tile(it, 2 * i + own0) * BN;
+        const bool need_mask = SHARED ? kbase + BN > all_see
+                                      : (kbase + BN > it.kv_len) || (causal && (long long)kbase + BN - 1 > first_limit) ||
+                                            mask_kind != FFPA_MASK_NONE;
         {
           uint32_t r0[32], r1[32], r2[32], r3[32];
           tmem_ld32(s_addr, r0);
@@ -394,7 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
             for (int c = 0; c < BN; ++c) x[c] *= ld_scale;
           }
         }
-        if (need_mask) {
+        if (SHARED && need_mask) mask_tail(x, kbase, seen);
+        if (!SHARED && need_mask) {
 #pragma unroll
           for (int q4 = 0; q4 < BN / 32; ++q4) {
             apply_mask32<UMASK>(x + 32 * q4, kbase + 32 * q4, it.kv_len, causal, row_limit, mrow,
@@ -429,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
       l_sum *= alpha;
       uint32_t pk[BN / 2];
       if (own) {
-        const float base = m_ref == -INFINITY ? 0.f : m_ref;
+        const float base = m_ref == -INFINITY ? 0.f : SHARED ? m_ref - lift : m_ref;
         // One branch per tile, not per element: the unrolled loop then holds
         // a single conversion per pair.
         l_sum += fp16 ? form_p<true, BN>(x, xs, base, pk) : form_p<false, BN>(x, xs, base, pk);
@@ -514,7 +561,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
       // it stage the output boxes for tensor stores.  Varlen: only a tile
       // whose 128 rows all lie in its sequence (a box must not reach into
       // the next sequence's rows).
-      if (p.o_tma && (!VARLEN || it.q0 + BM <= it.q_len))
+      if (SHARED)
+        store_part(p, it, 0, T > 0, lane_base, r, row_valid, l_sum, m_ref);
+      else if (p.o_tma && (!VARLEN || it.q0 + BM <= it.q_len))
         store_output_boxes<VARLEN>(p, it, T > 0, lane_base, warp, lane, row, row_valid, l_sum, m_ref,
                                    ring_u32 + (uint32_t)warp * 16384u);
       else
@@ -537,14 +586,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
   }
 }
 
-template <bool VARLEN, bool UMASK>
+template <int LAYOUT, bool UMASK>
 static ffpa_status launch_split_t(const Params& P, int items, size_t smem, cudaStream_t stream) {
   if (P.split_c != 2 || (P.nchunks != 2 && P.nchunks != 4 && P.nchunks != 6 && P.nchunks != 8))
     return FFPA_ERR_UNSUPPORTED;   // only the instantiated shapes
-  auto kern = P.nchunks == 8   ? ffpa_fwd_split_kernel<VARLEN, 8, UMASK>
-              : P.nchunks == 6 ? ffpa_fwd_split_kernel<VARLEN, 6, UMASK>
-              : P.nchunks == 4 ? ffpa_fwd_split_kernel<VARLEN, 4, UMASK>
-                               : ffpa_fwd_split_kernel<VARLEN, 2, UMASK>;
+  auto kern = P.nchunks == 8   ? ffpa_fwd_split_kernel<LAYOUT, 8, UMASK>
+              : P.nchunks == 6 ? ffpa_fwd_split_kernel<LAYOUT, 6, UMASK>
+              : P.nchunks == 4 ? ffpa_fwd_split_kernel<LAYOUT, 4, UMASK>
+                               : ffpa_fwd_split_kernel<LAYOUT, 2, UMASK>;
   const ffpa_status st =
       set_smem_attr_once(reinterpret_cast<const void*>(kern), P.device, static_cast<int>(SMEM_LIMIT - SPLIT_STATIC_RESERVE));
   if (st != FFPA_OK) return st;
@@ -554,9 +603,13 @@ static ffpa_status launch_split_t(const Params& P, int items, size_t smem, cudaS
 
 ffpa_status launch_split(bool varlen, bool umask, const Params& P, int items, size_t smem,
                          cudaStream_t stream) {
-  return varlen  ? launch_split_t<true, false>(P, items, smem, stream)
-         : umask ? launch_split_t<false, true>(P, items, smem, stream)
-                 : launch_split_t<false, false>(P, items, smem, stream);
+  return varlen  ? launch_split_t<LAYOUT_PACKED, false>(P, items, smem, stream)
+         : umask ? launch_split_t<LAYOUT_DENSE, true>(P, items, smem, stream)
+                 : launch_split_t<LAYOUT_DENSE, false>(P, items, smem, stream);
+}
+
+ffpa_status launch_split_shared(const Params& P, int items, size_t smem, cudaStream_t stream) {
+  return launch_split_t<LAYOUT_SHARED, false>(P, items, smem, stream);
 }
 
 
