@@ -169,7 +169,8 @@ bool strides_ok(const int64_t* str, const int64_t* size, int rank) {
 // A size-1 dimension gets a harmless stride so its (never used) value cannot
 // fail the encoder's alignment checks.
 ffpa_status encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base,
-                       const uint64_t* dims, const uint64_t* stride_bytes, const uint32_t* box) {
+                       const uint64_t* dims, const uint64_t* stride_bytes, const uint32_t* box,
+                       CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   auto enc = encode_fn();
   if (!enc) return FFPA_ERR_CUDA;
   cuuint64_t gdim[5];
@@ -188,7 +189,7 @@ ffpa_status encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const v
   }
   CUresult r = enc(m, dt, rank, const_cast<void*>(base), gdim, gstr, bx, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FFPA_OK : FFPA_ERR_INVALID;
 }
 
@@ -605,8 +606,12 @@ size_t plan_shared(SharedKernel k, int D, Params* P) {
 }
 
 ffpa_status encode_codes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* stride_bytes,
-                         const uint32_t* box) {
-  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, base, dims, stride_bytes, box);
+                         const uint32_t* box, int row_bytes) {
+  const CUtensorMapL2promotion l2 = row_bytes % 256 == 0   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                    : row_bytes % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                    : row_bytes % 64 == 0  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                           : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, base, dims, stride_bytes, box, l2);
 }
 
 // Kernels whose shared-memory limit was raised, per device (set-once facts).

@@ -103,8 +103,8 @@ struct DecodeParams {
   float scale_log2;
 };
 
-// Sizes of one call.  A tile has T = 16 keys for D > 512 and twice as many each
-// time D halves (at most 32 KB).
+// Sizes of one call.  A tile has T = 16 keys for rows of more than 1 KB and twice as many each
+// time they halve (at most 32 KB).
 struct DecodePlan {
   int nt, ctas, tile, chunks, ring_k, ring_v, head_tiles;
   size_t smem;
@@ -122,18 +122,30 @@ __host__ __device__ constexpr int decode_parts(int tile) { return tile >= 128 ? 
 __host__ __device__ constexpr int decode_groups(int tile) { return tile >= 32 ? tile / 32 : 1; }
 // Scores of two tiles (of one where a warp reads no other's).
 __host__ __device__ constexpr bool decode_own_keys(int tile) { return tile / 16 > DEC_WARPS; }
-__host__ __device__ constexpr size_t decode_score_bytes(int nt, int tile) {
-  return ((size_t)(decode_own_keys(tile) ? 1 : 2) * decode_parts(tile) * 8 * nt * (tile + 8) * 4 + 1023) / 1024 * 1024;
+// Column tiles of a warp in the second product (e4m3: twice the columns, as its tiles hold twice the keys).
+__host__ __device__ constexpr int decode_columns(int kind, int tile) { return kind == DECODE_E4M3 || tile < 32 ? 8 : 4; }
+// A head's sums of all groups of warps, as they are joined at a pair's end.
+__host__ __device__ constexpr size_t decode_join_bytes(int kind, int tile) {
+  return (size_t)decode_groups(tile) * (DEC_WARPS / decode_groups(tile) * decode_columns(kind, tile) * 16 + 4) * 4;
 }
+// (e4m3: room for the sums of eight heads where the ring leaves it, else four.)
+__host__ __device__ constexpr size_t decode_score_bytes(int kind, int nt, int tile) {
+  const size_t scores = (size_t)(decode_own_keys(tile) ? 1 : 2) * decode_parts(tile) * 8 * nt * (tile + 8) * 4;
+  const size_t join = kind == DECODE_E4M3 && tile >= 64 ? decode_join_bytes(kind, tile) * (tile >= 128 ? 8 : 4) : 0;
+  return ((scores > join ? scores : join) + 1023) / 1024 * 1024;
+}
+// e4m3: the queries of a pair as operands of the first product, 16 bytes a lane for 32 columns, and their units.
+__host__ __device__ constexpr size_t decode_query_bytes(int nt, int D) { return ((size_t)(D + 31) / 32 * nt * 512 + 64 * nt + 1023) / 1024 * 1024; }
 
 DecodePlan decode_plan(int D, int group, int kind) {
   DecodePlan p;
   p.nt = decode_nt(group);
   p.ctas = decode_ctas(p.nt);
   p.head_tiles = (group + 8 * p.nt - 1) / (8 * p.nt);
-  p.tile = D > 512 ? 16 : D > 256 ? 32 : D > 128 ? 64 : D > 64 ? 128 : 256;
-  p.chunks = (D * cache_bytes(kind) + 127) / 128;
-  const size_t fixed = decode_score_bytes(p.nt, p.tile);
+  const int row = D * cache_bytes(kind);
+  p.tile = row > 1024 ? 16 : row > 512 ? 32 : row > 256 ? 64 : row > 128 ? 128 : 256;
+  p.chunks = (row + 127) / 128;
+  const size_t fixed = decode_score_bytes(kind, p.nt, p.tile) + (kind == DECODE_E4M3 ? decode_query_bytes(p.nt, D) : 0);
   const size_t stage = (size_t)p.tile * (p.chunks * 128 + (kind == DECODE_E4M3 ? 4 : 0));
   // 8 KB a CTA stay for static shared memory, the alignment of the boxes, the system,
   // and a block of the joining kernel that is set up early (with 4 KB left 1 us more).
@@ -446,6 +458,55 @@ __device__ __forceinline__ void write_columns(char* out, int64_t o_sh, int heads
   if (head < heads && d < D) *reinterpret_cast<uint4*>(out + head * o_sh + d * 2) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// One head's queries as fp16 operands of the first product with e4m3 keys, by a warp: of
+// 32 columns, lane 4 head + c of a matrix load gets columns 4 c .. 4 c + 3 of either half; the
+// first two of each are column pair c of one step of 16, the others of the next.  bf16 queries
+// come in units of a power of two that lifts the largest to 2^14 .. 2^15: exact from 2^-28 of it on
+// and off by 2^-40 of it below.
+template <bool F16>
+__device__ __forceinline__ void bring_queries(const char* q, bool there, int D, char* query_s, int step, int head, float* unit) {
+  const int lane = threadIdx.x % 32;
+  uint4 x[4];
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int d = (i * 32 + lane) * 8;
+    x[i] = there && d < D ? *reinterpret_cast<const uint4*>(q + d * 2) : make_uint4(0, 0, 0, 0);
+  }
+  if (!F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = unpack2<false>(w[j]);
+        most = fmax3(most, fabsf(y.x), fabsf(y.y));
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+  }
+  const int e = min(max((int)(__float_as_uint(most) >> 23), 16), 254);
+  const float up = __uint_as_float((268 - e) << 23);
+  if (lane == 0) *unit = F16 ? 1.0f : __uint_as_float((e - 14) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int d = (i * 32 + lane) * 8;               // columns d .. d + 7: c = 0, 1 or 2, 3 of a half
+    if (d >= (D + 31) / 32 * 32) continue;
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h = w[j];
+      if (!F16) {
+        const float2 y = unpack2<false>(h);
+        h = pack_f16(y.x * up, y.y * up);
+      }
+      const int c = d % 16 / 4 + j / 2;
+      *reinterpret_cast<uint32_t*>(query_s + d / 32 * step + (head * 4 + c) * 16 + (j % 2 * 2 + d % 32 / 16) * 4) = h;
+    }
+  }
+}
+
 // Two column tiles as they come of e4m3 values (a lane holds columns 2 r and 2 r + 1
 // of a tile, r = lane / 4, in place of r and r + 8): 32 bytes of each head and tile.
 template <bool F16>
@@ -465,9 +526,10 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   constexpr int HEADS = 8 * NT, THREADS = DEC_THREADS;
   constexpr int PARTS = decode_parts(T), GROUPS = decode_groups(T), MT = T / 16;
   constexpr int KSTEPS = T < 32 ? 1 : 2;      // of 16 keys, of a warp in the second product
-  constexpr int DT = T < 32 ? 8 : 4;          // column tiles of a warp there
+  constexpr int DT = decode_columns(KIND, T); // column tiles of a warp there
   constexpr int WDS = DEC_WARPS / GROUPS;     // warps that share keys there
   constexpr int SPITCH = T + 8, SBUF = PARTS * HEADS * SPITCH;
+  constexpr int N = DEC_WARPS * 32;           // threads that compute
   constexpr bool OWN = decode_own_keys(T);    // a warp's scores are those of its own keys
   extern __shared__ char smem_raw[];
   __shared__ uint64_t full_k[DEC_RING_MAX], full_v[DEC_RING_MAX], empty_k[DEC_RING_MAX], empty_v[DEC_RING_MAX];
@@ -561,7 +623,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     if (c >= runs) return;   // (an exit counts for the dependent launch too)
     // Columns behind D meet zeros of Q and must be finite (boxes bring zeros).
     if (!P.boxed && P.D * cache_bytes(KIND) % 32 != 0) {
-      char* ring = smem + decode_score_bytes(NT, T);
+      char* ring = smem + decode_score_bytes(KIND, NT, T) + (E4M3 ? decode_query_bytes(NT, P.D) : 0);
       const int c16 = P.D * cache_bytes(KIND) / 16;
       for (int i = tid; i < (P.ring_k + P.ring_v) * T; i += THREADS)
         *reinterpret_cast<uint4*>(ring + (size_t)(i / T) * stage + (c16 >> 3) * (T * 128) + (i % T) * 128 +
@@ -578,10 +640,14 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   dependents_launch();
   const int n_tiles = (int)(hi - lo);
   float* scores = reinterpret_cast<float*>(smem);                  // [2, or 1 when OWN][PARTS][HEADS][SPITCH]
-  const uint32_t ring_k = smem_u32(smem + decode_score_bytes(NT, T));
+  const size_t fixed = decode_score_bytes(KIND, NT, T) + (E4M3 ? decode_query_bytes(NT, P.D) : 0);
+  const uint32_t ring_k = smem_u32(smem + fixed);
+  // (e4m3: the queries [32 columns][NT][lane] and their units [head], behind the scores)
+  char* query_s = smem + decode_score_bytes(KIND, NT, T);
+  float* unit_s = reinterpret_cast<float*>(query_s + (P.D + 31) / 32 * NT * 512);
   const uint32_t ring_v = ring_k + P.ring_k * stage;
   // (e4m3: the rows' scales behind the tiles)
-  float* scale_k = reinterpret_cast<float*>(smem + decode_score_bytes(NT, T) + (size_t)(P.ring_k + P.ring_v) * stage);
+  float* scale_k = reinterpret_cast<float*>(smem + fixed + (size_t)(P.ring_k + P.ring_v) * stage);
   float* scale_v = scale_k + P.ring_k * T;
 
   if (warp >= DEC_WARPS) {
@@ -605,7 +671,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   const int kper = (P.chunks + PARTS - 1) / PARTS * CHUNK;
   const int k0 = part * kper, kn = max(0, min(kper, ksteps - k0));
   const int wkey = warp / WDS, wd = warp % WDS;    // group of keys, share of columns
-  const int dper = E4M3 ? DT : (P.chunks + WDS - 1) / WDS * 4;   // (e4m3: half a chunk, or a whole one)
+  const int dper = E4M3 ? DT : (P.chunks + WDS - 1) / WDS * 4;   // (e4m3: a chunk)
   const int d0 = wd * dper, dn = max(0, min(dper, ksteps - d0));
   const int c2 = (lane % 4) * 2, hq = lane / 4;
   const uint32_t chunk_bytes = P.box_rows * 128;
@@ -615,22 +681,22 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   const int kr = key0 + (lane & 15);
   const uint32_t k_at = ring_k + row_at(kr) + k0 / CHUNK * chunk_bytes + (((lane >> 4) ^ (lane & 7)) << 4);
   const uint32_t k_at2 = OWN ? k_at - row_at(kr) + row_at(kr + 16) : 0;
-  // A matrix load brings 16 keys of 16 columns; of e4m3 values 32 keys of 16 columns, or 16
-  // of 32 where the warp has only 16.
-  const int vr = wkey * 32 + (!E4M3 ? (lane >> 4) * 8 + (lane & 7) : KSTEPS == 2 ? lane : lane & 15);
-  const int v_unit = !E4M3 ? (lane >> 3) & 1 : KSTEPS == 2 ? d0 & 4 : lane >> 4;
+  // A matrix load brings 16 keys of 16 columns; of e4m3 values 32 keys of 16 columns.
+  static_assert(!E4M3 || KSTEPS == 2, "32 keys a warp");
+  const int vr = wkey * 32 + (E4M3 ? lane : (lane >> 4) * 8 + (lane & 7));
+  const int v_unit = E4M3 ? 0 : (lane >> 3) & 1;
   const uint32_t v_x = d0 / CHUNK * chunk_bytes + ((v_unit ^ (lane & 7)) << 4);
   const uint32_t v_at = ring_v + row_at(vr) + v_x, v_at2 = E4M3 ? 0 : ring_v + row_at(vr + 16) + v_x;
-  uint32_t qf[8][NT][2];
+  uint32_t qf[E4M3 ? 1 : 8][NT][2];                // (e4m3: from shared memory)
   float acc[DT][NT][4];
   float top[NT], sum[NT];                          // of head 8 n + lane / 4
+  const uint32_t query_at = smem_u32(query_s) + k0 / 2 * NT * 512 + lane * 16;   // e4m3: of this warp's part
   float vtop[NT];                                  // e4m3: log2 of the unit of acc
   float q_unit[NT][2];                             // e4m3, bf16 queries: the units of heads c2 and c2 + 1
   int slot_k = 0, slot_v = 0;
   uint32_t lap_k = 0, lap_v = 0;
   bool alive = true;
   int buf = 0;
-  constexpr int N = DEC_WARPS * 32;
 
   for (int i0 = 0, turn = 0; i0 < n_tiles; turn ^= 1) {
     // ---- one pair's tiles of this run: [i0, i1)
@@ -646,24 +712,23 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     const int hk = cur.u / P.head_tiles, ht = cur.u % P.head_tiles;
     const int hq0 = hk * P.group + ht * HEADS;
     const int rows = min(HEADS, P.group - ht * HEADS);
+    if (E4M3) {
+      // (the last pair's scores are formed: all warps are behind a barrier that follows them)
+      for (int head = warp; head < HEADS; head += DEC_WARPS)
+        bring_queries<F16>(P.q + cur.b * P.q_sb + (int64_t)(hq0 + head) * P.q_sh, head < rows, P.D, query_s + head / 8 * 512, NT * 512,
+                           head % 8, unit_s + head);
+      named_bar_sync(1, N);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        q_unit[n][0] = unit_s[n * 8 + c2];
+        q_unit[n][1] = unit_s[n * 8 + c2 + 1];
+      }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int head = n * 8 + hq;
       const char* src = P.q + cur.b * P.q_sb + (int64_t)(hq0 + head) * P.q_sh;
-      if (E4M3) {
-        // Lane c of a head takes the columns that lane c of a matrix load gets: 4 c .. 4 c + 3
-        // of 16; the first two are column pair c of one step, the others of the next.
-#pragma unroll
-        for (int s = 0; s < 8; s += 2)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int d = (k0 + s + j) * 16 + lane % 4 * 4;
-            uint2 x = make_uint2(0, 0);
-            if (head < rows && s + j < kn && d < P.D) x = *reinterpret_cast<const uint2*>(src + d * 2);
-            qf[s][n][j] = x.x;
-            qf[s + 1][n][j] = x.y;
-          }
-      } else
+      if (!E4M3)
 #pragma unroll
       for (int s = 0; s < 8; s += 2) {             // 16 bytes a lane
         const int d = (k0 + s) * 16 + lane % 4 * 8;
@@ -700,34 +765,6 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
 
       // ---- scores of 16 keys over this warp's part of D
       if (alive) alive = all_waited(smem_u32(full_k + slot_k), lap_k, P, &abort_flag);
-      if (E4M3 && i == i0 && !F16) {
-        // bf16 queries as fp16, in units of a power of two that lifts the largest of the warp's
-        // columns to 2^14 .. 2^15: exact from 2^-28 of it on, and off by 2^-40 of it below.
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float most = 0.0f;
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 x = unpack2<false>(qf[s][n][j]);
-              most = fmax3(most, fabsf(x.x), fabsf(x.y));
-            }
-          most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-          const int e = min(max((int)(__float_as_uint(most) >> 23), 16), 254);
-          const float up = __uint_as_float((268 - e) << 23), down = __uint_as_float((e - 14) << 23);
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 x = unpack2<false>(qf[s][n][j]);
-              qf[s][n][j] = pack_f16(x.x * up, x.y * up);
-            }
-          q_unit[n][0] = __shfl_sync(~0u, down, c2 * 4);
-          q_unit[n][1] = __shfl_sync(~0u, down, c2 * 4 + 4);
-        }
-      }
       if (!E4M3 && i == i0) {                      // Q is here too: dealt out to the four lanes of a head
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -751,16 +788,18 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
           for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
         if (E4M3) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 8; ++x) {
             if (2 * x >= kn) break;
             uint32_t c[4], lo[4], hi[4];
-            ldm_x4(a0 ^ (x << 5), c);
+            ldm_x4((a0 + (x >> 2) * chunk_bytes) ^ ((x & 3) << 5), c);
 #pragma unroll
             for (int j = 0; j < 4; ++j) widen_e4m3(c[j], lo[j], hi[j]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma16<true>(s[n], lo, qf[2 * x][n]);
-              mma16<true>(s[n], hi, qf[2 * x + 1][n]);
+              const uint4 qx = ld_shared_v4(query_at + (x * NT + n) * 512);
+              const uint32_t q0[2] = {qx.x, qx.y}, q1[2] = {qx.z, qx.w};
+              mma16<true>(s[n], lo, q0);
+              mma16<true>(s[n], hi, q1);
             }
           }
           // times the keys' scales and the queries' units
@@ -897,17 +936,17 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         // A matrix load leaves a lane two neighbouring columns of two keys: the codes of one
         // column are its bytes 0 and 2, those of the next 1 and 3.
 #pragma unroll
-        for (int s = 0; s < DT; s += 3 - KSTEPS) {
+        for (int s = 0; s < DT; ++s) {
           if (s >= dn) break;
           uint32_t c[4];
           ldm_x4_trans((v_at + slot_v * stage) ^ (s << 4), c);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {              // steps of 16 keys, or column tiles
+          for (int g = 0; g < KSTEPS; ++g) {
             uint32_t a[4];
             widen_e4m3(__byte_perm(c[2 * g], 0, 0x3120), a[0], a[1]);
             widen_e4m3(__byte_perm(c[2 * g + 1], 0, 0x3120), a[2], a[3]);
             if (tail) {
-              const int k = (KSTEPS == 2 ? g * 16 : 0) + c2;
+              const int k = g * 16 + c2;
               const uint32_t m0 = (k < left ? 0xffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
               const uint32_t m1 = (k + 8 < left ? 0xffffu : 0u) | (k + 9 < left ? 0xffff0000u : 0u);
               a[0] &= m0;
@@ -915,11 +954,10 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
               a[2] &= m1;
               a[3] &= m1;
             }
-            constexpr int ACROSS = KSTEPS == 2 ? 0 : 1;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16<true>(acc[s + ACROSS * g][n], a, pf[(1 - ACROSS) * g][n]);
+            for (int n = 0; n < NT; ++n) mma16<true>(acc[s][n], a, pf[g][n]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16<true>(acc[s + ACROSS * g][n], a, pr[(1 - ACROSS) * g][n]);
+            for (int n = 0; n < NT; ++n) mma16<true>(acc[s][n], a, pr[g][n]);
           }
         }
       } else
@@ -1034,7 +1072,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     } else {
       // Every group leaves its sums where the scores were, as many heads at a
       // time as fit, and all threads join them two columns at a time.
-      constexpr int RP = WDS * DT * 16 + 4, ROUND = decode_score_bytes(NT, T) / (GROUPS * RP * 4);
+      constexpr int RP = WDS * DT * 16 + 4, ROUND = decode_score_bytes(KIND, NT, T) / decode_join_bytes(KIND, T);
       static_assert(ROUND >= 1, "a head's sums fit");
       const int half_d = P.D / 2;
 #pragma unroll 1
@@ -1252,7 +1290,8 @@ ffpa_status launch_decode_tile(const DecodeParams& P, const DecodePlan& pl, int 
 template <int KIND, bool F16>
 ffpa_status launch_decode(const DecodeParams& P, const DecodePlan& pl, int grid, int dev, cudaStream_t stream) {
   switch (pl.tile) {
-    case 16: return launch_decode_tile<KIND, F16, 16>(P, pl, grid, dev, stream);
+    case 16:   // (rows of more than 1 KB: never codes)
+      return launch_decode_tile<KIND, F16, KIND == DECODE_E4M3 ? 32 : 16>(P, pl, grid, dev, stream);
     case 32: return launch_decode_tile<KIND, F16, 32>(P, pl, grid, dev, stream);
     case 64: return launch_decode_tile<KIND, F16, 64>(P, pl, grid, dev, stream);
     case 128: return launch_decode_tile<KIND, F16, 128>(P, pl, grid, dev, stream);
@@ -1357,12 +1396,12 @@ ffpa_status run_decode(DecodeParams& P, const DecodeShape& s, ffpa_dtype dt, flo
         const uint64_t dims[5] = {wide, (uint64_t)s.page_size, (uint64_t)pl.chunks, (uint64_t)s.Hkv, (uint64_t)s.num_pages};
         const uint64_t str[4] = {row, 128, head, page};
         const uint32_t box[5] = {wide, (uint32_t)P.box_rows, (uint32_t)pl.chunks, 1, 1};
-        st = KIND == DECODE_E4M3 ? encode_codes(map, 5, base, dims, str, box) : encode_rows(map, dt, 5, base, dims, str, box);
+        st = KIND == DECODE_E4M3 ? encode_codes(map, 5, base, dims, str, box, s.D) : encode_rows(map, dt, 5, base, dims, str, box);
       } else {
         const uint64_t dims[4] = {(uint64_t)s.D, (uint64_t)s.page_size, (uint64_t)s.Hkv, (uint64_t)s.num_pages};
         const uint64_t str[3] = {row, head, page};
         const uint32_t box[4] = {wide, (uint32_t)P.box_rows, 1, 1};
-        st = KIND == DECODE_E4M3 ? encode_codes(map, 4, base, dims, str, box) : encode_rows(map, dt, 4, base, dims, str, box);
+        st = KIND == DECODE_E4M3 ? encode_codes(map, 4, base, dims, str, box, s.D) : encode_rows(map, dt, 4, base, dims, str, box);
       }
       if (st != FFPA_OK) return st;
     }

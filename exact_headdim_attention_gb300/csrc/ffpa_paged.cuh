@@ -22,9 +22,10 @@ ffpa_status call_status(int dev, const ffpa_options* options, int** err, int* sm
 ffpa_status encode_rows(CUtensorMap* map, ffpa_dtype dt, int rank, const void* base, const uint64_t* dims,
                         const uint64_t* stride_bytes, const uint32_t* box);
 
-// The same of boxes of 128 8-bit values.
+// The same of boxes of 128 8-bit values.  A head's row has row_bytes bytes: what L2 fetches at a time
+// divides it (B128 Hkv16 D128 with 256 bytes read 766 MB of 535, the next head's codes with each).
 ffpa_status encode_codes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* stride_bytes,
-                         const uint32_t* box);
+                         const uint32_t* box, int row_bytes);
 
 // Kernels that take the keys which a decode batch shares: which one, its CTAs an item, its plan
 // (sizes in *P; the dynamic shared memory is returned).
