@@ -54,7 +54,7 @@ __device__ __forceinline__ float max_from_bits(uint32_t h) { return __uint_as_fl
 // instruction queue is shallow, and loop overhead between MMAs leaves it
 // idle (measured: a runtime-count loop of 8 MMAs runs at about half rate).
 template <int LAYOUT, int NCH, bool UMASK, int C>
-__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(split_threads(LAYOUT), 1)
     ffpa_fwd_cluster_kernel(const __grid_constant__ Params p) {
   static_assert(C >= 2 && C <= 4 && NCH % C == 0 && NCH % 2 == 0, "unsupported split");
   const uint32_t rank = cluster_ctarank();
@@ -131,13 +131,14 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
   cluster_sync_all();      // every CTA's barriers exist before any remote operation
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  if (SHARED) dependents_launch();   // own keys run beside this kernel, where SMs are free
   const int T = it.ntiles;
   const int R = (T + C - 1) / C;                 // rounds of C key tiles
   const int own0 = (int)rank;                    // own tile of round i: C i + own0
   const unsigned long long tmo = p.timeout_ns;
   int* const err = p.err;
 
-  if (warp == PRODUCER_WARP) {
+  if (warp == PRODUCER_WARP || (SHARED && warp > MMA_WARP)) {
     // ------------------------------------------------------------ producer
     // One ring, filled in the MMA thread's order: QK^T stages (K pairs, and
     // Q pairs before the K pairs they meet when Q is streamed) of the first
@@ -150,13 +151,17 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
           prefetch_tmap(&p.tm_k);
           prefetch_tmap(&p.tm_v);
         }
-        SharedCopy copy{p, it, ring_u32, SLOT_BYTES, bar_full, bar_empty, NS, lane, 0, 0, 0u, inject != 0 && rank == 0, &abort_flag};
+        const int me = warp == PRODUCER_WARP ? 0 : warp - MMA_WARP;   // of three
+        SharedCopy copy{p, it, ring_u32, SLOT_BYTES, bar_full, bar_empty, NS, lane, 3, me, inject != 0 && rank == 0, &abort_flag};
         const uint32_t qb = smem_u32(&bar_q);
-        if (lane == 0) mbar_arrive_expect_tx(qb, copy.q_bytes(QRES ? NCH : qt));
-        __syncwarp();
-        copy.queries(pbuf_u32, qb, 0, qt, it.q0);
-        if (QRES) copy.queries(qs_u32, qb, qt, NCH - qt, it.q0);
+        if (me == 0) {
+          if (lane == 0) mbar_arrive_expect_tx(qb, copy.q_bytes(QRES ? NCH : qt));
+          __syncwarp();
+          copy.queries(pbuf_u32, qb, 0, qt, it.q0);
+          if (QRES) copy.queries(qs_u32, qb, qt, NCH - qt, it.q0);
+        }
         auto load_qk = [&](int j) -> bool {
+          if (me == 0) copy.ahead(j + p.sh.ahead);
           for (int c = 0; c < NCH; c += 2) {
             uint32_t fb = 0;
             if (!QRES && c >= qt) {
@@ -166,7 +171,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
             }
             const uint32_t dst = copy.acquire(2 * CHUNK_BYTES, fb);
             if (dst == ~0u) return false;
-            if (dst) copy.rows(&p.tm_k, dst, fb, (it.tile0 + j) * BN, BN, c, 2);
+            if (dst) copy.keys(dst, fb, (it.tile0 + j) * BN, c, 2);
           }
           return true;
         };
@@ -175,7 +180,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
             uint32_t fb = 0;
             const uint32_t dst = copy.acquire(vslot, fb);
             if (dst == ~0u) return false;
-            if (dst) copy.rows(&p.tm_v, dst, fb, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH);
+            if (dst) copy.values(dst, fb, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH);
           }
           return true;
         };
@@ -188,7 +193,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
           }
         }
         wait_drain(qb, 0, tmo, err);
-        copy.drain(inject != 0 && rank == 0);
+        copy.drain();
       }
     } else if (lane == 0 && T > 0) {
       prefetch_tmap(&p.tm_q);
@@ -304,7 +309,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
       const uint64_t ring_desc = sdesc_sw128(ring_u32, 16, 1024);
       const uint64_t qs_desc = sdesc_sw128(qs_u32, 16, 1024);
       const uint64_t pbuf_desc = sdesc_sw128(pbuf_u32, 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(ring_u32, vk * 128, 1024);
+      const uint64_t v_desc = SHARED ? shared_v_desc(ring_u32, p.sh.v_rows, VCH) : sdesc_sw128(ring_u32, vk * 128, 1024);
       const uint32_t s_col = tmem + S_COL;
       const uint32_t q_col = tmem + Q_TMEM_COL;
       ok = wait_on(smem_u32(&bar_q), 0) && wait_on(smem_u32(&bar_qt), 0);
@@ -359,7 +364,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
             // per 16 keys), V (MN-major, +2048 bytes per 16 keys).
             const int key = h * vk + 16 * kk;
             const uint64_t ad = a_desc + (((key >> 6) * CHUNK_BYTES) >> 4) + 2 * ((key & 63) >> 4);
-            umma_ss(tmem, ad, vd + 128 * kk, idesc_pv, o_acc ? 1u : 0u);
+            umma_ss(tmem, ad, vd + (SHARED ? shared_v_at(16 * kk, p.sh.v_rows, VCH) : 128 * kk), idesc_pv, o_acc ? 1u : 0u);
             o_acc = true;
           }
           umma_commit(smem_u32(&bar_empty[s]));
@@ -665,7 +670,7 @@ static ffpa_status launch_cluster_nc(const Params& P, int items, size_t smem, cu
   const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(kern), P.device,
                                             static_cast<int>(SMEM_LIMIT - SPLIT_STATIC_RESERVE));
   if (st != FFPA_OK) return st;
-  kern<<<C * items, SPLIT_THREADS, smem, stream>>>(P);
+  kern<<<C * items, split_threads(LAYOUT), smem, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
 }
 

@@ -72,6 +72,7 @@ constexpr uint32_t Q_TMEM_COL = 384;
 constexpr int Q_TMEM_MAX_CHUNKS = 4;
 constexpr uint32_t P_TILE_BYTES = BM * BN * 2;   // 2 x (128 rows x 64 keys), 16-bit
 constexpr size_t SPLIT_STATIC_RESERVE = 2048;    // static shared memory of the column-split kernel
+constexpr int split_threads(int layout) { return layout == 2 ? SPLIT_THREADS + 64 : SPLIT_THREADS; }   // (shared pages: two more copying warps)
 
 // ------------------------------------------------------------------ host
 // Launches of the forward kernels (one translation unit each; the column
@@ -257,6 +258,10 @@ struct SharedKeys {
   float2* part_ml;           // [item][128 rows] (maximum in log2 units, sum)
   int n_pages, num_pages, page_size;
   int box_rows;              // keys of a box: a power of two of 8 .. 128 that divides page_size
+  int v_rows;                // the same of V, whose boxes hold all chunks of a stage
+  int ahead;                 // key tiles (of the item) that are asked for ahead, into L2; 0: none
+  int ahead_rows;            // keys of a box that does so, all chunks of a row
+  CUtensorMap tm_k_ahead, tm_v_ahead;
   int tile_rows;             // rows of a query tile: whole requests, at most 128
   int splits;                // parts of the keys
   float lift;                // log2 of the factor on P (fp16: small weights stay in its range)
@@ -312,7 +317,7 @@ struct Item {
   int q0, q_len, kv_len, q_row0, kv_row0;
   int col_lo, dv, ntiles;
   int rot;   // first key tile visited; tiles are visited rot, rot+1, ... (mod ntiles)
-  int tile0, part;   // LAYOUT_SHARED: the first key tile of the item's part; its place in SharedKeys::part
+  int tile0, part, qt;   // LAYOUT_SHARED: the first key tile of the item's part; its place in SharedKeys::part; query tile
 };
 
 // Key tile visited at step j.  Work items of one head start at different
@@ -396,6 +401,7 @@ __device__ __forceinline__ void decode_item_shared(const Params& p, int L, int p
   it.tile0 = (int)(tiles * split / s.splits);
   it.ntiles = (int)(tiles * (split + 1) / s.splits) - it.tile0;
   it.part = ((it.hkv * s.splits + split) * p.n_qt + qt) * per;
+  it.qt = qt;
   it.rot = 0;
   const int c_lo = it.slice * p.nchunks / p.n_slices;
   const int c_hi = (it.slice + 1) * p.nchunks / p.n_slices;
@@ -692,76 +698,105 @@ __device__ __forceinline__ void store_part(const Params& p, const Item& it, int 
   }
 }
 
-// The copying warp of LAYOUT_SHARED: all its lanes, a box of a stage each.
+// A copying warp of LAYOUT_SHARED: all its lanes, a box of a stage each.  An SM starts a box every
+// hundred cycles or so a warp, and small pages make many boxes, so `copiers` warps share a
+// ring: every warp walks through all stages and takes those of its own slots (a wait by
+// parity must see every phase of its barrier, so a slot has one copier).
 struct SharedCopy {
   const Params& p;
   const Item& it;
   uint32_t ring, stride;
   uint64_t *full, *empty;
-  int slots, lane, slot = 0, issued = 0;
-  uint32_t lap = 0;
-  bool drop;
+  int slots, lane, copiers, me;      // this warp has the slots s with s % copiers == me
+  bool drop;                         // test hook: the first stage never comes
   volatile int* abort_flag;
+  int slot = 0;
+  uint32_t lap = 0, armed = 0, parity = 0;   // (bits: the slots that this warp armed, and their phases)
 
-  // The next stage, armed for `bytes`: its address, 0 where the test hook drops it, ~0 on abort.
+  // The next stage, armed for `bytes`: its address, 0 where it is not this warp's, ~0 on abort.
   __device__ __forceinline__ uint32_t acquire(uint32_t bytes, uint32_t& fb) {
-    const uint32_t eb = smem_u32(&empty[slot]);
-    const bool w = mbar_try_wait(eb, lap ^ 1u) || wait_bounded_inl(eb, lap ^ 1u, abort_flag, p.timeout_ns, p.err);
-    if (!__all_sync(0xffffffffu, w)) return ~0u;
-    fb = smem_u32(&full[slot]);
-    const uint32_t dst = ring + slot * stride;
-    ++issued;
+    const int s = slot;
+    const uint32_t l = lap;
     if (++slot == slots) {
       slot = 0;
       lap ^= 1u;
     }
-    if (drop) {
-      drop = false;
-      return 0u;
-    }
+    const bool dropped = drop;
+    drop = false;
+    if (s % copiers != me) return 0u;
+    const uint32_t eb = smem_u32(&empty[s]);
+    const bool w = mbar_try_wait(eb, l ^ 1u) || wait_bounded_inl(eb, l ^ 1u, abort_flag, p.timeout_ns, p.err);
+    if (!__all_sync(0xffffffffu, w)) return ~0u;
+    if (dropped) return 0u;
+    fb = smem_u32(&full[s]);
     if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
     __syncwarp();
-    return dst;
+    armed |= 1u << s;
+    parity = (parity & ~(1u << s)) | l << s;
+    return ring + s * stride;
   }
   // `chunks` chunks from chunk0 of the queries of a tile, each of tile_rows rows, 16 KB apart.
   __device__ __forceinline__ uint32_t q_bytes(int chunks) const { return (uint32_t)chunks * p.sh.tile_rows * 128u; }
   __device__ __forceinline__ void queries(uint32_t dst, uint32_t bar, int chunk0, int chunks, int row0) {
     if (lane < chunks) tma_load_5d(dst + lane * CHUNK_BYTES, &p.tm_q, bar, 0, 0, row0 / p.group, chunk0 + lane, it.hkv);
   }
-  // `keys` keys from key0 on (the first a multiple of the box), `chunks` chunks from chunk0, each
-  // `keys` rows.  What lies behind the last key, and a page that does not exist, becomes zeros.
-  __device__ __forceinline__ void rows(const CUtensorMap* map, uint32_t dst, uint32_t bar, int key0, int keys, int chunk0, int chunks) {
+  // Place of a key in its page; what lies behind the last key, and a page that does not exist, is
+  // outside the tensor: zeros.
+  __device__ __forceinline__ void place(int key, int& y, int& z) {
     const SharedKeys& s = p.sh;
-    const int boxes = keys / s.box_rows, c = lane / boxes, i = lane - c * boxes;
-    if (c >= chunks) return;
-    const int key = key0 + i * s.box_rows;
-    int y = 0, z = s.num_pages;
-    if (key < it.kv_len) {
-      const int j = key / s.page_size, page = __ldg(s.pages + j);
-      if (page >= 0 && page < s.num_pages) {
-        y = key - j * s.page_size;
-        z = page;
-      } else {
-        atomicCAS(p.err, 0, static_cast<int>(FFPA_ERR_INVALID));
-      }
+    y = 0;
+    z = s.num_pages;
+    if (key >= it.kv_len) return;
+    const int j = key / s.page_size, page = __ldg(s.pages + j);
+    if (page >= 0 && page < s.num_pages) {
+      y = key - j * s.page_size;
+      z = page;
+    } else {
+      atomicCAS(p.err, 0, static_cast<int>(FFPA_ERR_INVALID));
     }
-    tma_load_5d(dst + (uint32_t)(c * keys + i * s.box_rows) * 128u, map, bar, 0, y, chunk0 + c, it.hkv, z);
   }
-  // Every copy lands before the CTA ends (a dropped stage, the first, was never armed).
-  __device__ __forceinline__ void drain(bool dropped) {
-    const int n = issued < slots ? issued : slots;
-    int s = slot;
-    uint32_t lp = lap;
-    for (int i = 0; i < n; ++i) {
-      if (--s < 0) {
-        s = slots - 1;
-        lp ^= 1u;
-      }
-      if (dropped && issued - 1 - i == 0) continue;
-      wait_drain_inl(smem_u32(&full[s]), lp, p.timeout_ns, p.err);
-    }
+  // K: `chunks` chunks from chunk0 of the 128 keys from key0 on, chunk after chunk (a box each and page part).
+  __device__ __forceinline__ void keys(uint32_t dst, uint32_t bar, int key0, int chunk0, int chunks) {
+    const int boxes = BN / p.sh.box_rows, c = lane / boxes, i = lane - c * boxes;
+    if (c >= chunks) return;
+    int y, z;
+    place(key0 + i * p.sh.box_rows, y, z);
+    tma_load_5d(dst + (uint32_t)(c * BN + i * p.sh.box_rows) * 128u, &p.tm_k, bar, 0, y, chunk0 + c, it.hkv, z);
+  }
+  // V: `rows` keys from key0 on, chunks chunk0 .. of the boxes: v_rows keys of all chunks, box after box.
+  __device__ __forceinline__ void values(uint32_t dst, uint32_t bar, int key0, int rows, int chunk0, int chunks) {
+    const int vr = p.sh.v_rows;
+    if (lane >= rows / vr) return;
+    int y, z;
+    place(key0 + lane * vr, y, z);
+    tma_load_5d(dst + (uint32_t)(lane * chunks * vr) * 128u, &p.tm_v, bar, 0, y, chunk0, it.hkv, z);
+  }
+  // Keys and values of tile j of the item on their way to L2, from the query tile whose turn it is.
+  __device__ __forceinline__ void ahead(int j) {
+    const SharedKeys& s = p.sh;
+    const int boxes = BN / s.ahead_rows;
+    if (s.ahead == 0 || j >= it.ntiles || lane >= 2 * boxes || (it.tile0 + j) % p.n_qt != it.qt) return;
+    const bool v = lane >= boxes;
+    int y, z;
+    place((it.tile0 + j) * BN + (v ? lane - boxes : lane) * s.ahead_rows, y, z);
+    if (z < s.num_pages) tma_prefetch_5d(v ? &s.tm_v_ahead : &s.tm_k_ahead, 0, y, 0, it.hkv, z);
+  }
+  // Every copy of this warp lands before the CTA ends.
+  __device__ __forceinline__ void drain() {
+    for (int s = 0; s < slots; ++s)
+      if (armed >> s & 1u) wait_drain_inl(smem_u32(&full[s]), parity >> s & 1u, p.timeout_ns, p.err);
   }
 };
+
+// V of LAYOUT_SHARED in a stage, whose boxes of R = v_rows keys hold all chunks: the operand of 16 keys
+// (MN-major) has its chunks R rows apart and its second 8 keys 8 rows on, or in the next box where R = 8.
+__device__ __forceinline__ uint64_t shared_v_desc(uint32_t stage, int v_rows, int chunks) {
+  return sdesc_sw128(stage, (uint32_t)v_rows * 128u, v_rows == 8 ? (uint32_t)chunks * 1024u : 1024u);
+}
+// Offset (in 16 bytes) of key `key` of a stage in that operand's address.
+__device__ __forceinline__ uint32_t shared_v_at(int key, int v_rows, int chunks) {
+  return (uint32_t)(key / v_rows * (chunks - 1) * v_rows + key) * 8u;
+}
 
 // Maximum of n scores (n a multiple of 16): eight independent chains of
 // three-input maxima, then a small tree.

@@ -620,7 +620,10 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       if (P.lse)
         for (int h = tid; h < P.Hq; h += THREADS) P.lse[(int64_t)b * P.Hq + h] = -INFINITY;
     }
-    if (c >= runs) return;   // (an exit counts for the dependent launch too)
+    if (c >= runs) {         // (an exit counts for the dependent launch too)
+      if (KIND == DECODE_OWN) dependency_wait();
+      return;
+    }
     // Columns behind D meet zeros of Q and must be finite (boxes bring zeros).
     if (!P.boxed && P.D * cache_bytes(KIND) % 32 != 0) {
       char* ring = smem + decode_score_bytes(KIND, NT, T) + (E4M3 ? decode_query_bytes(NT, P.D) : 0);
@@ -661,6 +664,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       produce_boxes<KIND, PAGED>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
     else
       produce_pieces<KIND>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
+    if (KIND == DECODE_OWN) dependency_wait();
     return;
   }
 
@@ -1127,6 +1131,9 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     i0 = i1;
     cur = next_s[turn];
   }
+  // Own keys need nothing of the launch before this one (the shared keys'), beside which they run, but
+  // what follows waits for this kernel alone: it ends behind that one.
+  if (KIND == DECODE_OWN) dependency_wait();
 }
 
 // Joins the partial sums of the pairs cut between CTAs.  A pair over n CTAs is
@@ -1240,6 +1247,24 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) join_kernel(const __grid_c
   }
 }
 
+// A launch that may begin when the one before it in the stream says so (dependents_launch) or ends.
+template <class... Params, class... Args>
+ffpa_status launch_dependent(void (*fn)(Params...), int grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess) return FFPA_OK;
+  cudaGetLastError();
+  return FFPA_ERR_CUDA;
+}
+
 // Workspace: partial outputs, their maxima and sums, the cut pairs.
 struct DecodeSpace {
   size_t part, ml, cuts, total;
@@ -1259,26 +1284,19 @@ ffpa_status launch_decode_as(const DecodeParams& P, const DecodePlan& pl, int gr
   const auto fn = P.page_tiles ? &decode_kernel<KIND, F16, NT, T, true> : &decode_kernel<KIND, F16, NT, T, false>;
   const ffpa_status st = set_smem_attr_once(reinterpret_cast<const void*>(fn), dev, (int)pl.smem);
   if (st != FFPA_OK) return st;
-  fn<<<grid, DEC_THREADS, pl.smem, stream>>>(P);
-  if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
+  if (KIND == DECODE_OWN && P.shared_pages > 0) {
+    // Beside the shared keys' launch before it, as SMs come free, and done after it (see the kernel's end).
+    const ffpa_status own = launch_dependent(fn, grid, DEC_THREADS, pl.smem, stream, P);
+    if (own != FFPA_OK) return own;
+  } else {
+    fn<<<grid, DEC_THREADS, pl.smem, stream>>>(P);
+    if (cudaGetLastError() != cudaSuccess) return FFPA_ERR_CUDA;
+  }
   const int heads = 8 * NT;
   int log_rows = 0;
   while ((1 << log_rows) < (P.group < heads ? P.group : heads)) ++log_rows;
   // A dependent launch: its blocks are set up while the first kernel runs out.
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * grid);
-  cfg.blockDim = dim3(JOIN_WARPS * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<KIND, F16>, P, heads, log_rows) != cudaSuccess) {
-    cudaGetLastError();
-    return FFPA_ERR_CUDA;
-  }
-  return FFPA_OK;
+  return launch_dependent(join_kernel<KIND, F16>, 2 * grid, JOIN_WARPS * 32, 0, stream, P, heads, log_rows);
 }
 
 template <int KIND, bool F16, int T>

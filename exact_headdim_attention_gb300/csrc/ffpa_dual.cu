@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  if (SHARED) dependents_launch();   // own keys run beside this kernel, where SMs are free
   const int T = it.ntiles;
   const unsigned long long tmo = p.timeout_ns;
   int* const err = p.err;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
     // Each role branch starts with its warpgroup's register change, so that
     // the compiler allocates the branch under that budget.
     regs_lower<DUAL_REGS_LOW>();
-    if (warp == DUAL_PRODUCER_WARP) {
+    if (warp == DUAL_PRODUCER_WARP || (SHARED && warp != DUAL_MMA_WARP)) {
       // ------------------------------------------------------------ producer
       // Q_A and Q_B once, then the ring in the MMA thread's order: K_0; per
       // key tile j: K_{j+1}, V_j.
@@ -148,26 +149,31 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
             prefetch_tmap(&p.tm_k);
             prefetch_tmap(&p.tm_v);
           }
-          SharedCopy copy{p, it, ring_u32, TILE_BYTES, bar_full, bar_empty, NS, lane, 0, 0, 0u, inject != 0, &abort_flag};
+          const int me = warp == DUAL_PRODUCER_WARP ? 0 : warp - DUAL_MMA_WARP;   // of three
+          SharedCopy copy{p, it, ring_u32, TILE_BYTES, bar_full, bar_empty, NS, lane, 3, me, inject != 0, &abort_flag};
           const uint32_t qb = smem_u32(&bar_q);
-          if (lane == 0) mbar_arrive_expect_tx(qb, 2 * copy.q_bytes(NCH));
-          __syncwarp();
-          copy.queries(q_u32, qb, 0, NCH, it.q0);
-          copy.queries(q_u32 + TILE_BYTES, qb, 0, NCH, it.q0 + p.sh.tile_rows);
-          auto load = [&](const CUtensorMap* m, int j) -> bool {
+          if (me == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(qb, 2 * copy.q_bytes(NCH));
+            __syncwarp();
+            copy.queries(q_u32, qb, 0, NCH, it.q0);
+            copy.queries(q_u32 + TILE_BYTES, qb, 0, NCH, it.q0 + p.sh.tile_rows);
+          }
+          auto load = [&](bool v, int j) -> bool {
+            if (me == 0 && !v) copy.ahead(j + p.sh.ahead);
             uint32_t fb = 0;
             const uint32_t dst = copy.acquire(TILE_BYTES, fb);
             if (dst == ~0u) return false;
-            if (dst) copy.rows(m, dst, fb, (it.tile0 + j) * BN, BN, 0, NCH);
+            if (dst && v) copy.values(dst, fb, (it.tile0 + j) * BN, BN, 0, NCH);
+            if (dst && !v) copy.keys(dst, fb, (it.tile0 + j) * BN, 0, NCH);
             return true;
           };
-          bool ok = load(&p.tm_k, 0);
+          bool ok = load(false, 0);
           for (int j = 0; j < T && ok; ++j) {
-            if (j + 1 < T && !(ok = load(&p.tm_k, j + 1))) break;
-            ok = load(&p.tm_v, j);
+            if (j + 1 < T && !(ok = load(false, j + 1))) break;
+            ok = load(true, j);
           }
           wait_drain_inl(qb, 0, tmo, err);
-          copy.drain(inject != 0);
+          copy.drain();
         }
       } else if (lane == 0 && T > 0) {
         prefetch_tmap(&p.tm_q);
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
         const uint64_t ring_desc = sdesc_sw128(ring_u32, 16, 1024);
         const uint64_t q_desc = sdesc_sw128(q_u32, 16, 1024);
         const uint64_t p_desc = sdesc_sw128(p_u32, 16, 1024);
-        const uint64_t v_desc = sdesc_sw128(ring_u32, CHUNK_BYTES, 1024);
+        const uint64_t v_desc = SHARED ? shared_v_desc(ring_u32, p.sh.v_rows, NCH) : sdesc_sw128(ring_u32, CHUNK_BYTES, 1024);
         // S_g = Q_g K^T over D: 4 MMAs of 16 D-elements per 64-column chunk
         // (+32 bytes each, >>4 = 2), chunks 16 KB apart.
         auto qk = [&](int g, int sk) {
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
           for (int kk = 0; kk < BN / 16; ++kk) {
             const int key = 16 * kk;
             const uint64_t ad = ad0 + (((key >> 6) * CHUNK_BYTES) >> 4) + 2 * ((key & 63) >> 4);
-            umma_ss(o_col, ad, vd + 128 * kk, idesc_pv, (acc || kk > 0) ? 1u : 0u);
+            umma_ss(o_col, ad, vd + (SHARED ? shared_v_at(key, p.sh.v_rows, NCH) : 128 * kk), idesc_pv, (acc || kk > 0) ? 1u : 0u);
           }
           umma_commit(smem_u32(&bar_pv_done[g]));
         };

@@ -171,9 +171,4 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Dependent launch: let the next kernel of the stream start its blocks, and
-// wait (in that kernel) until this one's memory is visible.
-__device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 }  // namespace ffpa

@@ -83,7 +83,8 @@ struct MergeParams {
   int B, Hq, D, group, tile_rows, tiles, splits;   // query tiles of a part (with the empty one of a last pair)
 };
 
-constexpr int MERGE_WARPS = 8;
+constexpr int MERGE_WARPS = 4;
+constexpr int MERGE_FLIGHT = 8;   // parts on their way
 constexpr float LOG2E = 1.4426950408889634f;
 
 // A warp joins 128 columns of a row: the row's parts in order, then its own keys.
@@ -92,6 +93,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const __grid_co
   const int lane = threadIdx.x % 32;
   const int cols = (P.D + 127) / 128;
   const long long task = (long long)blockIdx.x * MERGE_WARPS + threadIdx.x / 32;
+  dependency_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && *P.shared_len < 0) report_invalid(P.err);
   const long long row = task / cols;               // b Hq + hq
   if (row >= (long long)P.B * P.Hq) return;
@@ -101,32 +103,40 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const __grid_co
   const int tile = r / P.tile_rows;
   // Part s of the row: ((hk splits + s) tiles + tile) 128 + its row of the tile.
   const int64_t first = ((int64_t)hk * P.splits * P.tiles + tile) * BM + (r - tile * P.tile_rows), step = (int64_t)P.tiles * BM;
-  const float own2 = P.own_lse[row] * LOG2E;
-  float top = own2;
-  for (int s = lane; s < P.splits; s += 32) {
-    const float2 ml = P.part_ml[first + s * step];
-    if (ml.y != 0.0f) top = fmaxf(top, ml.x);
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  const float base = top == -INFINITY ? 0.0f : top;
   const bool mine = col < P.D;
-  float4 a = make_float4(0, 0, 0, 0);
-  float l = 0.0f;
-  for (int s0 = 0; s0 < P.splits; s0 += 4) {
-    float2 ml[4];
-    float4 x[4];
+  const int at = min(col, P.D - 4);
+  const float* from = P.part + first * P.D + at;
+  const float own2 = P.own_lse[row] * LOG2E;
+  const float4 own = *reinterpret_cast<const float4*>(P.own + row * P.D + at);
+  // Parts four at a time, in order, with the maximum so far; a part without keys for this row has no
+  // sums (and its memory may hold anything).
+  float top = own2, l = own2 == -INFINITY ? 0.0f : 1.0f;
+  float4 a = own2 == -INFINITY ? make_float4(0, 0, 0, 0) : own;
+  for (int s0 = 0; s0 < P.splits; s0 += MERGE_FLIGHT) {
+    float2 ml[MERGE_FLIGHT];
+    float4 x[MERGE_FLIGHT];
+    float now = top;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = s0 + i < P.splits;
-      ml[i] = in ? P.part_ml[first + (s0 + i) * step] : make_float2(0.0f, 0.0f);
-      // (a part without keys for this row has no sums)
-      x[i] = in && mine && ml[i].y != 0.0f ? *reinterpret_cast<const float4*>(P.part + (first + (s0 + i) * step) * P.D + col)
-                                           : make_float4(0, 0, 0, 0);
+    for (int i = 0; i < MERGE_FLIGHT; ++i) {
+      const int s = min(s0 + i, P.splits - 1);
+      ml[i] = P.part_ml[first + s * step];
+      x[i] = *reinterpret_cast<const float4*>(from + s * step * P.D);
+      if (s0 + i >= P.splits) ml[i].y = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float f = ml[i].y != 0.0f ? ex2_approx(ml[i].x - base) : 0.0f;
+    for (int i = 0; i < MERGE_FLIGHT; ++i)
+      if (ml[i].y != 0.0f) now = fmaxf(now, ml[i].x);
+    const float base = now == -INFINITY ? 0.0f : now, f0 = ex2_approx(top - base);
+    top = now;
+    l *= f0;
+    a.x *= f0;
+    a.y *= f0;
+    a.z *= f0;
+    a.w *= f0;
+#pragma unroll
+    for (int i = 0; i < MERGE_FLIGHT; ++i) {
+      if (ml[i].y == 0.0f) continue;
+      const float f = ex2_approx(ml[i].x - base);
       l += f * ml[i].y;
       a.x += f * x[i].x;
       a.y += f * x[i].y;
@@ -134,20 +144,11 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const __grid_co
       a.w += f * x[i].w;
     }
   }
-  if (own2 != -INFINITY) {
-    const float f = ex2_approx(own2 - base);
-    const float4 x = mine ? *reinterpret_cast<const float4*>(P.own + row * P.D + col) : make_float4(0, 0, 0, 0);
-    l += f;
-    a.x += f * x.x;
-    a.y += f * x.y;
-    a.z += f * x.z;
-    a.w += f * x.w;
-  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   if (mine)
     *reinterpret_cast<uint2*>(P.o + b * P.o_sb + hq * P.o_sh + col * 2) =
         make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-  if (P.lse && col == 0) P.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+  if (P.lse && col == 0) P.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -218,14 +219,22 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
     SharedKeys& S = P.sh;
     S.box_rows = BM;
     while (page_size % S.box_rows != 0) S.box_rows /= 2;
-    if (S.box_rows > P.vk) S.box_rows = P.vk;        // a stage of V holds whole boxes
-    for (int i = 0; i < 2; ++i) {
-      const int64_t* of = i ? v_str : k_str;
+    S.v_rows = S.box_rows < P.vk ? S.box_rows : P.vk;   // a stage of V holds whole boxes
+    S.ahead_rows = S.box_rows;
+    while (S.ahead_rows > 8 && S.ahead_rows * D * 2 > 32768) S.ahead_rows /= 2;
+    // Key tiles asked for ahead, beyond those that are on their way to the ring: a round of a cluster's
+    // tiles, else 256 KB of keys and values.
+    S.ahead = pl.ctas > 1 ? pl.ctas : 256 * 1024 / (BN * D * 4);
+    for (int i = 0; i < 4; ++i) {
+      // K a chunk a box, V the chunks of a stage, and both whole rows for what is asked for ahead.
+      const int64_t* of = i % 2 ? v_str : k_str;
       const uint64_t one = (uint64_t)D * 2, head = Hkv > 1 ? (uint64_t)of[2] * 2 : one;
       const uint64_t dims[5] = {DK, (uint64_t)page_size, (uint64_t)(D / DK), (uint64_t)Hkv, (uint64_t)num_pages};
       const uint64_t str[4] = {(uint64_t)of[1] * 2, DK * 2, head, num_pages > 1 ? (uint64_t)of[0] * 2 : one};
-      const uint32_t box[5] = {DK, (uint32_t)S.box_rows, 1, 1, 1};
-      if ((st = encode_rows(i ? &P.tm_v : &P.tm_k, dt, 5, i ? v_cache : k_cache, dims, str, box)) != FFPA_OK) return st;
+      const uint32_t box[5] = {DK, (uint32_t)(i == 0 ? S.box_rows : i == 1 ? S.v_rows : S.ahead_rows),
+                               (uint32_t)(i == 0 ? 1 : i == 1 ? P.vchunks : D / DK), 1, 1};
+      CUtensorMap* map = i == 0 ? &P.tm_k : i == 1 ? &P.tm_v : i == 2 ? &S.tm_k_ahead : &S.tm_v_ahead;
+      if ((st = encode_rows(map, dt, 5, i % 2 ? v_cache : k_cache, dims, str, box)) != FFPA_OK) return st;
     }
     S.pages = shared_pages;
     S.len = shared_len;
@@ -297,8 +306,7 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
   M.splits = pl.splits;
   const long long tasks = (long long)B * Hq * ((D + 127) / 128);
   const int grid = (int)((tasks + MERGE_WARPS - 1) / MERGE_WARPS);
-  (dt == FFPA_FP16 ? merge_kernel<true> : merge_kernel<false>)<<<grid, MERGE_WARPS * 32, 0, s>>>(M);
-  return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
+  return launch_dependent(dt == FFPA_FP16 ? merge_kernel<true> : merge_kernel<false>, grid, MERGE_WARPS * 32, 0, s, M);
 }
 
 }  // extern "C"

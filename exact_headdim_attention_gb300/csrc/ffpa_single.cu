@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  if (SHARED) dependents_launch();   // own keys run beside this kernel, where SMs are free
   const int T = it.ntiles;
   const unsigned long long tmo = p.timeout_ns;
   int* const err = p.err;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
           prefetch_tmap(k_role ? &p.tm_k : &p.tm_v);
         }
         SharedCopy copy{p, it, k_role ? ring_u32 : vring_u32, k_role ? SLOT_BYTES : vslot, k_role ? bar_full : bar_vfull,
-                        k_role ? bar_empty : bar_vempty, k_role ? NS : NSV, lane, 0, 0, 0u, k_role && inject != 0, &abort_flag};
+                        k_role ? bar_empty : bar_vempty, k_role ? NS : NSV, lane, 1, 0, k_role && inject != 0, &abort_flag};
         bool ok = true;
         const uint32_t qb = smem_u32(&bar_q);
         if (k_role && q_res) {
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
         for (int j = 0; j < T && ok; ++j) {
           const int key0 = (it.tile0 + j) * BN;
           uint32_t fb = 0, dst;
+          if (k_role) copy.ahead(j + p.sh.ahead);
           for (int pr = 0; k_role && pr < qpairs && ok; ++pr) {
             if (!q_res) {
               dst = copy.acquire(copy.q_bytes(kchunks), fb);
@@ -107,16 +109,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
             }
             dst = copy.acquire((uint32_t)kchunks * CHUNK_BYTES, fb);
             if (!(ok = dst != ~0u)) break;
-            if (dst) copy.rows(&p.tm_k, dst, fb, key0, BN, 2 * pr, kchunks);
+            if (dst) copy.keys(dst, fb, key0, 2 * pr, kchunks);
           }
           for (int h = 0; !k_role && h < BN / vk && ok; ++h) {
             dst = copy.acquire(vslot, fb);
             if (!(ok = dst != ~0u)) break;
-            copy.rows(&p.tm_v, dst, fb, key0 + h * vk, vk, it.col_lo / DK, p.vchunks);
+            copy.values(dst, fb, key0 + h * vk, vk, it.col_lo / DK, p.vchunks);
           }
         }
         if (k_role && q_res) wait_drain(qb, 0, tmo, err);
-        copy.drain(k_role && inject != 0);
+        copy.drain();
       }
     } else if (lane == 0 && T > 0) {
       const bool k_role = warp == PRODUCER_WARP;
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
         }
       } else {
         const uint32_t idesc_pv = idesc_f16(!fp16, BM, it.dv, false, true);
-        const uint64_t v_desc = sdesc_sw128(vring_u32, vk * 128, 1024);
+        const uint64_t v_desc = SHARED ? shared_v_desc(vring_u32, p.sh.v_rows, p.vchunks) : sdesc_sw128(vring_u32, vk * 128, 1024);
         for (int j = 0; j < T && ok; ++j) {
           const int b = j & 1;
           if (!(ok = wait_on(smem_u32(&bar_p_full[b]), (j >> 1) & 1))) break;
@@ -304,6 +306,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
             if (s < 0) { ok = false; break; }
             const uint64_t vd = v_desc + ((s * vslot) >> 4);
             const uint32_t pc = p_col + ((h * vk) >> 1);
+            if (SHARED) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                if (16 * kk < vk)
+                  umma_ts(tmem, pc + 8 * kk, vd + shared_v_at(16 * kk, p.sh.v_rows, p.vchunks), idesc_pv,
+                          (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
+              release(s);
+              continue;
+            }
             // 16 keys per MMA: +8 TMEM columns of P, +2048 bytes (>>4 = 128) of V.
             umma_ts(tmem, pc, vd, idesc_pv, (j > 0 || h > 0) ? 1u : 0u);
             umma_ts(tmem, pc + 8, vd + 128, idesc_pv, 1u);

@@ -32,7 +32,7 @@ namespace ffpa {
 // instruction queue is shallow, and loop overhead between MMAs leaves it
 // idle (measured: a runtime-count loop of 8 MMAs runs at about half rate).
 template <int LAYOUT, int NCH, bool UMASK>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(split_threads(LAYOUT), 1)
     ffpa_fwd_split_kernel(const __grid_constant__ Params p) {
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
@@ -102,13 +102,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
   cluster_sync_all();      // the peer's barriers exist before any remote operation
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  if (SHARED) dependents_launch();   // own keys run beside this kernel, where SMs are free
   const int T = it.ntiles;
   const int R = (T + 1) >> 1;                  // rounds of two key tiles
   const int own0 = (int)rank, peer0 = (int)peer;   // tile of round i: 2 i + own0 / 2 i + peer0
   const unsigned long long tmo = p.timeout_ns;
   int* const err = p.err;
 
-  if (warp == PRODUCER_WARP) {
+  if (warp == PRODUCER_WARP || (SHARED && warp > MMA_WARP)) {
     // ------------------------------------------------------------ producer
     // One ring, filled in the MMA thread's order: K of the first own tile,
     // then per round i: K of the own tile of round i+1, V (this CTA's
@@ -120,18 +121,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
           prefetch_tmap(&p.tm_k);
           prefetch_tmap(&p.tm_v);
         }
-        SharedCopy copy{p, it, ring_u32, SLOT_BYTES, bar_full, bar_empty, NS, lane, 0, 0, 0u, inject != 0 && rank == 0, &abort_flag};
+        const int me = warp == PRODUCER_WARP ? 0 : warp - MMA_WARP;   // of three
+        SharedCopy copy{p, it, ring_u32, SLOT_BYTES, bar_full, bar_empty, NS, lane, 3, me, inject != 0 && rank == 0, &abort_flag};
         const uint32_t qb = smem_u32(&bar_q);
-        if (lane == 0) mbar_arrive_expect_tx(qb, copy.q_bytes(nchunks));
-        __syncwarp();
-        copy.queries(pown_u32, qb, 0, qt, it.q0);
-        copy.queries(qs_u32, qb, qt, nchunks - qt, it.q0);
+        if (me == 0) {
+          if (lane == 0) mbar_arrive_expect_tx(qb, copy.q_bytes(nchunks));
+          __syncwarp();
+          copy.queries(pown_u32, qb, 0, qt, it.q0);
+          copy.queries(qs_u32, qb, qt, nchunks - qt, it.q0);
+        }
         auto load_k = [&](int j) -> bool {
+          if (me == 0) copy.ahead(j + p.sh.ahead);
           for (int c = 0; c < nchunks; c += 2) {
             uint32_t fb = 0;
             const uint32_t dst = copy.acquire(2 * CHUNK_BYTES, fb);
             if (dst == ~0u) return false;
-            if (dst) copy.rows(&p.tm_k, dst, fb, (it.tile0 + j) * BN, BN, c, 2);
+            if (dst) copy.keys(dst, fb, (it.tile0 + j) * BN, c, 2);
           }
           return true;
         };
@@ -140,7 +145,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
             uint32_t fb = 0;
             const uint32_t dst = copy.acquire(vslot, fb);
             if (dst == ~0u) return false;
-            copy.rows(&p.tm_v, dst, fb, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH);
+            if (dst) copy.values(dst, fb, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH);
           }
           return true;
         };
@@ -151,7 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
           if (2 * i + peer0 < T && !(ok = load_v(2 * i + peer0))) break;
         }
         wait_drain(qb, 0, tmo, err);
-        copy.drain(inject != 0 && rank == 0);
+        copy.drain();
       }
     } else if (lane == 0 && T > 0) {
       prefetch_tmap(&p.tm_q);
@@ -256,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
       const uint64_t qs_desc = sdesc_sw128(qs_u32, 16, 1024);
       const uint64_t pown_desc = sdesc_sw128(pown_u32, 16, 1024);
       const uint64_t ppeer_desc = sdesc_sw128(ppeer_u32, 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(ring_u32, vk * 128, 1024);
+      const uint64_t v_desc = SHARED ? shared_v_desc(ring_u32, p.sh.v_rows, VCH) : sdesc_sw128(ring_u32, vk * 128, 1024);
       const uint32_t s_col = tmem + S_COL;
       const uint32_t q_col = tmem + Q_TMEM_COL;
       ok = wait_on(smem_u32(&bar_q), 0) && wait_on(smem_u32(&bar_qt), 0);
@@ -304,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT_THREADS, 1)
             // per 16 keys), V (MN-major, +2048 bytes per 16 keys).
             const int key = h * vk + 16 * kk;
             const uint64_t ad = a_desc + (((key >> 6) * CHUNK_BYTES) >> 4) + 2 * ((key & 63) >> 4);
-            umma_ss(tmem, ad, vd + 128 * kk, idesc_pv, o_acc ? 1u : 0u);
+            umma_ss(tmem, ad, vd + (SHARED ? shared_v_at(16 * kk, p.sh.v_rows, VCH) : 128 * kk), idesc_pv, o_acc ? 1u : 0u);
             o_acc = true;
           }
           umma_commit(smem_u32(&bar_empty[s]));
@@ -597,7 +602,7 @@ static ffpa_status launch_split_t(const Params& P, int items, size_t smem, cudaS
   const ffpa_status st =
       set_smem_attr_once(reinterpret_cast<const void*>(kern), P.device, static_cast<int>(SMEM_LIMIT - SPLIT_STATIC_RESERVE));
   if (st != FFPA_OK) return st;
-  kern<<<2 * items, SPLIT_THREADS, smem, stream>>>(P);
+  kern<<<2 * items, split_threads(LAYOUT), smem, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
