@@ -755,21 +755,32 @@ struct SharedCopy {
       atomicCAS(p.err, 0, static_cast<int>(FFPA_ERR_INVALID));
     }
   }
-  // K: `chunks` chunks from chunk0 of the 128 keys from key0 on, chunk after chunk (a box each and page part).
-  __device__ __forceinline__ void keys(uint32_t dst, uint32_t bar, int key0, int chunk0, int chunks) {
+  // Whether the next stage is this warp's (what a stage copies is looked up before its slot is waited for).
+  __device__ __forceinline__ bool mine() const { return slot % copiers == me; }
+  // A stage of K: `chunks` chunks from chunk0 of the 128 keys from key0 on, chunk after chunk (a box each
+  // and page part).  false on abort.
+  __device__ __forceinline__ bool keys(uint32_t bytes, int key0, int chunk0, int chunks) {
     const int boxes = BN / p.sh.box_rows, c = lane / boxes, i = lane - c * boxes;
-    if (c >= chunks) return;
-    int y, z;
-    place(key0 + i * p.sh.box_rows, y, z);
-    tma_load_5d(dst + (uint32_t)(c * BN + i * p.sh.box_rows) * 128u, &p.tm_k, bar, 0, y, chunk0 + c, it.hkv, z);
+    int y = 0, z = 0;
+    if (mine() && c < chunks) place(key0 + i * p.sh.box_rows, y, z);
+    uint32_t fb = 0;
+    const uint32_t dst = acquire(bytes, fb);
+    if (dst == ~0u) return false;
+    if (dst != 0u && c < chunks)
+      tma_load_5d(dst + (uint32_t)(c * BN + i * p.sh.box_rows) * 128u, &p.tm_k, fb, 0, y, chunk0 + c, it.hkv, z);
+    return true;
   }
-  // V: `rows` keys from key0 on, chunks chunk0 .. of the boxes: v_rows keys of all chunks, box after box.
-  __device__ __forceinline__ void values(uint32_t dst, uint32_t bar, int key0, int rows, int chunk0, int chunks) {
+  // A stage of V: `rows` keys from key0 on, chunks chunk0 .. of the boxes: v_rows keys of all chunks, box after box.
+  __device__ __forceinline__ bool values(uint32_t bytes, int key0, int rows, int chunk0, int chunks) {
     const int vr = p.sh.v_rows;
-    if (lane >= rows / vr) return;
-    int y, z;
-    place(key0 + lane * vr, y, z);
-    tma_load_5d(dst + (uint32_t)(lane * chunks * vr) * 128u, &p.tm_v, bar, 0, y, chunk0, it.hkv, z);
+    int y = 0, z = 0;
+    if (mine() && lane < rows / vr) place(key0 + lane * vr, y, z);
+    uint32_t fb = 0;
+    const uint32_t dst = acquire(bytes, fb);
+    if (dst == ~0u) return false;
+    if (dst != 0u && lane < rows / vr)
+      tma_load_5d(dst + (uint32_t)(lane * chunks * vr) * 128u, &p.tm_v, fb, 0, y, chunk0, it.hkv, z);
+    return true;
   }
   // Keys and values of tile j of the item on their way to L2, from the query tile whose turn it is.
   __device__ __forceinline__ void ahead(int j) {

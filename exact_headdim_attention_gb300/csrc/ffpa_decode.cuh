@@ -518,6 +518,13 @@ __device__ __forceinline__ void write_columns8(char* out, int64_t o_sh, int head
         make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
 }
 
+// Own keys need nothing of the launch before (the shared keys'), beside which they run, but what
+// follows waits for this kernel alone: its last block, and with it the kernel, ends behind that one.
+// (With every block waiting, the SMs that the shared keys leave free took one round of blocks.)
+__device__ __forceinline__ void end_behind_launch_before() {
+  if (blockIdx.x == gridDim.x - 1) dependency_wait();
+}
+
 template <int KIND, bool F16, int NT, int T, bool PAGED>
 __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(const __grid_constant__ DecodeParams P) {
   constexpr bool E4M3 = KIND == DECODE_E4M3;
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         for (int h = tid; h < P.Hq; h += THREADS) P.lse[(int64_t)b * P.Hq + h] = -INFINITY;
     }
     if (c >= runs) {         // (an exit counts for the dependent launch too)
-      if (KIND == DECODE_OWN) dependency_wait();
+      if (KIND == DECODE_OWN) end_behind_launch_before();
       return;
     }
     // Columns behind D meet zeros of Q and must be finite (boxes bring zeros).
@@ -664,7 +671,6 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       produce_boxes<KIND, PAGED>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
     else
       produce_pieces<KIND>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
-    if (KIND == DECODE_OWN) dependency_wait();
     return;
   }
 
@@ -1131,9 +1137,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     i0 = i1;
     cur = next_s[turn];
   }
-  // Own keys need nothing of the launch before this one (the shared keys'), beside which they run, but
-  // what follows waits for this kernel alone: it ends behind that one.
-  if (KIND == DECODE_OWN) dependency_wait();
+  if (KIND == DECODE_OWN) end_behind_launch_before();
 }
 
 // Joins the partial sums of the pairs cut between CTAs.  A pair over n CTAs is

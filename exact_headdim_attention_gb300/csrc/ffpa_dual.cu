@@ -160,12 +160,7 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
           }
           auto load = [&](bool v, int j) -> bool {
             if (me == 0 && !v) copy.ahead(j + p.sh.ahead);
-            uint32_t fb = 0;
-            const uint32_t dst = copy.acquire(TILE_BYTES, fb);
-            if (dst == ~0u) return false;
-            if (dst && v) copy.values(dst, fb, (it.tile0 + j) * BN, BN, 0, NCH);
-            if (dst && !v) copy.keys(dst, fb, (it.tile0 + j) * BN, 0, NCH);
-            return true;
+            return v ? copy.values(TILE_BYTES, (it.tile0 + j) * BN, BN, 0, NCH) : copy.keys(TILE_BYTES, (it.tile0 + j) * BN, 0, NCH);
           };
           bool ok = load(false, 0);
           for (int j = 0; j < T && ok; ++j) {

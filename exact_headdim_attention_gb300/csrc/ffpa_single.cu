@@ -107,15 +107,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
               if (!(ok = dst != ~0u)) break;
               if (dst) copy.queries(dst, fb, 2 * pr, kchunks, it.q0);
             }
-            dst = copy.acquire((uint32_t)kchunks * CHUNK_BYTES, fb);
-            if (!(ok = dst != ~0u)) break;
-            if (dst) copy.keys(dst, fb, key0, 2 * pr, kchunks);
+            ok = copy.keys((uint32_t)kchunks * CHUNK_BYTES, key0, 2 * pr, kchunks);
           }
-          for (int h = 0; !k_role && h < BN / vk && ok; ++h) {
-            dst = copy.acquire(vslot, fb);
-            if (!(ok = dst != ~0u)) break;
-            copy.values(dst, fb, key0 + h * vk, vk, it.col_lo / DK, p.vchunks);
-          }
+          for (int h = 0; !k_role && h < BN / vk && ok; ++h) ok = copy.values(vslot, key0 + h * vk, vk, it.col_lo / DK, p.vchunks);
         }
         if (k_role && q_res) wait_drain(qb, 0, tmo, err);
         copy.drain();

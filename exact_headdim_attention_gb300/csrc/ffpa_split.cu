@@ -132,21 +132,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(split_threads(LAYOUT
         }
         auto load_k = [&](int j) -> bool {
           if (me == 0) copy.ahead(j + p.sh.ahead);
-          for (int c = 0; c < nchunks; c += 2) {
-            uint32_t fb = 0;
-            const uint32_t dst = copy.acquire(2 * CHUNK_BYTES, fb);
-            if (dst == ~0u) return false;
-            if (dst) copy.keys(dst, fb, (it.tile0 + j) * BN, c, 2);
-          }
+          for (int c = 0; c < nchunks; c += 2)
+            if (!copy.keys(2 * CHUNK_BYTES, (it.tile0 + j) * BN, c, 2)) return false;
           return true;
         };
         auto load_v = [&](int j) -> bool {
-          for (int h = 0; h < BN / vk; ++h) {
-            uint32_t fb = 0;
-            const uint32_t dst = copy.acquire(vslot, fb);
-            if (dst == ~0u) return false;
-            if (dst) copy.values(dst, fb, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH);
-          }
+          for (int h = 0; h < BN / vk; ++h)
+            if (!copy.values(vslot, (it.tile0 + j) * BN + h * vk, vk, it.col_lo / DK, VCH)) return false;
           return true;
         };
         bool ok = own0 >= T || load_k(own0);
