@@ -161,7 +161,6 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(split_threads(LAYOUT
           if (QRES) copy.queries(qs_u32, qb, qt, NCH - qt, it.q0);
         }
         auto load_qk = [&](int j) -> bool {
-          if (me == 0) copy.ahead(j + p.sh.ahead);
           for (int c = 0; c < NCH; c += 2) {
             uint32_t fb = 0;
             if (!QRES && c >= qt) {

@@ -259,9 +259,6 @@ struct SharedKeys {
   int n_pages, num_pages, page_size;
   int box_rows;              // keys of a box: a power of two of 8 .. 128 that divides page_size
   int v_rows;                // the same of V, whose boxes hold all chunks of a stage
-  int ahead;                 // key tiles (of the item) that are asked for ahead, into L2; 0: none
-  int ahead_rows;            // keys of a box that does so, all chunks of a row
-  CUtensorMap tm_k_ahead, tm_v_ahead;
   int tile_rows;             // rows of a query tile: whole requests, at most 128
   int splits;                // parts of the keys
   float lift;                // log2 of the factor on P (fp16: small weights stay in its range)
@@ -711,6 +708,8 @@ struct SharedCopy {
   bool drop;                         // test hook: the first stage never comes
   volatile int* abort_flag;
   int slot = 0;
+  // (the query tiles of a part read the same keys, but at about the same time)
+  uint64_t once = once_policy();
   uint32_t lap = 0, armed = 0, parity = 0;   // (bits: the slots that this warp armed, and their phases)
 
   // The next stage, armed for `bytes`: its address, 0 where it is not this warp's, ~0 on abort.
@@ -767,7 +766,7 @@ struct SharedCopy {
     const uint32_t dst = acquire(bytes, fb);
     if (dst == ~0u) return false;
     if (dst != 0u && c < chunks)
-      tma_load_5d(dst + (uint32_t)(c * BN + i * p.sh.box_rows) * 128u, &p.tm_k, fb, 0, y, chunk0 + c, it.hkv, z);
+      tma_load_5d(dst + (uint32_t)(c * BN + i * p.sh.box_rows) * 128u, &p.tm_k, fb, 0, y, chunk0 + c, it.hkv, z, once);
     return true;
   }
   // A stage of V: `rows` keys from key0 on, chunks chunk0 .. of the boxes: v_rows keys of all chunks, box after box.
@@ -779,18 +778,8 @@ struct SharedCopy {
     const uint32_t dst = acquire(bytes, fb);
     if (dst == ~0u) return false;
     if (dst != 0u && lane < rows / vr)
-      tma_load_5d(dst + (uint32_t)(lane * chunks * vr) * 128u, &p.tm_v, fb, 0, y, chunk0, it.hkv, z);
+      tma_load_5d(dst + (uint32_t)(lane * chunks * vr) * 128u, &p.tm_v, fb, 0, y, chunk0, it.hkv, z, once);
     return true;
-  }
-  // Keys and values of tile j of the item on their way to L2, from the query tile whose turn it is.
-  __device__ __forceinline__ void ahead(int j) {
-    const SharedKeys& s = p.sh;
-    const int boxes = BN / s.ahead_rows;
-    if (s.ahead == 0 || j >= it.ntiles || lane >= 2 * boxes || (it.tile0 + j) % p.n_qt != it.qt) return;
-    const bool v = lane >= boxes;
-    int y, z;
-    place((it.tile0 + j) * BN + (v ? lane - boxes : lane) * s.ahead_rows, y, z);
-    if (z < s.num_pages) tma_prefetch_5d(v ? &s.tm_v_ahead : &s.tm_k_ahead, 0, y, 0, it.hkv, z);
   }
   // Every copy of this warp lands before the CTA ends.
   __device__ __forceinline__ void drain() {

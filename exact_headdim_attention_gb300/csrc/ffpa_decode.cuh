@@ -278,6 +278,7 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
       page = P.table[p.b * P.table_str + skip + j];
     }
   };
+  const uint64_t once = once_policy();
   look_up(at);
   int slot = 0, i = 0;
   uint32_t lap = 0;
@@ -305,9 +306,9 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     if (mine) {
       const uint32_t dst = ring + slot * stage + to;
       if (P.box_chunks == 1)
-        tma_load_4d(dst, map, bar, chunk * (128 / cache_bytes(KIND)), y, head, z);
+        tma_load_4d(dst, map, bar, chunk * (128 / cache_bytes(KIND)), y, head, z, once);
       else
-        tma_load_5d(dst, map, bar, 0, y, 0, head, z);
+        tma_load_5d(dst, map, bar, 0, y, 0, head, z, once);
     }
     if (KIND == DECODE_E4M3) {
       // The rows' scales, four bytes each, from the pages that the boxes' lanes know.

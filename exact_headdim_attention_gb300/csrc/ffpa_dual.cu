@@ -159,7 +159,6 @@ __global__ void __launch_bounds__(DUAL_THREADS, 1) ffpa_fwd_dual_kernel(const __
             copy.queries(q_u32 + TILE_BYTES, qb, 0, NCH, it.q0 + p.sh.tile_rows);
           }
           auto load = [&](bool v, int j) -> bool {
-            if (me == 0 && !v) copy.ahead(j + p.sh.ahead);
             return v ? copy.values(TILE_BYTES, (it.tile0 + j) * BN, BN, 0, NCH) : copy.keys(TILE_BYTES, (it.tile0 + j) * BN, 0, NCH);
           };
           bool ok = load(false, 0);

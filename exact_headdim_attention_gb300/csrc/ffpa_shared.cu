@@ -220,21 +220,14 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
     S.box_rows = BM;
     while (page_size % S.box_rows != 0) S.box_rows /= 2;
     S.v_rows = S.box_rows < P.vk ? S.box_rows : P.vk;   // a stage of V holds whole boxes
-    S.ahead_rows = S.box_rows;
-    while (S.ahead_rows > 8 && S.ahead_rows * D * 2 > 32768) S.ahead_rows /= 2;
-    // Key tiles asked for ahead, beyond those that are on their way to the ring: a round of a cluster's
-    // tiles, else 256 KB of keys and values.
-    S.ahead = pl.ctas > 1 ? pl.ctas : 256 * 1024 / (BN * D * 4);
-    for (int i = 0; i < 4; ++i) {
-      // K a chunk a box, V the chunks of a stage, and both whole rows for what is asked for ahead.
-      const int64_t* of = i % 2 ? v_str : k_str;
+    for (int i = 0; i < 2; ++i) {
+      // K a chunk a box, V the chunks of a stage.
+      const int64_t* of = i ? v_str : k_str;
       const uint64_t one = (uint64_t)D * 2, head = Hkv > 1 ? (uint64_t)of[2] * 2 : one;
       const uint64_t dims[5] = {DK, (uint64_t)page_size, (uint64_t)(D / DK), (uint64_t)Hkv, (uint64_t)num_pages};
       const uint64_t str[4] = {(uint64_t)of[1] * 2, DK * 2, head, num_pages > 1 ? (uint64_t)of[0] * 2 : one};
-      const uint32_t box[5] = {DK, (uint32_t)(i == 0 ? S.box_rows : i == 1 ? S.v_rows : S.ahead_rows),
-                               (uint32_t)(i == 0 ? 1 : i == 1 ? P.vchunks : D / DK), 1, 1};
-      CUtensorMap* map = i == 0 ? &P.tm_k : i == 1 ? &P.tm_v : i == 2 ? &S.tm_k_ahead : &S.tm_v_ahead;
-      if ((st = encode_rows(map, dt, 5, i % 2 ? v_cache : k_cache, dims, str, box)) != FFPA_OK) return st;
+      const uint32_t box[5] = {DK, (uint32_t)(i ? S.v_rows : S.box_rows), (uint32_t)(i ? P.vchunks : 1), 1, 1};
+      if ((st = encode_rows(i ? &P.tm_v : &P.tm_k, dt, 5, i ? v_cache : k_cache, dims, str, box)) != FFPA_OK) return st;
     }
     S.pages = shared_pages;
     S.len = shared_len;

@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) ffpa_fwd_kernel(const __grid_cons
         for (int j = 0; j < T && ok; ++j) {
           const int key0 = (it.tile0 + j) * BN;
           uint32_t fb = 0, dst;
-          if (k_role) copy.ahead(j + p.sh.ahead);
           for (int pr = 0; k_role && pr < qpairs && ok; ++pr) {
             if (!q_res) {
               dst = copy.acquire(copy.q_bytes(kchunks), fb);

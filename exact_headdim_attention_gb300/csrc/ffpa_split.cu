@@ -131,7 +131,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(split_threads(LAYOUT
           copy.queries(qs_u32, qb, qt, nchunks - qt, it.q0);
         }
         auto load_k = [&](int j) -> bool {
-          if (me == 0) copy.ahead(j + p.sh.ahead);
           for (int c = 0; c < nchunks; c += 2)
             if (!copy.keys(2 * CHUNK_BYTES, (it.tile0 + j) * BN, c, 2)) return false;
           return true;
