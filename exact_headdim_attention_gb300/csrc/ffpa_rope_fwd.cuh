@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
       }
     }
     const int per = steps(first);
+    const bool codes = E4M3 && __any_sync(~0u, it.which > 0);   // (rows of a warp may be of both kinds)
 #pragma unroll 1
     for (int h = 0; h < per; ++h) {
       copy_wait<ROPE_DEPTH - 2>();
@@ -244,10 +245,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
       }
       issue();
       const float sum = row_sum<LPR>(sq.x + sq.y);
-      if (E4M3) {
+      if (E4M3 && codes) {
+        // Codes do not depend on the row's norm: it goes into the scale alone.
         float2 y[ITER][VEC];
         float top = 0.0f;
-        const float r = norm ? rsqrtf(sum * inv_d + P.eps) : 1.0f;
         if (on) {
 #pragma unroll
           for (int k = 0; k < ITER; ++k)
@@ -255,38 +256,45 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
               float2 x[VEC];
               widen<F16, VEC>(ra[k], x);
               widen<F16, VEC>(rb[k], x + VEC / 2);
+              if (it.which < 2) {
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) y[k][i] = it.which < 2 ? mul2(x[i], f0[k][i]) : x[i];
-              if (it.which < 2 && ch[k].pair) {
+                for (int i = 0; i < VEC; ++i) y[k][i] = mul2(x[i], f0[k][i]);
+                if (ch[k].pair) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) y[k][i] = fma2(partner<VEC, INTER>(x, i), f1[k][i], y[k][i]);
+                  for (int i = 0; i < VEC; ++i) y[k][i] = fma2(partner<VEC, INTER>(x, i), f1[k][i], y[k][i]);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) y[k][i] = x[i];
               }
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                y[k][i] = mul2(y[k][i], make_float2(r, r));
-                top = fmax3(top, fabsf(y[k][i].x), fabsf(y[k][i].y));
-              }
+              for (int i = 0; i < VEC; ++i) top = fmax3(top, fabsf(y[k][i].x), fabsf(y[k][i].y));
             }
         }
         top = row_max_of<LPR>(top);
         if (!on) continue;
-        if (it.which == 0) {
+        const float r = norm ? rsqrtf(sum * inv_d + P.eps) : 1.0f;
+        if (it.which == 0) {                       // (queries beside keys in a warp)
 #pragma unroll
           for (int k = 0; k < ITER; ++k)
             if (ch[k].live) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) y[k][i] = mul2(y[k][i], make_float2(r, r));
               *reinterpret_cast<Raw<VEC>*>(dst + ch[k].a * 2) = narrow<F16, VEC>(y[k]);
               *reinterpret_cast<Raw<VEC>*>(dst + ch[k].b * 2) = narrow<F16, VEC>(y[k] + VEC / 2);
             }
         } else {
           // (the smallest scale is a normal number, and its inverse finite)
-          const float whole = fmaxf(top, 0x1p-117f), f = top == 0.0f ? 1.0f : 448.0f / whole;
+          constexpr float least = 0x1p-117f;
+          const float whole = top * r;
+          const float f = top == 0.0f ? 1.0f : whole < least ? r * (448.0f / least) : 448.0f / top;
 #pragma unroll
           for (int k = 0; k < ITER; ++k)
             if (ch[k].live) {
               store_codes<VEC>(dst + ch[k].a, y[k], f);
               store_codes<VEC>(dst + ch[k].b, y[k] + VEC / 2, f);
             }
-          if (lane == 0) *dst_scale = top == 0.0f ? 1.0f : whole / 448.0f;
+          if (lane == 0) *dst_scale = top == 0.0f ? 1.0f : fmaxf(whole, least) * (1.0f / 448.0f);
           dst_scale += scale_h;
         }
         dst += dst_h;
