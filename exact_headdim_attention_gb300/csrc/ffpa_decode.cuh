@@ -88,6 +88,7 @@ struct DecodeParams {
   int64_t table_str;
   const float *ks, *vs;                 // e4m3: scales [page][head][slot], element strides
   int64_t ks_sp, ks_sh, vs_sp, vs_sh;
+  int scale4;                           // four slots' scales are 16 bytes on a boundary
   const int32_t* shared_len;            // own keys: keys that all requests share, in whole pages
   int shared_pages;                     // at most so many of them
   float* o32;                           // own keys: [B][Hq][D] outputs
@@ -245,11 +246,14 @@ __device__ __forceinline__ void fetch_queries(const DecodeParams& P, const Place
   for (int x = threadIdx.x % 32; x < rows * lines; x += 32) fetch_l2(q + x / lines * P.q_sh + x % lines * 128);
 }
 
-// The scale of one key (or value), zero where there is none.
-__device__ __forceinline__ void copy_scale(const DecodeParams& P, bool is_v, uint32_t dst, bool there, int page, int head, int in_page) {
+// The scales of `per` keys (or values) of a page, of which `there` exist: zeros for the others.
+__device__ __forceinline__ void copy_scales(const DecodeParams& P, bool is_v, uint32_t dst, int there, int per, int page, int head, int in_page) {
   const float* src = is_v ? P.vs : P.ks;
-  if (there) src += page * (is_v ? P.vs_sp : P.ks_sp) + head * (is_v ? P.vs_sh : P.ks_sh) + in_page;
-  copy4_async(dst, src, there ? 4 : 0);
+  if (there > 0) src += page * (is_v ? P.vs_sp : P.ks_sp) + head * (is_v ? P.vs_sh : P.ks_sh) + in_page;
+  if (per == 4)
+    copy16_async(dst, src, there <= 0 ? 0 : min(there, 4) * 4);
+  else
+    copy4_async(dst, src, there > 0 ? 4 : 0);
 }
 
 // K (or V) tiles of the run as tensor boxes, a box a lane, its page looked up
@@ -311,11 +315,13 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
         tma_load_5d(dst, map, bar, 0, y, 0, head, z, once);
     }
     if (KIND == DECODE_E4M3) {
-      // The rows' scales, four bytes each, from the pages that the boxes' lanes know.
-      for (int r = lane; r < (T < 32 ? 32 : T); r += 32) {
-        const int owner = min(r, T - 1) / P.box_rows * per_row, in_box = r % P.box_rows;
+      // The rows' scales, from the pages that the boxes' lanes know, four rows a lane where they
+      // are 16 bytes on a boundary (one by one they took 2200 cycles of a tile of 256 keys).
+      const int per = !PAGED && P.scale4 ? 4 : 1;
+      for (int r0 = 0; r0 < T; r0 += 32 * per) {
+        const int r = r0 + lane * per, owner = min(r, T - 1) / P.box_rows * per_row, in_box = r % P.box_rows;
         const int rz = __shfl_sync(~0u, z, owner), ry = __shfl_sync(~0u, y, owner) + in_box;
-        if (r < T) copy_scale(P, is_v, scale_ring + (slot * T + r) * 4, r < keys && rz < P.num_pages, rz, head, ry);
+        if (r < T) copy_scales(P, is_v, scale_ring + (slot * T + r) * 4, rz < P.num_pages ? keys - r : 0, per, rz, head, ry);
       }
       copy_arrive(bar);
     }
@@ -400,7 +406,7 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int
       if (32 * j >= T) break;
       const int end = min(32, T - 32 * j);
       if (KIND == DECODE_E4M3 && lane < end)
-        copy_scale(P, is_v, scale_ring + (slot * T + 32 * j + lane) * 4, from[j] >= 0, scale_page[j], hk, scale_at[j]);
+        copy_scales(P, is_v, scale_ring + (slot * T + 32 * j + lane) * 4, from[j] >= 0, 1, scale_page[j], hk, scale_at[j]);
       // Four rows a lane at a time: their offsets first, then the copies.
       for (int r = 0; r < end; r += 4 * step) {
         int64_t row_at[4];
@@ -789,6 +795,67 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
             qf[s + 1][n][1] = r[3];
           }
       }
+      if (E4M3) {
+        // Both key tiles of a warp that has two, and the two steps of a matrix load apart: chains of
+        // products that do not wait for each other.
+        constexpr int Y = OWN ? 2 : 1;
+        float s[Y][2][NT][4];
+#pragma unroll
+        for (int y = 0; y < Y; ++y)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) s[y][h][n][j] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < (OWN ? 4 : 8); ++x) {
+          if (2 * x >= kn) break;
+          uint32_t q0[NT][2], q1[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 qx = ld_shared_v4(query_at + (x * NT + n) * 512);
+            q0[n][0] = qx.x;
+            q0[n][1] = qx.y;
+            q1[n][0] = qx.z;
+            q1[n][1] = qx.w;
+          }
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const uint32_t a0 = (y ? k_at2 : k_at) + slot_k * stage;
+            uint32_t c[4], lo[4], hi[4];
+            ldm_x4((a0 + (x >> 2) * chunk_bytes) ^ ((x & 3) << 5), c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) widen_e4m3(c[j], lo[j], hi[j]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16<true>(s[y][0][n], lo, q0[n]);
+              mma16<true>(s[y][1][n], hi, q1[n]);
+            }
+          }
+        }
+        // times the keys' scales and the queries' units
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          const float* sk = scale_k + slot_k * T + key0 + y * 16 + hq;
+          const float s0 = sk[0], s8 = sk[8];
+          float* dst = sc + (part * HEADS + c2) * SPITCH + key0 + y * 16 + hq;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float f[4] = {s0, s0, s8, s8};
+            if (!F16) {
+              f[0] *= q_unit[n][0];
+              f[1] *= q_unit[n][1];
+              f[2] *= q_unit[n][0];
+              f[3] *= q_unit[n][1];
+            }
+            dst[n * 8 * SPITCH] = (s[y][0][n][0] + s[y][1][n][0]) * f[0];
+            dst[(n * 8 + 1) * SPITCH] = (s[y][0][n][1] + s[y][1][n][1]) * f[1];
+            dst[n * 8 * SPITCH + 8] = (s[y][0][n][2] + s[y][1][n][2]) * f[2];
+            dst[(n * 8 + 1) * SPITCH + 8] = (s[y][0][n][3] + s[y][1][n][3]) * f[3];
+          }
+        }
+      } else
 #pragma unroll
       for (int y = 0; y < (OWN ? 2 : 1); ++y) {
         const uint32_t a0 = (y ? k_at2 : k_at) + slot_k * stage;
@@ -797,41 +864,13 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
-        if (E4M3) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            if (2 * x >= kn) break;
-            uint32_t c[4], lo[4], hi[4];
-            ldm_x4((a0 + (x >> 2) * chunk_bytes) ^ ((x & 3) << 5), c);
+        for (int x = 0; x < 8; ++x) {
+          if (x >= kn) break;
+          uint32_t a[4];
+          ldm_x4((a0 + (x >> 2) * chunk_bytes) ^ ((x & 3) << 5), a);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) widen_e4m3(c[j], lo[j], hi[j]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 qx = ld_shared_v4(query_at + (x * NT + n) * 512);
-              const uint32_t q0[2] = {qx.x, qx.y}, q1[2] = {qx.z, qx.w};
-              mma16<true>(s[n], lo, q0);
-              mma16<true>(s[n], hi, q1);
-            }
-          }
-          // times the keys' scales and the queries' units
-          const float* sk = scale_k + slot_k * T + key0 + y * 16 + hq;
-          const float s0 = sk[0], s8 = sk[8];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            s[n][0] *= F16 ? s0 : s0 * q_unit[n][0];
-            s[n][1] *= F16 ? s0 : s0 * q_unit[n][1];
-            s[n][2] *= F16 ? s8 : s8 * q_unit[n][0];
-            s[n][3] *= F16 ? s8 : s8 * q_unit[n][1];
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            if (x >= kn) break;
-            uint32_t a[4];
-            ldm_x4((a0 + (x >> 2) * chunk_bytes) ^ ((x & 3) << 5), a);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16<F16>(s[n], a, qf[x][n]);
-          }
+          for (int n = 0; n < NT; ++n) mma16<F16>(s[n], a, qf[x][n]);
         }
         float* dst = sc + (part * HEADS + c2) * SPITCH + key0 + y * 16 + hq;
 #pragma unroll
@@ -947,28 +986,38 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         // A matrix load leaves a lane two neighbouring columns of two keys: the codes of one
         // column are its bytes 0 and 2, those of the next 1 and 3.
 #pragma unroll
-        for (int s = 0; s < DT; ++s) {
+        for (int s = 0; s < DT; s += 2) {            // (two column tiles: two chains of products)
           if (s >= dn) break;
-          uint32_t c[4];
-          ldm_x4_trans((v_at + slot_v * stage) ^ (s << 4), c);
+          uint32_t c[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) ldm_x4_trans((v_at + slot_v * stage) ^ ((s + h) << 4), c[h]);
 #pragma unroll
           for (int g = 0; g < KSTEPS; ++g) {
-            uint32_t a[4];
-            widen_e4m3(__byte_perm(c[2 * g], 0, 0x3120), a[0], a[1]);
-            widen_e4m3(__byte_perm(c[2 * g + 1], 0, 0x3120), a[2], a[3]);
-            if (tail) {
-              const int k = g * 16 + c2;
-              const uint32_t m0 = (k < left ? 0xffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
-              const uint32_t m1 = (k + 8 < left ? 0xffffu : 0u) | (k + 9 < left ? 0xffff0000u : 0u);
-              a[0] &= m0;
-              a[1] &= m0;
-              a[2] &= m1;
-              a[3] &= m1;
+            uint32_t a[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              widen_e4m3(__byte_perm(c[h][2 * g], 0, 0x3120), a[h][0], a[h][1]);
+              widen_e4m3(__byte_perm(c[h][2 * g + 1], 0, 0x3120), a[h][2], a[h][3]);
+              if (tail) {
+                const int k = g * 16 + c2;
+                const uint32_t m0 = (k < left ? 0xffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
+                const uint32_t m1 = (k + 8 < left ? 0xffffu : 0u) | (k + 9 < left ? 0xffff0000u : 0u);
+                a[h][0] &= m0;
+                a[h][1] &= m0;
+                a[h][2] &= m1;
+                a[h][3] &= m1;
+              }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16<true>(acc[s][n], a, pf[g][n]);
+            for (int n = 0; n < NT; ++n) {
+              mma16<true>(acc[s][n], a[0], pf[g][n]);
+              mma16<true>(acc[s + 1][n], a[1], pf[g][n]);
+            }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16<true>(acc[s][n], a, pr[g][n]);
+            for (int n = 0; n < NT; ++n) {
+              mma16<true>(acc[s][n], a[0], pr[g][n]);
+              mma16<true>(acc[s + 1][n], a[1], pr[g][n]);
+            }
           }
         }
       } else
@@ -1492,6 +1541,8 @@ ffpa_status decode_entry(const void* q, const void* k_cache, const void* v_cache
     P.ks_sh = ks_str[1];
     P.vs_sp = vs_str[0];
     P.vs_sh = vs_str[1];
+    const int64_t odd = (s.num_pages > 1 ? P.ks_sp | P.vs_sp : 0) | (s.Hkv > 1 ? P.ks_sh | P.vs_sh : 0) | s.page_size;
+    P.scale4 = odd % 4 == 0 && on_boundary(k_scale, 16) && on_boundary(v_scale, 16);
   }
   return run_decode<KIND>(P, s, dt, sc, sms, dev, static_cast<char*>(workspace), options, reinterpret_cast<cudaStream_t>(stream));
 }
