@@ -536,6 +536,7 @@ template <int KIND, bool F16, int NT, int T, bool PAGED>
 __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(const __grid_constant__ DecodeParams P) {
   constexpr bool E4M3 = KIND == DECODE_E4M3;
   constexpr bool P16 = F16 || E4M3;                  // P (and what it meets) is fp16
+  constexpr bool TWO = !E4M3 || F16;                 // P as two values (e4m3 with bf16 outputs: as one, see below)
   constexpr int CHUNK = 8 / cache_bytes(KIND);       // 16-column steps of a 128-byte chunk
   constexpr int HEADS = 8 * NT, THREADS = DEC_THREADS;
   constexpr int PARTS = decode_parts(T), GROUPS = decode_groups(T), MT = T / 16;
@@ -779,6 +780,21 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       float* sc = scores + (OWN ? 0 : buf) * SBUF;
       buf ^= 1;
       if (OWN) __syncwarp();
+      if (E4M3 && OWN && left <= 0) {              // the tile's keys end before this warp's
+        if (alive) alive = all_waited(smem_u32(full_k + slot_k), lap_k, P, &abort_flag);
+        if (lane == 0) mbar_arrive(smem_u32(empty_k + slot_k));
+        if (++slot_k == P.ring_k) {
+          slot_k = 0;
+          lap_k ^= 1u;
+        }
+        if (alive) alive = all_waited(smem_u32(full_v + slot_v), lap_v, P, &abort_flag);
+        if (lane == 0) mbar_arrive(smem_u32(empty_v + slot_v));
+        if (++slot_v == P.ring_v) {
+          slot_v = 0;
+          lap_v ^= 1u;
+        }
+        continue;
+      }
 
       // ---- scores of 16 keys over this warp's part of D
       if (alive) alive = all_waited(smem_u32(full_k + slot_k), lap_k, P, &abort_flag);
@@ -961,11 +977,17 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
           moved |= unit != vtop[n];
           vtop[n] = unit;
 #pragma unroll
-          for (int j = 0; j < 2 * KSTEPS; ++j)
-            split2<true>(x[j].x * lift, x[j].y * lift, pf[j >> 1][n][j & 1], pr[j >> 1][n][j & 1]);
+          for (int j = 0; j < 2 * KSTEPS; ++j) {
+            // An output of bf16 is rounded to 2^-8 of itself; one fp16 value of a weight, off by 2^-11, adds 1 % to
+            // that error (B128 Hkv16 D128, bf16: 116 us, with two 121).
+            if (TWO)
+              split2<true>(x[j].x * lift, x[j].y * lift, pf[j >> 1][n][j & 1], pr[j >> 1][n][j & 1]);
+            else
+              pf[j >> 1][n][j & 1] = pack_f16(x[j].x * lift, x[j].y * lift);
+          }
         }
       }
-      if (__any_sync(~0u, moved)) {
+      if (__any_sync(~0u, moved) && (!E4M3 || i != i0)) {   // (the first tile's sums are zeros)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float f0 = __shfl_sync(~0u, fac[n], c2 * 4), f1 = __shfl_sync(~0u, fac[n], c2 * 4 + 4);
@@ -1013,11 +1035,12 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
               mma16<true>(acc[s][n], a[0], pf[g][n]);
               mma16<true>(acc[s + 1][n], a[1], pf[g][n]);
             }
+            if (TWO)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16<true>(acc[s][n], a[0], pr[g][n]);
-              mma16<true>(acc[s + 1][n], a[1], pr[g][n]);
-            }
+              for (int n = 0; n < NT; ++n) {
+                mma16<true>(acc[s][n], a[0], pr[g][n]);
+                mma16<true>(acc[s + 1][n], a[1], pr[g][n]);
+              }
           }
         }
       } else

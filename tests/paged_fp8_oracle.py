@@ -54,8 +54,9 @@ def widened(codes, scale):
 def decode(q, kc, vc, ks, vs, table, lens, scale=None):
     """(o, lse, bound on |o's error|, bound on |lse's error|) in 64 bits.
 
-    o is rounded once (u |o|).  A weight times its value's scale enters the sum as two fp16 values: off by
-    2^-21 of it, or 2^-40 of the largest such product, times the code (at most 448).  A score is a sum of
+    o is rounded once (u |o|).  A weight times its value's scale enters the sum as two fp16 values, off by
+    2^-21 of it, or (bf16) as one, off by half a step of fp16, 2^-11; and below the normal range by half
+    of 2^-24, which is 2^-40 of the largest such product (2^15), times the code (at most 448).  A score is a sum of
     at most 64 steps of 16 products, each step off by 2^-23 of partial sums below `size` (the sum of
     the products' sizes, here at most a few times 8): 2^-17 of `size`; the units and scales it is
     multiplied by add 2^-21 of it, and bf16 queries' small columns less.  Exponentials and the other fp32
@@ -63,6 +64,7 @@ def decode(q, kc, vc, ks, vs, table, lens, scale=None):
     B, Hq, D = q.shape
     page, Hkv = kc.shape[1], kc.shape[2]
     u = po.half_step(q.dtype)
+    weight = 2.0 ** -21 if q.dtype == torch.float16 else 2.0 ** -11
     scale = D ** -0.5 if scale is None else scale
     o = torch.zeros(B, Hq, D, dtype=torch.float64)
     bound = torch.zeros_like(o)
@@ -84,7 +86,7 @@ def decode(q, kc, vc, ks, vs, table, lens, scale=None):
             p = torch.exp(x - lse[b, h])
             o[b, h] = p @ vv
             # a weight off by a factor 1 + off moves numerator and sum
-            bound[b, h] = u * o[b, h].abs() + ((p * (off + 2.0 ** -21)) @ vv.abs()) + (p @ off) * o[b, h].abs()
+            bound[b, h] = u * o[b, h].abs() + ((p * (off + weight)) @ vv.abs()) + (p @ off) * o[b, h].abs()
             bound[b, h] += 2.0 ** -39 * (p * sv).max() * 448 * n
             if q.dtype == torch.float16:
                 bound[b, h] += 2.0 ** -25                               # half the smallest fp16
