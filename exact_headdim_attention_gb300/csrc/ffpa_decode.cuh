@@ -153,7 +153,7 @@ DecodePlan decode_plan(int D, int group, int kind) {
   int n = static_cast<int>((SMEM_LIMIT / p.ctas - 8192 - fixed) / stage);
   if (n > 2 * DEC_RING_MAX) n = 2 * DEC_RING_MAX;
   p.ring_v = n / 2;
-  p.ring_k = n - n / 2;
+  p.ring_k = kind == DECODE_E4M3 ? n / 2 : n - n / 2;   // (e4m3: filled in turn)
   p.smem = 1024 + fixed + (size_t)(p.ring_k + p.ring_v) * stage;
   return p;
 }
@@ -259,10 +259,10 @@ __device__ __forceinline__ void copy_scales(const DecodeParams& P, bool is_v, ui
 // K (or V) tiles of the run as tensor boxes, a box a lane, its page looked up
 // one tile ahead.  A page that does not exist, and rows that belong to no key,
 // have a coordinate behind the last page: the copy writes zeros there.
-template <int KIND, bool PAGED>
+template <bool PAGED>
 __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int heads, bool is_v, int skip, Place at,
-                                              const Run& run, uint32_t ring, uint32_t scale_ring, int slots, uint64_t* full,
-                                              uint64_t* empty, volatile int* abort_flag) {
+                                              const Run& run, uint32_t ring, int slots, uint64_t* full, uint64_t* empty,
+                                              volatile int* abort_flag) {
   const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles, n_tiles = run.n;
   const CUtensorMap* map = is_v ? &P.map_v : &P.map_k;
   const int per_row = P.chunks / P.box_chunks;          // boxes side by side (at most 32 boxes a tile)
@@ -292,12 +292,6 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     if (keyed && !good) report_invalid(P.err);
     const int y = good ? in_page : 0, z = good ? page : P.num_pages;
     if (is_v && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
-    int keys = 0;                                  // of the tile
-    if (KIND == DECODE_E4M3) {
-      const int key0 = first_key<PAGED>(P, at.t, T);
-      keys = at.len - key0;
-      if (PAGED) keys = min(keys, P.page_size - key0 % P.page_size);
-    }
     advance<PAGED>(P, pairs, at, T, skip);
     if (i + 1 < n_tiles) {
       look_up(at);
@@ -310,20 +304,9 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     if (mine) {
       const uint32_t dst = ring + slot * stage + to;
       if (P.box_chunks == 1)
-        tma_load_4d(dst, map, bar, chunk * (128 / cache_bytes(KIND)), y, head, z, once);
+        tma_load_4d(dst, map, bar, chunk * 64, y, head, z, once);
       else
         tma_load_5d(dst, map, bar, 0, y, 0, head, z, once);
-    }
-    if (KIND == DECODE_E4M3) {
-      // The rows' scales, from the pages that the boxes' lanes know, four rows a lane where they
-      // are 16 bytes on a boundary (one by one they took 2200 cycles of a tile of 256 keys).
-      const int per = !PAGED && P.scale4 ? 4 : 1;
-      for (int r0 = 0; r0 < T; r0 += 32 * per) {
-        const int r = r0 + lane * per, owner = min(r, T - 1) / P.box_rows * per_row, in_box = r % P.box_rows;
-        const int rz = __shfl_sync(~0u, z, owner), ry = __shfl_sync(~0u, y, owner) + in_box;
-        if (r < T) copy_scales(P, is_v, scale_ring + (slot * T + r) * 4, rz < P.num_pages ? keys - r : 0, per, rz, head, ry);
-      }
-      copy_arrive(bar);
     }
     if (++slot == slots) {
       slot = 0;
@@ -339,6 +322,105 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     }
     --slot;
     wait_drain(smem_u32(full + slot), lap, P.timeout_ns, P.err);
+  }
+}
+
+// e4m3: the same by two warps, each with half of the rows of every K and V tile (and their scales, which an
+// arrival of every lane reports): the pages are looked up once for both, and a tile of small pages, whose boxes an
+// SM starts one in 85 cycles a warp, is on its way in half the time (B128 Hkv16 D128, pages of 16, with a warp for K
+// and one for V: 121 us).
+template <bool PAGED>
+__device__ __forceinline__ void produce_halves(const DecodeParams& P, int T, int heads, int half, Place at, const Run& run,
+                                               uint32_t ring_k, uint32_t ring_v, uint32_t scale_k, uint32_t scale_v,
+                                               uint64_t* full_k, uint64_t* full_v, uint64_t* empty_k, uint64_t* empty_v,
+                                               volatile int* abort_flag) {
+  const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles, n_tiles = run.n, slots = P.ring_k;
+  const int per_row = P.chunks / P.box_chunks;
+  const int boxes = T / P.box_rows;                 // one: the first warp's
+  const int mine_n = boxes > 1 ? boxes / 2 : half == 0 ? 1 : 0, row0 = boxes > 1 ? half * (T / 2) : 0;
+  const int row = row0 + lane / per_row * P.box_rows, chunk = lane % per_row;
+  const bool mine = lane < mine_n * per_row;
+  const uint32_t box_bytes = P.box_rows * P.box_chunks * 128, stage = T * P.chunks * 128;
+  const uint32_t to = row * P.chunks * 128 + chunk * box_bytes, bytes = mine_n * per_row * box_bytes;
+  // Rows whose scales this warp brings, and the row of the page that this lane knows (as many as boxes, or one).
+  const int s0 = half * (T / 2), per = !PAGED && P.scale4 ? 4 : 1;
+  const int known = boxes > 1 ? row : 0;
+  int page = -1, in_page = 0;
+  bool keyed = false;
+  auto look_up = [&](const Place& p) {
+    const int key = first_key<PAGED>(P, p.t, T) + known;
+    keyed = (boxes > 1 ? mine : true) && key < p.len;
+    page = -1;
+    in_page = 0;
+    if (keyed) {
+      const int j = key / P.page_size;
+      in_page = key - j * P.page_size;
+      page = P.table[p.b * P.table_str + j];
+    }
+  };
+  const uint64_t once = once_policy();
+  look_up(at);
+  int slot = 0, i = 0;
+  uint32_t lap = 0;
+  bool alive = true, v_missing = false;
+  for (; i < n_tiles; ++i) {
+    const int head = at.u / P.head_tiles;
+    const bool good = page >= 0 && page < P.num_pages;
+    if (keyed && !good) report_invalid(P.err);
+    const int y = good ? in_page : 0, z = good ? page : P.num_pages;
+    if (half && lane == 0 && (at.t == 0 || i == 0)) note_cut(P, at, run, i, heads);
+    const int key0 = first_key<PAGED>(P, at.t, T);
+    int keys = at.len - key0;
+    if (PAGED) keys = min(keys, P.page_size - key0 % P.page_size);
+    advance<PAGED>(P, pairs, at, T, 0);
+    if (i + 1 < n_tiles) {
+      look_up(at);
+      if (half && at.t == 0) fetch_queries(P, at, heads);
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      uint64_t* empty = v ? empty_v : empty_k;
+      alive = all_waited(smem_u32(empty + slot), lap ^ 1u, P, abort_flag) && !P.drop;
+      if (!alive) {
+        v_missing = v;
+        break;
+      }
+      const uint32_t bar = smem_u32((v ? full_v : full_k) + slot);
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      if (mine) {
+        const uint32_t dst = (v ? ring_v : ring_k) + slot * stage + to;
+        const CUtensorMap* map = v ? &P.map_v : &P.map_k;
+        if (P.box_chunks == 1)
+          tma_load_4d(dst, map, bar, chunk * 128, y, head, z, once);
+        else
+          tma_load_5d(dst, map, bar, 0, y, 0, head, z, once);
+      }
+      for (int r0 = s0; r0 < s0 + T / 2; r0 += 32 * per) {
+        const int r = r0 + lane * per, in = min(r, s0 + T / 2 - 1);
+        const int owner = boxes > 1 ? (in - row0) / P.box_rows * per_row : 0, in_box = boxes > 1 ? r % P.box_rows : r;
+        const int rz = __shfl_sync(~0u, z, owner), ry = __shfl_sync(~0u, y, owner) + in_box;
+        if (r < s0 + T / 2)
+          copy_scales(P, v, (v ? scale_v : scale_k) + (slot * T + r) * 4, rz < P.num_pages ? keys - r : 0, per, rz, head, ry);
+      }
+      copy_arrive(bar);
+    }
+    if (!alive) break;
+    if (++slot == slots) {
+      slot = 0;
+      lap ^= 1u;
+    }
+  }
+  // Copies still in flight land before the CTA ends: the tiles before this one, and its K where only V is missing.
+  if (v_missing) wait_drain(smem_u32(full_k + slot), lap, P.timeout_ns, P.err);
+  for (int j = i < slots ? i : slots; j > 0; --j) {
+    if (slot == 0) {
+      slot = slots;
+      lap ^= 1u;
+    }
+    --slot;
+    wait_drain(smem_u32(full_k + slot), lap, P.timeout_ns, P.err);
+    wait_drain(smem_u32(full_v + slot), lap, P.timeout_ns, P.err);
   }
 }
 
@@ -571,7 +653,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       prefetch_tmap(&P.map_v);
     }
     if (tid < DEC_RING_MAX) {
-      const int arrivals = P.boxed ? (E4M3 ? 33 : 1) : 32;
+      const int arrivals = P.boxed ? (E4M3 ? 66 : 1) : 32;   // (e4m3: of two copying warps)
       mbar_init(smem_u32(full_k + tid), arrivals);
       mbar_init(smem_u32(full_v + tid), arrivals);
       mbar_init(smem_u32(empty_k + tid), DEC_WARPS);
@@ -675,8 +757,11 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
     const int slots = is_v ? P.ring_v : P.ring_k;
     const Run run{lo, total, total < gridDim.x ? total : gridDim.x, n_tiles};
     const uint32_t scale_ring = smem_u32(is_v ? scale_v : scale_k);
-    if (PAGED || P.boxed)
-      produce_boxes<KIND, PAGED>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
+    if (E4M3 && (PAGED || P.boxed))
+      produce_halves<PAGED>(P, T, HEADS, is_v, cur, run, ring_k, ring_v, smem_u32(scale_k), smem_u32(scale_v), full_k, full_v,
+                            empty_k, empty_v, &abort_flag);
+    else if (PAGED || P.boxed)
+      produce_boxes<PAGED>(P, T, HEADS, is_v, skip, cur, run, ring, slots, full, empty, &abort_flag);
     else
       produce_pieces<KIND>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
     return;
