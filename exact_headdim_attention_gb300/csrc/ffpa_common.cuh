@@ -689,8 +689,7 @@ __device__ __forceinline__ void store_part(const Params& p, const Item& it, int 
     reg_fence(o);
     if (row_valid && c0 < dcols) {
 #pragma unroll
-      for (int v = 0; v < 8; ++v)
-        reinterpret_cast<uint4*>(out + c0)[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+      for (int v = 0; v < 4; ++v) st_global_v8(out + c0 + 8 * v, o + 8 * v);
     }
   }
 }

@@ -1130,25 +1130,34 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
         }
       } else
 #pragma unroll
-      for (int s = 0; s < DT; ++s) {
+      for (int s = 0; s < DT; s += 2) {              // (two column tiles: two chains of products)
         if (s >= dn) break;
 #pragma unroll
         for (int g = 0; g < KSTEPS; ++g) {
-          uint32_t a[4];
-          ldm_x4_trans(((g ? v_at2 : v_at) + slot_v * stage + (s >> 2) * chunk_bytes) ^ ((s & 3) << 5), a);
-          if (tail) {
-            const int k = g * 16 + c2;
-            const uint32_t m0 = (k < left ? 0xffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
-            const uint32_t m1 = (k + 8 < left ? 0xffffu : 0u) | (k + 9 < left ? 0xffff0000u : 0u);
-            a[0] &= m0;
-            a[1] &= m0;
-            a[2] &= m1;
-            a[3] &= m1;
+          uint32_t a[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ldm_x4_trans(((g ? v_at2 : v_at) + slot_v * stage + (s >> 2) * chunk_bytes) ^ (((s + h) & 3) << 5), a[h]);
+            if (tail) {
+              const int k = g * 16 + c2;
+              const uint32_t m0 = (k < left ? 0xffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
+              const uint32_t m1 = (k + 8 < left ? 0xffffu : 0u) | (k + 9 < left ? 0xffff0000u : 0u);
+              a[h][0] &= m0;
+              a[h][1] &= m0;
+              a[h][2] &= m1;
+              a[h][3] &= m1;
+            }
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16<F16>(acc[s][n], a, pf[g][n]);
+          for (int n = 0; n < NT; ++n) {
+            mma16<F16>(acc[s][n], a[0], pf[g][n]);
+            mma16<F16>(acc[s + 1][n], a[1], pf[g][n]);
+          }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16<F16>(acc[s][n], a, pr[g][n]);
+          for (int n = 0; n < NT; ++n) {
+            mma16<F16>(acc[s][n], a[0], pr[g][n]);
+            mma16<F16>(acc[s + 1][n], a[1], pr[g][n]);
+          }
         }
       }
       __syncwarp();
@@ -1365,6 +1374,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) join_kernel(const __grid_c
   __shared__ float2 ml_s[JOIN_WARPS];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int tasks = (P.D + 127) / 128 << log_rows;
+  if (KIND == DECODE_OWN) dependents_launch();     // (the merge waits for this kernel's end)
   dependency_wait();
   const int4 m = P.cuts[blockIdx.x];
   const int n = m.x >> 16, first = m.x & 0xffff;   // CTAs of the pair
