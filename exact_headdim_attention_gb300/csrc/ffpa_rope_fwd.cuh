@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
     }
     const int per = steps(first);
     const bool codes = E4M3 && __any_sync(~0u, it.which > 0);   // (rows of a warp may be of both kinds)
+    const bool turned = it.which < 2 && (!E4M3 || norm || P.rot > 0);   // (e4m3: else rows are as they came)
 #pragma unroll 1
     for (int h = 0; h < per; ++h) {
       copy_wait<ROPE_DEPTH - 2>();
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
               float2 x[VEC];
               widen<F16, VEC>(ra[k], x);
               widen<F16, VEC>(rb[k], x + VEC / 2);
-              if (it.which < 2) {
+              if (turned) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) y[k][i] = mul2(x[i], f0[k][i]);
                 if (ch[k].pair) {
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
 #pragma unroll
       for (int k = 0; k < ITER; ++k)
         if (ch[k].live) {
-          if (it.which < 2) {
+          if (turned) {
             float2 x[VEC], y[VEC];
             widen<F16, VEC>(ra[k], x);
             widen<F16, VEC>(rb[k], x + VEC / 2);
