@@ -406,11 +406,13 @@ __device__ __forceinline__ void decode_item_shared(const Params& p, int L, int p
   it.dv = (c_hi - c_lo) * DK;
 }
 
-// Keys that row r of a query tile (whose first row is row0) sees; all for rows that are not stored.
+// Keys that row r of a query tile (whose first row is row0) sees here: all, or none where its request ends
+// among them (such a request attends with its own keys: what lies behind its last key may be
+// anything, and zero times that is not zero).  All for rows that are not stored.
 __device__ __forceinline__ int shared_limit(const Params& p, const Item& it, int row0, int r) {
   const int row = row0 + r;
   if (r >= p.sh.tile_rows || row >= it.q_len) return it.kv_len;
-  return min(max(p.sh.lens[row / p.group], 0), it.kv_len);
+  return p.sh.lens[row / p.group] >= it.kv_len ? it.kv_len : 0;
 }
 
 // Masks 128 scores of a row that sees `limit` keys.

@@ -90,6 +90,7 @@ struct DecodeParams {
   int64_t ks_sp, ks_sh, vs_sp, vs_sh;
   int scale4;                           // four slots' scales are 16 bytes on a boundary
   const int32_t* shared_len;            // own keys: keys that all requests share, in whole pages
+  const int32_t* shared_table;          // their pages
   int shared_pages;                     // at most so many of them
   float* o32;                           // own keys: [B][Hq][D] outputs
   unsigned long long timeout_ns;
@@ -163,11 +164,17 @@ struct Place {
   int b, u, t, tiles, len;
 };
 
-// Keys of a request behind the first `skip` pages.
+// Keys of a request behind the `skip` pages that are shared; all of one that ends among those.
 __device__ __forceinline__ int clamped_len(const DecodeParams& P, int n, int skip) {
   const long long cap = (long long)P.max_pages * P.page_size;
   n = n < 0 ? 0 : n > cap ? (int)cap : n;
-  return skip == 0 ? n : max(0, n - skip * P.page_size);
+  return n < skip * P.page_size ? n : n - skip * P.page_size;
+}
+// The pages of those keys.
+template <int KIND>
+__device__ __forceinline__ const int32_t* pages_of(const DecodeParams& P, int b, int skip) {
+  if (KIND == DECODE_OWN && skip > 0 && P.lens[b] < skip * P.page_size) return P.shared_table;
+  return P.table + b * P.table_str + skip;
 }
 // A length out of range.
 __device__ __forceinline__ bool bad_len(const DecodeParams& P, int n) { return n < 0 || n > (long long)P.max_pages * P.page_size; }
@@ -259,7 +266,7 @@ __device__ __forceinline__ void copy_scales(const DecodeParams& P, bool is_v, ui
 // K (or V) tiles of the run as tensor boxes, a box a lane, its page looked up
 // one tile ahead.  A page that does not exist, and rows that belong to no key,
 // have a coordinate behind the last page: the copy writes zeros there.
-template <bool PAGED>
+template <int KIND, bool PAGED>
 __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int heads, bool is_v, int skip, Place at,
                                               const Run& run, uint32_t ring, int slots, uint64_t* full, uint64_t* empty,
                                               volatile int* abort_flag) {
@@ -279,7 +286,7 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     if (keyed) {
       const int j = key / P.page_size;
       in_page = key - j * P.page_size;
-      page = P.table[p.b * P.table_str + skip + j];
+      page = pages_of<KIND>(P, p.b, skip)[j];
     }
   };
   const uint64_t once = once_policy();
@@ -446,7 +453,7 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int
     for (int j = 0; j < 8; ++j) {
       if (32 * j >= T) break;
       const int r = lane + 32 * j, key = p.t * T + r;
-      page[j] = r < T && key < p.len ? P.table[p.b * P.table_str + skip + key / P.page_size] : -1;
+      page[j] = r < T && key < p.len ? pages_of<KIND>(P, p.b, skip)[key / P.page_size] : -1;
     }
   };
   look_up(at);
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       produce_halves<PAGED>(P, T, HEADS, is_v, cur, run, ring_k, ring_v, smem_u32(scale_k), smem_u32(scale_v), full_k, full_v,
                             empty_k, empty_v, &abort_flag);
     else if (PAGED || P.boxed)
-      produce_boxes<PAGED>(P, T, HEADS, is_v, skip, cur, run, ring, slots, full, empty, &abort_flag);
+      produce_boxes<KIND, PAGED>(P, T, HEADS, is_v, skip, cur, run, ring, slots, full, empty, &abort_flag);
     else
       produce_pieces<KIND>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
     return;

@@ -276,6 +276,7 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
   P.table_str = table_str;
   P.shared_len = shared_len;
   P.shared_pages = pages;
+  P.shared_table = shared_pages;
   st = run_decode<DECODE_OWN>(P, shape, dt, sc, sms, dev, ws, options, s);
   if (st != FFPA_OK) return st;
 

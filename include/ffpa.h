@@ -695,12 +695,13 @@ ffpa_status ffpa_kv_read(const void* k_cache, const void* v_cache, const float* 
  *     min(shared_len[0] / page_size, n_shared) * page_size keys.  (0: as ffpa_decode_paged.)
  *   block_table, seq_lens: as for ffpa_decode_paged, over ALL keys of a request, the
  *     shared ones among them; the first S / page_size entries of a row are not read.
- *     A request of fewer than S keys sees that many of the shared ones.
+ *     A request of fewer than S keys sees that many of the shared ones (they are read once more
+ *     for it).
  *   workspace: of at least ffpa_decode_shared_workspace_bytes(B, Hq, Hkv, D) bytes.
  *
  * The result is that of ffpa_decode_paged with the shared pages in every row of the table,
  * up to the order of the sums; a softmax weight of a shared key enters them as a 16-bit
- * value (2^-9 of itself, fp16 2^-12 and 2^-24 of the largest) and all else in fp32.
+ * value (bf16: off by 2^-8 of itself, fp16: by 2^-11, or by 2^-32 of the largest) and all else in fp32.
  * D a multiple of 64 from 64 to 1024, page_size a multiple of 8 (else FFPA_ERR_UNSUPPORTED).
  * Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
  */

@@ -301,6 +301,22 @@ def test_append_slots_beyond_the_cache_are_reported():
     device_ok()
 
 
+def test_append_into_strided_scales():
+    """Scales cut from a wider buffer, keys' and values' halves of one."""
+    case = append_case(40, 2, 2, 128, 16, 4, BF, 64, True, 15)
+    q, k, v, pos, inv, w, slots = case
+    d = lambda t: t.to(DEV)   # noqa: E731
+    both = torch.full((4, 2, 3, 19), -7.0, device=DEV)
+    ks, vs = both[:, 0, :2, 1:17], both[:, 1, 1:, 3:]
+    cache = torch.full((4, 16, 2, 2, 128), 0x7f, dtype=torch.uint8, device=DEV).view(E4M3)
+    kc, vc = cache[:, :, 0], cache[:, :, 1]
+    word = word_()
+    out = pkg.ffpa_kv_append_fp8(d(q), d(k), d(v), kc, vc, ks, vs, d(slots), d(pos), d(inv), d(w[0]), d(w[1]), status=word)
+    torch.cuda.synchronize()
+    check_append(case, (out, kc, vc, ks, vs, word.item()))
+    assert (both[:, 0, 2] == -7).all() and (both[:, 1, 0] == -7).all() and (both[..., 0] == -7).all() and (both[:, 0, :, 17:] == -7).all()
+
+
 def test_append_agrees_with_the_16_bit_append():
     """The same rows in a 16-bit cache: queries equal bit for bit, keys within half a step of e4m3 and of bf16."""
     case = append_case(60, 4, 2, 512, 16, 6, BF, 512, True, 14)
@@ -362,6 +378,19 @@ def test_read_head_dims(D, codes, dtype):
 @pytest.mark.parametrize("Hkv,D,codes", [(1, 64, True), (8, 128, True), (2, 72, False)])
 def test_read_lengths_and_pages(lens, page, Hkv, D, codes):
     check_read(read_case(lens, Hkv, D, page, page + len(lens), codes, HF, layout="phs" if page == 16 else "psh"), HF, spare=page % 2)
+
+
+def test_read_into_strided_rows():
+    """Outputs as slices of one buffer of keys and values."""
+    kc, vc, ks, vs, table, n, cu = read_case([20, 0, 33], 2, 128, 16, 5)
+    both = torch.full((60, 5, 128), 9.0, dtype=BF, device=DEV)
+    k, v = both[:53, :2], both[:53, 3:]
+    d = [t.to(DEV) for t in (kc, vc, table, cu, ks, vs)]
+    pkg.ffpa_kv_read(*d[:4], 53, k_scale=d[4], v_scale=d[5], k_out=k, v_out=v)
+    device_ok()
+    close(k, *p8.read(kc, ks, table, n, BF), "k")
+    close(v, *p8.read(vc, vs, table, n, BF), "v")
+    assert (both[:, 2] == 9).all() and (both[53:] == 9).all()
 
 
 def test_read_defaults_and_nothing():

@@ -100,6 +100,18 @@ def test_requests_shorter_than_the_prefix(D):
     assert (o[0] == 0).all() and (o[7] == 0).all() and (lse[[0, 7]] == -math.inf).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256, 320, 1024])
+def test_shared_pages_may_hold_anything_behind_the_last_key(D):
+    """Where no request is as long as the shared keys, infinities and NaN behind the longest."""
+    lens = [0, 1, 100, 129, 256, 300, 0, 127]
+    args, ref = make([0] * 8, 320, 4, 2, D, 16, BF, seed=D, lens=lens)
+    q, kc, vc, pages = args[:4]
+    for i, p in enumerate(pages.tolist()):
+        seen = max(0, min(16, 300 - 16 * i))
+        kc[p, seen:], vc[p, seen:] = math.nan, math.inf
+    check(args, ref, f"D={D}")
+
+
 @pytest.mark.parametrize("scale", [0.0, 0.5, -0.1])
 @pytest.mark.parametrize("D", [128, 256, 512])
 def test_softmax_scale(D, scale):
