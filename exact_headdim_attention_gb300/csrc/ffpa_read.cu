@@ -4,7 +4,8 @@
 // Every row is read and written once: the memory's bandwidth is the bound.  A block
 // takes some tokens of keys or of values; it looks up their requests and pages first,
 // then all its threads move 16-byte pieces, FLIGHT of them on their way a thread, in
-// the order of the output.
+// the order of the output.  24 contexts of up to 8192 keys, Hkv8 D512, codes: 297 us, 6.4 TB/s of bytes read and
+// written; 40 of up to 3000, Hkv16 D128, 16 bits: 157 us, 6.4 TB/s.
 #include "ffpa_paged.cuh"
 
 namespace ffpa {

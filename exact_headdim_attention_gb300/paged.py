@@ -14,6 +14,10 @@ is shared by all layers.  As in _binding.py every computation runs in the CUDA k
 ABI (include/ffpa.h); tensors are checked, outputs allocated and the ABI called in
 csrc/paged_binding.cpp, because calls that serve single tokens are as short as a few microseconds.
 
+A cache of 8 bits a value is written by ffpa_kv_append_fp8 and read by ffpa_decode_paged_fp8; ffpa_kv_read
+returns cached rows as packed 16-bit ones, for a prompt's attention behind them; ffpa_decode_shared
+takes the place of ffpa_decode_paged where requests share the pages of their first tokens.
+
 A call on a stream of the caller's (stream=) makes its outputs in the current stream's memory, as the
 attention calls do: the caller orders the two streams and keeps the outputs until the call is done.
 """
