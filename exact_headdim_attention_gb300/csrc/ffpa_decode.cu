@@ -1,6 +1,15 @@
 // Attention of one new token per request over a paged cache of 16-bit values.
 #include "ffpa_decode.cuh"
 
+namespace ffpa {
+
+ffpa_status run_decode_16(DecodeParams& P, const DecodeShape& s, ffpa_dtype dt, float sc, int sms, int dev, char* ws,
+                          const ffpa_options* options, cudaStream_t stream) {
+  return run_decode<DECODE_16>(P, s, dt, sc, sms, dev, ws, options, stream);
+}
+
+}  // namespace ffpa
+
 extern "C" {
 
 size_t ffpa_decode_paged_workspace_bytes(int Hq, int Hkv, int D) { return ffpa::decode_bytes(Hq, Hkv, D); }

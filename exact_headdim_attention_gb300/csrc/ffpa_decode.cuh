@@ -67,17 +67,6 @@ enum DecodeKind {
 };
 __host__ __device__ constexpr int cache_bytes(int kind) { return kind == DECODE_E4M3 ? 1 : 2; }
 
-namespace {
-
-constexpr int DEC_WARPS = 8;          // that multiply
-constexpr int DEC_THREADS = (DEC_WARPS + 2) * 32;   // and one each that brings K and V
-constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
-// Powers of two above the maximum at which fp16 forms its exponentials: the largest is
-// 2^15, and 2^-39 of it is the smallest that counts.
-constexpr float P_LIFT = 15.0f;
-// SMs of any sm_103 part; the workspace is sized for them without asking a device.
-constexpr int DEC_SMS_MAX = 160;
-
 struct DecodeParams {
   CUtensorMap map_k, map_v;
   const char *q, *k, *v;
@@ -96,7 +85,7 @@ struct DecodeParams {
   const float *ks, *vs;                 // e4m3: scales [page][head][slot], element strides
   int64_t ks_sp, ks_sh, vs_sp, vs_sh;
   int scale4;                           // four slots' scales are 16 bytes on a boundary
-  const int32_t* shared_len;            // own keys: keys that all requests share, in whole pages
+  const int32_t* shared_len;            // own keys (and 16 bits, else 0): keys that all requests share, in whole pages
   const int32_t* shared_table;          // their pages
   int shared_pages;                     // at most so many of them
   float* o32;                           // own keys: [B][Hq][D] outputs
@@ -111,6 +100,28 @@ struct DecodeParams {
   int ring_k, ring_v, drop;
   float scale_log2;
 };
+
+struct DecodeShape {
+  int B, Hq, Hkv, D, num_pages, page_size, max_pages;
+  const int64_t *k_str, *v_str;
+  bool held() const { return num_pages > 0 && max_pages > 0; }
+};
+
+// Decode over a 16-bit cache with P's pointers set (ffpa_decode.cu); shared_len, shared_table and shared_pages name
+// pages that stand before every request's own, or are 0.
+ffpa_status run_decode_16(DecodeParams& P, const DecodeShape& s, ffpa_dtype dt, float sc, int sms, int dev, char* ws,
+                          const ffpa_options* options, cudaStream_t stream);
+
+namespace {
+
+constexpr int DEC_WARPS = 8;          // that multiply
+constexpr int DEC_THREADS = (DEC_WARPS + 2) * 32;   // and one each that brings K and V
+constexpr int DEC_RING_MAX = 8;       // tiles of K (and of V) in the ring
+// Powers of two above the maximum at which fp16 forms its exponentials: the largest is
+// 2^15, and 2^-39 of it is the smallest that counts.
+constexpr float P_LIFT = 15.0f;
+// SMs of any sm_103 part; the workspace is sized for them without asking a device.
+constexpr int DEC_SMS_MAX = 160;
 
 // Sizes of one call.  A tile has T = 16 keys for rows of more than 1 KB and twice as many each
 // time they halve (at most 32 KB).
@@ -177,11 +188,13 @@ __device__ __forceinline__ int clamped_len(const DecodeParams& P, int n, int ski
   n = n < 0 ? 0 : n > cap ? (int)cap : n;
   return n < skip * P.page_size ? n : n - skip * P.page_size;
 }
-// The pages of those keys.
+// Page j of those keys (16 bits: of all keys of a request, the first of them in the shared pages).
 template <int KIND>
-__device__ __forceinline__ const int32_t* pages_of(const DecodeParams& P, int b, int skip) {
-  if (KIND == DECODE_OWN && skip > 0 && P.lens[b] < skip * P.page_size) return P.shared_table;
-  return P.table + b * P.table_str + skip;
+__device__ __forceinline__ int page_of(const DecodeParams& P, int b, int j, int shared) {
+  const int32_t* t = P.table + b * P.table_str;
+  if (KIND == DECODE_16 && j < shared) t = P.shared_table;
+  if (KIND == DECODE_OWN) t = shared > 0 && P.lens[b] < shared * P.page_size ? P.shared_table : t + shared;
+  return t[j];
 }
 // A length out of range.
 __device__ __forceinline__ bool bad_len(const DecodeParams& P, int n) { return n < 0 || n > (long long)P.max_pages * P.page_size; }
@@ -189,7 +202,7 @@ __device__ __forceinline__ bool bad_len(const DecodeParams& P, int n) { return n
 // The pages that all requests share, of which only whole ones count.
 template <int KIND>
 __device__ __forceinline__ int pages_shared(const DecodeParams& P) {
-  if (KIND != DECODE_OWN) return 0;
+  if (KIND == DECODE_E4M3 || !P.shared_len) return 0;
   const int n = *P.shared_len;
   return n < 0 ? 0 : min(n / P.page_size, min(P.shared_pages, P.max_pages));
 }
@@ -274,7 +287,7 @@ __device__ __forceinline__ void copy_scales(const DecodeParams& P, bool is_v, ui
 // one tile ahead.  A page that does not exist, and rows that belong to no key,
 // have a coordinate behind the last page: the copy writes zeros there.
 template <int KIND, bool PAGED>
-__device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int heads, bool is_v, int skip, Place at,
+__device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int heads, bool is_v, int skip, int shared, Place at,
                                               const Run& run, uint32_t ring, int slots, uint64_t* full, uint64_t* empty,
                                               volatile int* abort_flag) {
   const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles, n_tiles = run.n;
@@ -293,7 +306,7 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     if (keyed) {
       const int j = key / P.page_size;
       in_page = key - j * P.page_size;
-      page = pages_of<KIND>(P, p.b, skip)[j];
+      page = page_of<KIND>(P, p.b, j, shared);
     }
   };
   const uint64_t once = once_policy();
@@ -443,7 +456,7 @@ __device__ __forceinline__ void produce_halves(const DecodeParams& P, int T, int
 // lanes to a row.  A row without a key, or of a page that does not exist,
 // becomes zeros.
 template <int KIND>
-__device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int heads, bool is_v, int skip, Place at,
+__device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int heads, bool is_v, int skip, int shared, Place at,
                                                const Run& run, uint32_t ring, uint32_t scale_ring, int slots, uint64_t* full,
                                                uint64_t* empty, volatile int* abort_flag) {
   const int lane = threadIdx.x % 32, pairs = P.Hkv * P.head_tiles, n_tiles = run.n;
@@ -460,7 +473,7 @@ __device__ __forceinline__ void produce_pieces(const DecodeParams& P, int T, int
     for (int j = 0; j < 8; ++j) {
       if (32 * j >= T) break;
       const int r = lane + 32 * j, key = p.t * T + r;
-      page[j] = r < T && key < p.len ? pages_of<KIND>(P, p.b, skip)[key / P.page_size] : -1;
+      page[j] = r < T && key < p.len ? page_of<KIND>(P, p.b, key / P.page_size, shared) : -1;
     }
   };
   look_up(at);
@@ -653,7 +666,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = P.Hkv * P.head_tiles;
   const uint32_t stage = T * P.chunks * 128;
-  const int skip = pages_shared<KIND>(P);
+  const int shared = pages_shared<KIND>(P), skip = KIND == DECODE_OWN ? shared : 0;
+  if (KIND == DECODE_16 && P.shared_len && tid == 0 && blockIdx.x == 0 && *P.shared_len < 0) report_invalid(P.err);
 
   // ---- this CTA's run of tiles
   long long total, lo, hi;
@@ -775,9 +789,9 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
       produce_halves<PAGED>(P, T, HEADS, is_v, cur, run, ring_k, ring_v, smem_u32(scale_k), smem_u32(scale_v), full_k, full_v,
                             empty_k, empty_v, &abort_flag);
     else if (PAGED || P.boxed)
-      produce_boxes<KIND, PAGED>(P, T, HEADS, is_v, skip, cur, run, ring, slots, full, empty, &abort_flag);
+      produce_boxes<KIND, PAGED>(P, T, HEADS, is_v, skip, shared, cur, run, ring, slots, full, empty, &abort_flag);
     else
-      produce_pieces<KIND>(P, T, HEADS, is_v, skip, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
+      produce_pieces<KIND>(P, T, HEADS, is_v, skip, shared, cur, run, ring, scale_ring, slots, full, empty, &abort_flag);
     return;
   }
 
@@ -1505,12 +1519,6 @@ ffpa_status launch_decode(const DecodeParams& P, const DecodePlan& pl, int grid,
 
 
 // ---- host: what the entry points share
-
-struct DecodeShape {
-  int B, Hq, Hkv, D, num_pages, page_size, max_pages;
-  const int64_t *k_str, *v_str;
-  bool held() const { return num_pages > 0 && max_pages > 0; }
-};
 
 // The checks that need no device (pointers may be anything).  Element sizes: queries and
 // outputs 2 bytes, the cache's by its kind.

@@ -88,6 +88,12 @@ struct MergeParams {
   int B, Hq, D, group, tile_rows, tiles, splits;   // query tiles of a part (with the empty one of a last pair)
 };
 
+// Where all requests' reads of the shared keys come to no more than this, one decode over all keys reads them
+// from L2, in two launches in place of four; for one request it reads no more than the split does.  Measured, one
+// pass and split (us): 8 MB (B1 S2048 Hkv8 D128) 8.9 and 14.1, 33 MB (B16 S1010 Hkv4 D128) 12.4 and 13.8, 34 MB
+// (B4 S2048 Hkv8 D128) 11.8 and 14.7, 67 MB (B16 S2048 Hkv4 D128) 14.6 and 15.0, 134 MB (B64 S1024 Hkv4 D128) 21.3
+// and 19.2, 537 MB (B8 S4096 Hkv8 D512) 56.7 and 29.6; B1 S16384 Hkv8 D512 46.1 and 57.7.
+constexpr double ONE_PASS_BYTES = 64e6;
 constexpr int MERGE_WARPS = 4;
 constexpr int MERGE_FLIGHT = 8;   // parts on their way
 constexpr float LOG2E = 1.4426950408889634f;
@@ -208,9 +214,32 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
   if (pages == 0) pl.splits = 0;
   const SharedSpace sp = shared_space(B, Hq, Hkv, D, pl.parts());
 
+  DecodeParams P{};
+  P.err = err;
+  P.q = static_cast<const char*>(q);
+  P.k = static_cast<const char*>(k_cache);
+  P.v = static_cast<const char*>(v_cache);
+  P.table = block_table;
+  P.lens = seq_lens;
+  P.q_sb = q_str[0] * 2;
+  P.q_sh = q_str[1] * 2;
+  P.table_str = table_str;
+  P.shared_len = shared_len;
+  P.shared_table = shared_pages;
+  P.shared_pages = pages;
+  const int way = options ? options->kernel : FFPA_VARIANT_AUTO;
+  if (way == FFPA_VARIANT_SINGLE ||
+      (way == FFPA_VARIANT_AUTO && (B == 1 || (double)B * Hkv * D * 4 * pages * page_size <= ONE_PASS_BYTES))) {
+    P.o = static_cast<char*>(o);
+    P.lse = lse;
+    P.o_sb = o_str[0] * 2;
+    P.o_sh = o_str[1] * 2;
+    return run_decode_16(P, shape, dt, sc, sms, dev, ws, options, s);
+  }
+
   // ---- the shared keys
   if (pages > 0) {
-    Params P{};
+    Params P{};                                      // (of the forward kernels)
     const size_t smem = plan_shared(pl.kernel, D, &P);
     const int group = Hq / Hkv;
     // Queries as (64, heads of a group, requests, chunks, key heads); a box is a chunk of a tile.
@@ -267,21 +296,8 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
   }
 
   // ---- the requests' own keys
-  DecodeParams P{};
-  P.err = err;
-  P.q = static_cast<const char*>(q);
-  P.k = static_cast<const char*>(k_cache);
-  P.v = static_cast<const char*>(v_cache);
   P.o32 = reinterpret_cast<float*>(ws + sp.o32);
   P.lse = reinterpret_cast<float*>(ws + sp.lse);
-  P.table = block_table;
-  P.lens = seq_lens;
-  P.q_sb = q_str[0] * 2;
-  P.q_sh = q_str[1] * 2;
-  P.table_str = table_str;
-  P.shared_len = shared_len;
-  P.shared_pages = pages;
-  P.shared_table = shared_pages;
   st = run_decode<DECODE_OWN>(P, shape, dt, sc, sms, dev, ws, options, s);
   if (st != FFPA_OK) return st;
 

@@ -74,11 +74,11 @@ def _on_stream(workspace, need, t, stream):
         return torch.empty(max(need, 256), dtype=torch.uint8, device=t.device)
 
 
-def _call_options(t, status, wait_timeout_ns=None, test_drop_first_copy=False):
+def _call_options(t, status, wait_timeout_ns=None, test_drop_first_copy=False, kernel=None):
     """(the call's ffpa_options, kept alive by the caller; their address), or (None, None)."""
-    if status is None and not wait_timeout_ns and not test_drop_first_copy:
+    if status is None and not wait_timeout_ns and not test_drop_first_copy and kernel is None:
         return None, None
-    ref = _options(t, None, status, wait_timeout_ns, test_drop_first_copy)
+    ref = _options(t, kernel, status, wait_timeout_ns, test_drop_first_copy)
     return ref, ctypes.addressof(ref._obj)
 
 
@@ -286,20 +286,22 @@ def decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
 def ffpa_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, shared_pages: torch.Tensor,
                        shared_len: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *,
                        scale: float | None = None, enable_gqa: bool = False, return_lse: bool = False, out=None,
-                       lse=None, workspace=None, stream=None, status=None, wait_timeout_ns=None,
-                       test_drop_first_copy=False):
+                       lse=None, workspace=None, stream=None, kernel=None, status=None,
+                       wait_timeout_ns=None, test_drop_first_copy=False):
     """ffpa_decode_paged for requests that begin with the same tokens, through ``ffpa_decode_shared``.
 
     The first shared_len[0] keys (int32 [1]; whole pages of them count) of every request lie in shared_pages
     (int32 [n], in order), which are read and multiplied once for the whole batch.  block_table and
     seq_lens are those of ffpa_decode_paged, the shared keys included; the entries of the shared pages in
     block_table are not read, and a request of fewer keys sees that many.  D a multiple of 64, page_size
-    of 8.  Other arguments and the result as for ffpa_decode_paged; workspace: of
-    decode_shared_workspace_bytes(...) bytes."""
+    of 8.  kernel: "single" decodes over all keys of each request in one pass (the shared pages are read
+    for every request: a few, or short ones), "split" reads the shared keys apart; None chooses by the
+    batch and the number of shared_pages.  Other arguments and the result as for ffpa_decode_paged;
+    workspace: of decode_shared_workspace_bytes(...) bytes."""
     if stream is not None:
         need = decode_shared_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2])
         workspace = _on_stream(workspace, need, q, stream)
-    keep, options = _call_options(q, status, wait_timeout_ns, test_drop_first_copy)
+    keep, options = _call_options(q, status, wait_timeout_ns, test_drop_first_copy, kernel)
     r = _native().decode_shared(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale, enable_gqa,
                                 return_lse, out, lse, workspace, _handle(stream), options)
     if type(r) is int:

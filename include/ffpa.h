@@ -483,8 +483,8 @@ ffpa_status ffpa_bwd_noalloc(const void* q, const void* k, const void* v, const 
  * the host.  The kernels check them: one that is out of range is never used
  * as an address, and the call's status word (ffpa_options.status, or the
  * device's fallback word) records FFPA_ERR_INVALID.  ffpa_decode_paged takes
- * the wait limit and the test hook too; the other options have no effect on
- * these entry points.
+ * the wait limit and the test hook too, ffpa_decode_shared these and the kernel choice; the
+ * other options have no effect on these entry points.
  */
 
 /*
@@ -627,8 +627,8 @@ ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_
  *
  *     scale = a / 448,   codes = e4m3(y * (448 / a))
  *
- * in fp32, codes rounded to nearest even (a row of zeros: scale 1; a row with an
- * infinity or a NaN: codes and scale that are not finite).  Each code is off by at
+ * in fp32, codes rounded to nearest even (a row of zeros: scale 1; a NaN stays one;
+ * a row with an infinity has an infinite scale).  Each code is off by at
  * most 2^-4 of its value, or 2^-10 scales.  The rows are not rounded to 16 bits
  * before.  Arguments and checks otherwise as for ffpa_kv_append.
  */
@@ -703,7 +703,10 @@ ffpa_status ffpa_kv_read(const void* k_cache, const void* v_cache, const float* 
  * up to the order of the sums; a softmax weight of a shared key enters them as a 16-bit
  * value (bf16: off by 2^-8 of itself, fp16: by 2^-11, or by 2^-32 of the largest) and all else in fp32.
  * D a multiple of 64 from 64 to 1024, page_size a multiple of 8 (else FFPA_ERR_UNSUPPORTED).
- * Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
+ * options->kernel: FFPA_VARIANT_AUTO chooses, by the batch and n_shared, between reading the
+ * shared keys apart from the requests' own and (where that is little) one pass over all keys of
+ * each request; FFPA_VARIANT_SINGLE always takes the one pass (as exact as ffpa_decode_paged), another value
+ * never.  Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
  */
 size_t ffpa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D);
 ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,

@@ -52,8 +52,9 @@ def test_shared_pages():
     pkg.ffpa_kv_append(None, k, v, kc, vc, slots)
     table, lens = ids[None].int(), torch.tensor([T], dtype=torch.int32, device=DEV)
     shared = torch.tensor([128], dtype=torch.int32, device=DEV)
-    o = pkg.ffpa_decode_shared(q, kc, vc, table[0, :8].contiguous(), shared, table, lens, enable_gqa=True)
     few = near(ids.numel())
-    want = pkg.ffpa_decode_shared(q, kc[ids], vc[ids], few[0, :8].contiguous(), shared, few, lens, enable_gqa=True)
-    assert torch.equal(o, want)
+    for kernel in ("split", "single"):
+        o = pkg.ffpa_decode_shared(q, kc, vc, table[0, :8].contiguous(), shared, table, lens, enable_gqa=True, kernel=kernel)
+        want = pkg.ffpa_decode_shared(q, kc[ids], vc[ids], few[0, :8].contiguous(), shared, few, lens, enable_gqa=True, kernel=kernel)
+        assert torch.equal(o, want)
     device_ok()

@@ -1,5 +1,6 @@
 """Decode attention of a batch with a shared prefix on the GPU, against the 64-bit reference of decode
 attention over the same keys (paged_oracle.py, whose bound counts one rounding of a weight)."""
+import functools
 import math
 
 import pytest
@@ -45,13 +46,19 @@ def make(own, shared, Hq, Hkv, D, page, dtype, seed=0, layout="psh", scale=None,
 
 
 def check(args, ref, what="", scale=None, **kw):
-    word = word_()
-    o, lse = pkg.ffpa_decode_shared(*args, scale=scale, enable_gqa=True, return_lse=True, status=word, **kw)
-    torch.cuda.synchronize()
-    assert word.item() == pkg.FFPA_OK
-    close(o, ref[0], ref[2], f"{what} O")
-    close(lse, ref[1], ref[3], f"{what} LSE")
+    """In one pass, by the call's own choice, and with the shared keys apart (whose result is returned)."""
+    for kernel in ("single", None, "split"):
+        word = word_()
+        o, lse = pkg.ffpa_decode_shared(*args, scale=scale, enable_gqa=True, return_lse=True, status=word, kernel=kernel, **kw)
+        torch.cuda.synchronize()
+        assert word.item() == pkg.FFPA_OK
+        close(o, ref[0], ref[2], f"{what} {kernel} O")
+        close(lse, ref[1], ref[3], f"{what} {kernel} LSE")
     return o, lse
+
+
+def split(*args, **kw):
+    return pkg.ffpa_decode_shared(*args, kernel="split", **kw)
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
@@ -96,7 +103,7 @@ def test_requests_shorter_than_the_prefix(D):
     lens = [0, 1, 100, 129, 256, 300, 320, 0, 127]
     args, ref = make([0] * 9, 320, 4, 2, D, 16, BF, seed=D, lens=lens)
     check(args, ref, f"D={D}")
-    o, lse = pkg.ffpa_decode_shared(*args, enable_gqa=True, return_lse=True)
+    o, lse = split(*args, enable_gqa=True, return_lse=True)
     assert (o[0] == 0).all() and (o[7] == 0).all() and (lse[[0, 7]] == -math.inf).all()
 
 
@@ -148,7 +155,7 @@ def test_scores_that_grow_along_the_prefix(D, dtype):
     # Partial sums of a score are as large as the score here (63 D^0.5 / 2 D^-0.5 ... up to 62 in units of the
     # exponent, in at most 64 fp32 steps of 2^-24 each): 62 * 64 * 2^-24 = 2^-12 of each weight.
     more = 2.0 ** -12 * vc.cpu().double().nan_to_num().abs().max()
-    o, lse = pkg.ffpa_decode_shared(*args, enable_gqa=True, return_lse=True)
+    o, lse = split(*args, enable_gqa=True, return_lse=True)
     device_ok()
     close(o, ref[0], ref[2] + more, "O")
     close(lse, ref[1], ref[3] + 2.0 ** -12, "LSE")
@@ -163,13 +170,17 @@ def test_agrees_with_decode_and_repeats():
     both = table.clone()
     both[:, :pages.numel()] = pages
     o, lse = pkg.ffpa_decode_paged(q, kc, vc, both, n, enable_gqa=True, return_lse=True)
+    one = pkg.ffpa_decode_shared(*args, enable_gqa=True, return_lse=True, kernel="single")
+    assert torch.equal(one[0], o) and torch.equal(one[1], lse)
     assert (lse - la).abs().max() < 1e-4 and (o.float() - a.float()).abs().max() < 2e-2
     ws = torch.empty(pkg.decode_shared_workspace_bytes(4, 16, 4, 512), dtype=torch.uint8, device=DEV).fill_(255)
-    c = pkg.ffpa_decode_shared(*args, enable_gqa=True, workspace=ws)
+    c = split(*args, enable_gqa=True, workspace=ws)
     assert torch.equal(a, c)
 
 
-def test_captured_lengths_may_change():
+@pytest.mark.parametrize("kernel", ["split", "single"])
+def test_captured_lengths_may_change(kernel):
+    split = functools.partial(pkg.ffpa_decode_shared, kernel=kernel)
     args, _ = make([40, 0, 300, 9], 700, 8, 2, 256, 16, BF, seed=4)
     q, kc, vc, pages, sl, table, n = args
     sl, n = sl.clone(), n.clone()
@@ -177,11 +188,11 @@ def test_captured_lengths_may_change():
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        pkg.ffpa_decode_shared(q, kc, vc, pages, sl, table, n, enable_gqa=True)
+        split(q, kc, vc, pages, sl, table, n, enable_gqa=True)
         side.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            o = pkg.ffpa_decode_shared(q, kc, vc, pages, sl, table, n, enable_gqa=True)
+            o = split(q, kc, vc, pages, sl, table, n, enable_gqa=True)
     full = n.tolist()
     for shared, lens in ((700, full), (0, full), (16, [5, 700, 0, 300]), (10 ** 6, [1, 2, 704, 33]), (350, full)):
         with torch.cuda.stream(side):
@@ -203,15 +214,17 @@ def test_nothing_shared_and_nothing_cached():
     kc = torch.empty(0, 16, 2, 64, dtype=BF, device=DEV)
     table, n = torch.zeros(2, 0, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
     none, zero = torch.empty(0, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
-    o, lse = pkg.ffpa_decode_shared(q, kc, kc, none, zero, table, n, enable_gqa=True, return_lse=True)
+    o, lse = split(q, kc, kc, none, zero, table, n, enable_gqa=True, return_lse=True)
     assert (o == 0).all() and (lse == -math.inf).all()
-    assert pkg.ffpa_decode_shared(q[:0], kc, kc, none, zero, table[:0], n[:0], enable_gqa=True).shape == (0, 4, 64)
+    assert split(q[:0], kc, kc, none, zero, table[:0], n[:0], enable_gqa=True).shape == (0, 4, 64)
     device_ok()
 
 
+@pytest.mark.parametrize("kernel", ["split", "single"])
 @pytest.mark.parametrize("D", [64, 256, 512, 768])
-def test_bad_pages_and_lengths_are_reported(D):
+def test_bad_pages_and_lengths_are_reported(D, kernel):
     """A shared page that does not exist counts as keys and values of zeros; a negative shared length as none."""
+    split = functools.partial(pkg.ffpa_decode_shared, kernel=kernel)
     args, _ = make([40, 0, 70], 200, 4, 2, D, 16, BF, seed=15)
     q, kc, vc, pages, sl, table, n = args
     kc, vc = torch.nan_to_num(kc), torch.nan_to_num(vc)
@@ -219,18 +232,18 @@ def test_bad_pages_and_lengths_are_reported(D):
     for bad in (kc.shape[0], -1, -2 ** 31, 2 ** 31 - 1):
         p2, word = pages.clone(), word_()
         p2[5] = bad
-        o = pkg.ffpa_decode_shared(q, kc, vc, p2, sl, table, n, enable_gqa=True, status=word)
+        o = split(q, kc, vc, p2, sl, table, n, enable_gqa=True, status=word)
         assert word.item() == pkg.FFPA_ERR_INVALID
         p2[5] = kc.shape[0]
-        assert torch.equal(o, pkg.ffpa_decode_shared(q, k0, v0, p2, sl, table, n, enable_gqa=True))
+        assert torch.equal(o, split(q, k0, v0, p2, sl, table, n, enable_gqa=True))
     word = word_()
     table[:, :pages.numel()] = pages
-    o = pkg.ffpa_decode_shared(q, kc, vc, pages, torch.full_like(sl, -5), table, n, enable_gqa=True, status=word)
+    o = split(q, kc, vc, pages, torch.full_like(sl, -5), table, n, enable_gqa=True, status=word)
     assert word.item() == pkg.FFPA_ERR_INVALID
-    assert torch.equal(o, pkg.ffpa_decode_shared(q, kc, vc, pages, torch.zeros_like(sl), table, n, enable_gqa=True))
+    assert torch.equal(o, split(q, kc, vc, pages, torch.zeros_like(sl), table, n, enable_gqa=True))
     n2, word = torch.tensor([-1, 200, 2 ** 31 - 1], dtype=torch.int32, device=DEV), word_()
     t2 = table.clamp(min=0)
-    o = pkg.ffpa_decode_shared(q, kc, vc, pages, sl, t2, n2, enable_gqa=True, status=word)
+    o = split(q, kc, vc, pages, sl, t2, n2, enable_gqa=True, status=word)
     assert word.item() == pkg.FFPA_ERR_INVALID and (o[0] == 0).all() and torch.isfinite(o).all()
     device_ok()
 
@@ -239,9 +252,11 @@ def test_bad_pages_and_lengths_are_reported(D):
 def test_ends_when_a_wait_runs_out(D, B):
     args, ref = make([3] * B, 500, 8, 2, D, 16, BF, seed=D)
     word = word_()
-    pkg.ffpa_decode_shared(*args, enable_gqa=True, status=word, wait_timeout_ns=3_000_000, test_drop_first_copy=True)
-    torch.cuda.synchronize()
-    assert word.item() == pkg.FFPA_ERR_DEVICE_TIMEOUT
+    for kernel in ("split", "single"):
+        word.zero_()
+        pkg.ffpa_decode_shared(*args, enable_gqa=True, status=word, kernel=kernel, wait_timeout_ns=3_000_000, test_drop_first_copy=True)
+        torch.cuda.synchronize()
+        assert word.item() == pkg.FFPA_ERR_DEVICE_TIMEOUT
     check(args, ref)
     device_ok()
 
@@ -257,4 +272,8 @@ def test_torch_operator_and_streams():
     o2 = pkg.ffpa_decode_shared(*args, enable_gqa=True, stream=side)
     side.synchronize()
     assert torch.equal(o, o2)
+    side.wait_stream(torch.cuda.current_stream())
+    o3 = split(*args, enable_gqa=True, stream=side)
+    side.synchronize()
+    close(o3, ref[0], ref[2], "O")
     device_ok()

@@ -1,6 +1,8 @@
 """Host side of the 8-bit paged cache and of decode attention behind shared pages: refusals of the C ABI
 and of the binding, operators' registration and fakes, and the references that the GPU tests use."""
+import contextlib
 import ctypes
+import functools
 import math
 
 import pytest
@@ -146,7 +148,7 @@ def test_binding_refusals(lib):
     k16, sp, sl = kc.to(BF), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     for kw, want in ((dict(q=q.half()), TypeError), (dict(k_cache=kc, v_cache=kc), TypeError), (dict(shared_pages=sp.long()), TypeError),
                      (dict(shared_pages=sp[None]), ValueError), (dict(shared_len=torch.zeros(2, dtype=torch.int32)), ValueError),
-                     (dict(shared_len=sl.long()), TypeError), (dict(block_table=table[:1]), ValueError)):
+                     (dict(shared_len=sl.long()), TypeError), (dict(kernel="both"), ValueError), (dict(block_table=table[:1]), ValueError)):
         a = dict(q=q, k_cache=k16, v_cache=k16, shared_pages=sp, shared_len=sl, block_table=table, seq_lens=lens, enable_gqa=True)
         a.update(kw)
         with pytest.raises(want):
@@ -194,3 +196,19 @@ def test_the_reference_decode_is_attention_over_the_values():
     want = torch.nn.functional.scaled_dot_product_attention(q.double().transpose(0, 1)[None], k.transpose(0, 1)[None],
                                                             v.transpose(0, 1)[None], enable_gqa=True)[0].transpose(0, 1)
     assert (o - want).abs().max() < 1e-12
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_binding_refuses_tensors_without_memory(device):
+    """The calls under the operators take tensors with memory only: traced ones (and such on no device) are refused."""
+    with FakeTensorMode() if device == "cpu" else contextlib.nullcontext():
+        e = functools.partial(torch.empty, device=device)
+        q, k, kc = e(2, 4, 128, dtype=BF), e(2, 2, 128, dtype=BF), e(3, 16, 2, 128, dtype=BF)
+        kq, ks = e(3, 16, 2, 128, dtype=E4M3), e(3, 2, 16)
+        table, lens, slots = e(2, 2, dtype=torch.int32), e(2, dtype=torch.int32), e(2, dtype=torch.int64)
+        for call in (lambda: pkg.ffpa_kv_append_fp8(q, k, k, kq, kq, ks, ks, slots),
+                     lambda: pkg.ffpa_decode_paged_fp8(q, kq, kq, ks, ks, table, lens, enable_gqa=True),
+                     lambda: pkg.ffpa_kv_read(kc, kc, table, e(3, dtype=torch.int32), 8),
+                     lambda: pkg.ffpa_decode_shared(q, kc, kc, lens, lens[:1], table, lens, enable_gqa=True)):
+            with pytest.raises(TypeError, match="memory of its own"):
+                call()
