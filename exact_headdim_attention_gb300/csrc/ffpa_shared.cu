@@ -21,6 +21,7 @@ namespace {
 struct SharedPlan {
   SharedKernel kernel;
   int ctas, per, tile_rows, n_qt, items, splits;
+  double us;                                       // the estimate, for a number of keys
   int64_t parts() const { return (int64_t)items * splits * per; }
 };
 
@@ -43,9 +44,13 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int D, int sms, long long keys) {
   int most = 2 * slots / p.items;
   if (most < 1) most = 1;
   p.splits = most;
+  p.us = 0;
   if (keys > 0) {
     const double tiles_all = (double)((keys + BN - 1) / BN);
     const double tile_us = 4.0 * BM * BN * D * p.per / p.ctas / 8.4e6, part_us = p.items * p.per * (double)BM * D * 8.0 / 6e6;
+    // Beside other launches a tile of a CTA takes longer: 6 TFLOPS (4.2 with Q streamed), at D = 64 the 1 us of its
+    // softmax.  (Cut by that estimate, B16 S4096 Hkv4 D128 took 24 us in place of 16: more parts are dear to join.)
+    const double slow_us = 4.0 * BM * BN * D * p.per / p.ctas / (D > 512 ? 4.2e6 : 6e6), real_us = slow_us > 1.0 ? slow_us : 1.0;
     double best = 0;
     for (int s = 1; s <= most && s <= tiles_all; ++s) {
       const int waves = (p.items * s + slots - 1) / slots;
@@ -54,6 +59,7 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int D, int sms, long long keys) {
       if (s == 1 || us < best) {
         best = us;
         p.splits = s;
+        p.us = waves * (longest * real_us + 3.0) + s * part_us;
       }
     }
   }
@@ -88,12 +94,16 @@ struct MergeParams {
   int B, Hq, D, group, tile_rows, tiles, splits;   // query tiles of a part (with the empty one of a last pair)
 };
 
-// Where all requests' reads of the shared keys come to no more than this, one decode over all keys reads them
-// from L2, in two launches in place of four; for one request it reads no more than the split does.  Measured, one
-// pass and split (us): 8 MB (B1 S2048 Hkv8 D128) 8.9 and 14.1, 33 MB (B16 S1010 Hkv4 D128) 12.4 and 13.8, 34 MB
-// (B4 S2048 Hkv8 D128) 11.8 and 14.7, 67 MB (B16 S2048 Hkv4 D128) 14.6 and 15.0, 134 MB (B64 S1024 Hkv4 D128) 21.3
-// and 19.2, 537 MB (B8 S4096 Hkv8 D512) 56.7 and 29.6; B1 S16384 Hkv8 D512 46.1 and 57.7.
-constexpr double ONE_PASS_BYTES = 64e6;
+// One decode over all keys of each request takes two launches in place of four, and its reads of the shared keys
+// come from L2 but for the first; for one request they are no more than the split's.  It is taken where the estimates
+// say so.  Measured, one pass and split (us): B2 S5003 Hkv4 D1024 32 and 48, B2 S18858 Hkv1 D512 17 and 30, B3 S3305 Hkv8
+// D128 13.7 and 16.6, B4 S30111 Hkv4 D64 20 and 27.5, B16 S1010 Hkv4 D128 12.4 and 13.8, B8 S1024 Hkv8 D512 23 and 19.5,
+// B4 S8192 Hkv8 D256 36 and 25, B16 S3353 Hkv2 D512 29 and 21; of 134 such sizes the estimates take the slower way
+// for 10, eight of them by 9 % or less, B2 S16384 Hkv8 D512 by 16 %, B32 S950 Hkv8 D64 by 24 %.
+bool one_pass(int B, int Hkv, int D, double keys, const SharedPlan& split) {
+  return B == 1 || 9.0 + B * Hkv * keys * D * 4.0 / 10.6e6 <= 10.0 + split.us;
+}
+
 constexpr int MERGE_WARPS = 4;
 constexpr int MERGE_FLIGHT = 8;   // parts on their way
 constexpr float LOG2E = 1.4426950408889634f;
@@ -185,7 +195,8 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
   float sc = 0.0f;
   ffpa_status st = check_decode(DECODE_OWN, dt, shape, scale, enable_gqa, &sc);
   if (st != FFPA_OK) return st;
-  if (n_shared < 0) return FFPA_ERR_INVALID;
+  const int way = options ? options->kernel : FFPA_VARIANT_AUTO;
+  if (n_shared < 0 || (way != FFPA_VARIANT_AUTO && way != FFPA_VARIANT_SINGLE && way != FFPA_VARIANT_SPLIT)) return FFPA_ERR_INVALID;
   if (D % 64 != 0 || page_size % 8 != 0 || Hq / Hkv > BM) return FFPA_ERR_UNSUPPORTED;
   if (B == 0) return FFPA_OK;
   st = check_decode_rows(DECODE_OWN, shape, q, k_cache, v_cache, o, lse, q_str, o_str, block_table, table_str, seq_lens, workspace);
@@ -227,9 +238,8 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
   P.shared_len = shared_len;
   P.shared_table = shared_pages;
   P.shared_pages = pages;
-  const int way = options ? options->kernel : FFPA_VARIANT_AUTO;
   if (way == FFPA_VARIANT_SINGLE ||
-      (way == FFPA_VARIANT_AUTO && (B == 1 || (double)B * Hkv * D * 4 * pages * page_size <= ONE_PASS_BYTES))) {
+      (way == FFPA_VARIANT_AUTO && one_pass(B, Hkv, D, (double)pages * page_size, pl))) {
     P.o = static_cast<char*>(o);
     P.lse = lse;
     P.o_sb = o_str[0] * 2;

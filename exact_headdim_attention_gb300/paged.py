@@ -296,7 +296,7 @@ def ffpa_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     block_table are not read, and a request of fewer keys sees that many.  D a multiple of 64, page_size
     of 8.  kernel: "single" decodes over all keys of each request in one pass (the shared pages are read
     for every request: a few, or short ones), "split" reads the shared keys apart; None chooses by the
-    batch and the number of shared_pages.  Other arguments and the result as for ffpa_decode_paged;
+    sizes and the number of shared_pages.  Other arguments and the result as for ffpa_decode_paged;
     workspace: of decode_shared_workspace_bytes(...) bytes."""
     if stream is not None:
         need = decode_shared_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2])

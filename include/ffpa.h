@@ -130,7 +130,7 @@ typedef struct ffpa_options {
   int* status;
   /* Time limit of every in-kernel wait, in nanoseconds; 0 = 2e9 (2 s). */
   uint64_t wait_timeout_ns;
-  /* FFPA_VARIANT_* (forward only); any other value is FFPA_ERR_INVALID. */
+  /* FFPA_VARIANT_* (forward and ffpa_decode_shared only); any other value is FFPA_ERR_INVALID. */
   int kernel;
   /* TEST HOOK, not for production use: nonzero makes this call's kernels
    * skip the first tensor copy of each CTA, so that the pipeline wait that
@@ -703,10 +703,10 @@ ffpa_status ffpa_kv_read(const void* k_cache, const void* v_cache, const float* 
  * up to the order of the sums; a softmax weight of a shared key enters them as a 16-bit
  * value (bf16: off by 2^-8 of itself, fp16: by 2^-11, or by 2^-32 of the largest) and all else in fp32.
  * D a multiple of 64 from 64 to 1024, page_size a multiple of 8 (else FFPA_ERR_UNSUPPORTED).
- * options->kernel: FFPA_VARIANT_AUTO chooses, by the batch and n_shared, between reading the
+ * options->kernel: FFPA_VARIANT_AUTO chooses, by the sizes and n_shared, between reading the
  * shared keys apart from the requests' own and (where that is little) one pass over all keys of
- * each request; FFPA_VARIANT_SINGLE always takes the one pass (as exact as ffpa_decode_paged), another value
- * never.  Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
+ * each request; FFPA_VARIANT_SINGLE always takes the one pass (as exact as ffpa_decode_paged),
+ * FFPA_VARIANT_SPLIT never; other values are FFPA_ERR_INVALID.  Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
  */
 size_t ffpa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D);
 ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,

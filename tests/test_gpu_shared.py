@@ -206,7 +206,9 @@ def test_captured_lengths_may_change(kernel):
     device_ok()
 
 
-def test_nothing_shared_and_nothing_cached():
+@pytest.mark.parametrize("kernel", ["split", "single", None])
+def test_nothing_shared_and_nothing_cached(kernel):
+    split = functools.partial(pkg.ffpa_decode_shared, kernel=kernel)
     args, ref = make([40, 3], 0, 4, 2, 128, 16, BF, seed=5)
     assert args[3].numel() == 0
     check(args, ref)

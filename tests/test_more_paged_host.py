@@ -11,6 +11,7 @@ from torch._subclasses.fake_tensor import FakeTensorMode
 
 import exact_headdim_attention_gb300 as pkg
 from exact_headdim_attention_gb300 import build as bld
+from exact_headdim_attention_gb300._binding import Options
 from tests import paged_fp8_oracle as p8
 from tests.test_paged_host import FAKE, arr, rope_arg
 
@@ -54,12 +55,13 @@ def read_call(lib, dt=0, T=20, B=2, Hkv=2, D=128, pages=8, page=16, width=4, kc=
 
 
 def shared_call(lib, dt=0, B=2, Hq=4, Hkv=2, D=128, pages=8, page=16, width=4, n=3, q=FAKE, k=FAKE, o=FAKE, sp=FAKE, sl=FAKE, table=FAKE,
-                table_str=4, lens=FAKE, q_str=None, scale=None, gqa=1, ws=FAKE, ws_bytes=1 << 30):
+                table_str=4, lens=FAKE, q_str=None, scale=None, gqa=1, ws=FAKE, ws_bytes=1 << 30,
+                kernel=0):
     q_str = q_str or arr(Hq * D, D, 1)
     k_str = arr(page * Hkv * D, Hkv * D, D, 1)
     sc = None if scale is None else ctypes.byref(ctypes.c_float(scale))
     return lib.ffpa_decode_shared(q, k, FAKE, o, None, dt, B, Hq, Hkv, D, pages, page, width, n, q_str, k_str, k_str, q_str, sp, sl, table,
-                                  table_str, lens, sc, gqa, ws, ws_bytes, None, None)
+                                  table_str, lens, sc, gqa, ws, ws_bytes, None, ctypes.byref(Options(None, 0, kernel, 0)))
 
 
 def test_decode_fp8_refusals(lib):
@@ -101,7 +103,8 @@ def test_shared_refusals(lib):
                      (dict(Hq=258, Hkv=2), UNSUPPORTED), (dict(n=-1), INVALID), (dict(B=-1), INVALID), (dict(Hq=5), INVALID), (dict(gqa=0), INVALID),
                      (dict(sp=None), INVALID), (dict(sl=None), INVALID), (dict(sp=FAKE + 2), INVALID), (dict(sl=FAKE + 1), INVALID),
                      (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(o=None), INVALID), (dict(lens=None), INVALID), (dict(table=None), INVALID),
-                     (dict(ws=None), INVALID), (dict(ws=FAKE + 16), INVALID), (dict(q_str=arr(512, 132, 1)), INVALID), (dict(scale=math.nan), INVALID)):
+                     (dict(ws=None), INVALID), (dict(ws=FAKE + 16), INVALID), (dict(q_str=arr(512, 132, 1)), INVALID), (dict(scale=math.nan), INVALID),
+                     (dict(kernel=-1), INVALID), (dict(kernel=2), INVALID), (dict(kernel=4), INVALID), (dict(kernel=5), INVALID)):
         assert shared_call(lib, **kw) == want, kw
     assert shared_call(lib, B=0) == OK
     need = pkg.decode_shared_workspace_bytes(2, 4, 2, 128)
@@ -148,7 +151,7 @@ def test_binding_refusals(lib):
     k16, sp, sl = kc.to(BF), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     for kw, want in ((dict(q=q.half()), TypeError), (dict(k_cache=kc, v_cache=kc), TypeError), (dict(shared_pages=sp.long()), TypeError),
                      (dict(shared_pages=sp[None]), ValueError), (dict(shared_len=torch.zeros(2, dtype=torch.int32)), ValueError),
-                     (dict(shared_len=sl.long()), TypeError), (dict(kernel="both"), ValueError), (dict(block_table=table[:1]), ValueError)):
+                     (dict(shared_len=sl.long()), TypeError), (dict(kernel="both"), ValueError), (dict(kernel="dual"), ValueError), (dict(block_table=table[:1]), ValueError)):
         a = dict(q=q, k_cache=k16, v_cache=k16, shared_pages=sp, shared_len=sl, block_table=table, seq_lens=lens, enable_gqa=True)
         a.update(kw)
         with pytest.raises(want):
