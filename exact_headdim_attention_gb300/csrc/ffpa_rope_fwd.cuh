@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
       issue();
       const float sum = row_sum<LPR>(sq.x + sq.y);
       if (E4M3 && codes) {
-        // Codes do not depend on the row's norm: it goes into the scale alone.
+        // Codes do not depend on the row's norm: it goes into the scale alone (but in the smallest rows).
         float2 y[ITER][VEC];
         float top = 0.0f;
         if (on) {
@@ -287,17 +287,28 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
               *reinterpret_cast<Raw<VEC>*>(dst + ch[k].b * 2) = narrow<F16, VEC>(y[k] + VEC / 2);
             }
         } else {
-          // (the smallest scale is a normal number, and its inverse finite)
           constexpr float least = 0x1p-117f;
           const float whole = top * r;
-          const float f = top == 0.0f ? 1.0f : whole < least ? r * (448.0f / least) : 448.0f / top;
+          float f = 448.0f / top, scale = whole * (1.0f / 448.0f);
+          // Rows whose factor or scale would leave the normal range, zeros among them: the norm's factor goes
+          // into the row first, and the smallest scale is a normal number whose inverse is finite.
+          if (fminf(top, whole) < least) {
+            if (top != 0.0f) {
+#pragma unroll
+              for (int k = 0; k < ITER; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) y[k][i] = mul2(y[k][i], make_float2(r, r));
+            }
+            f = top == 0.0f ? 1.0f : 448.0f / fmaxf(whole, least);
+            scale = top == 0.0f ? 1.0f : fmaxf(whole, least) * (1.0f / 448.0f);
+          }
 #pragma unroll
           for (int k = 0; k < ITER; ++k)
             if (ch[k].live) {
               store_codes<VEC>(dst + ch[k].a, y[k], f);
               store_codes<VEC>(dst + ch[k].b, y[k] + VEC / 2, f);
             }
-          if (lane == 0) *dst_scale = top == 0.0f ? 1.0f : fmaxf(whole, least) * (1.0f / 448.0f);
+          if (lane == 0) *dst_scale = scale;
           dst_scale += scale_h;
         }
         dst += dst_h;
