@@ -290,9 +290,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
           constexpr float least = 0x1p-117f;
           const float whole = top * r;
           float f = 448.0f / top, scale = whole * (1.0f / 448.0f);
-          // Rows whose factor or scale would leave the normal range, zeros among them: the norm's factor goes
-          // into the row first, and the smallest scale is a normal number whose inverse is finite.
-          if (fminf(top, whole) < least) {
+          // Rows whose factor or scale would leave the normal range, zeros and those that the norm makes NaN
+          // among them: the norm's factor goes into the row first, and the smallest scale is a normal number
+          // whose inverse is finite.  (A NaN spreads through the norm; an infinity has the norm's factor 0.)
+          if (top < least || !(whole >= least)) {
             if (top != 0.0f) {
 #pragma unroll
               for (int k = 0; k < ITER; ++k)
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, rope_blocks<VEC, ITER>()) rope_k
                 for (int i = 0; i < VEC; ++i) y[k][i] = mul2(y[k][i], make_float2(r, r));
             }
             f = top == 0.0f ? 1.0f : 448.0f / fmaxf(whole, least);
-            scale = top == 0.0f ? 1.0f : fmaxf(whole, least) * (1.0f / 448.0f);
+            scale = whole > 0.0f ? fmaxf(whole, least) * (1.0f / 448.0f) : r == r ? 1.0f : r;
           }
 #pragma unroll
           for (int k = 0; k < ITER; ++k)

@@ -628,7 +628,8 @@ ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_
  *     scale = a / 448,   codes = e4m3(y * (448 / a))
  *
  * in fp32, codes rounded to nearest even (a row of zeros: scale 1; one with a < 2^-117: that of a = 2^-117;
- * a NaN stays one; a row with an infinity has an infinite scale).  Each code is off by at
+ * a NaN stays one; a row with an infinity has an infinite scale; as the norm makes a row with a NaN
+ * all NaN, its scale is NaN too, and one with an infinity zeros but for a NaN there).  Each code is off by at
  * most 2^-4 of its value, or 2^-10 scales.  The rows are not rounded to 16 bits
  * before.  Arguments and checks otherwise as for ffpa_kv_append.
  */

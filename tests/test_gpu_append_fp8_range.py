@@ -1,5 +1,5 @@
 """Rows at the ends of the range going into the paged cache of 8 bits a value, on the GPU: the smallest
-normed rows against the 64-bit definition."""
+normed rows against the 64-bit definition, rows with NaN and infinities against the 16-bit append."""
 import pytest
 import torch
 
@@ -79,3 +79,41 @@ def test_smallest_weighted_rows(D, rot):
     k[..., 1::7] = 0.0
     case = rows_case(k, k.clone(), rot, True, HF, D, w_size=2.0 ** -100)
     check_small(case, run_append(case, 16, 2))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D,rot", [(64, 0), (80, 40), (128, 128), (512, 256), (1024, 0)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_rows_with_nan_and_infinities(norm, D, rot, dtype):
+    """Codes are NaN where the 16-bit append's row is not finite, and there alone.  The scale of a row with a NaN is
+    NaN with the norm; of one with an infinity 1 with the norm (it leaves zeros) and infinite without."""
+    g = torch.Generator().manual_seed(D)
+    k = torch.randn(7, 2, D, generator=g).to(dtype)
+    k[1, 0, 3] = torch.nan
+    k[2, 1, D - 1] = torch.inf
+    k[3, 0, 5], k[3, 0, 0] = -torch.inf, torch.inf
+    k[4, 1, 2], k[4, 1, 9] = torch.nan, torch.inf
+    k[5] = torch.nan
+    case = rows_case(k, k.clone(), rot, norm, dtype, D)
+    _, kc, vc, ks, vs, word = run_append(case, 16, 1)
+    assert word == pkg.FFPA_OK
+    q, _, v, pos, inv, w, slots = case
+    d = lambda t: None if t is None else t.to("cuda:0")   # noqa: E731
+    x16 = torch.zeros(2, 1, 16, 2, D, dtype=dtype, device="cuda:0")
+    pkg.ffpa_kv_append(d(q), d(k), d(v), x16[0], x16[1], d(slots), d(pos) if rot else None, d(inv), d(w[0]), d(w[1]))
+    torch.cuda.synchronize()
+    for cache, scale, x, normed in ((kc, ks, x16[0], norm), (vc, vs, x16[1], False)):
+        codes, scale = stored(cache, scale, 7)
+        codes, x = codes.float(), x[0, :7].float().cpu()
+        bad = ~torch.isfinite(x)
+        assert torch.equal(torch.isnan(codes), bad)
+        nan, endless = torch.isnan(k).any(-1), torch.isinf(k).any(-1)
+        some = nan | endless
+        if normed:
+            assert torch.isnan(scale[nan]).all() and (scale[endless & ~nan] == 1).all()
+            assert (codes[some.unsqueeze(-1) & ~bad] == 0).all()
+        else:
+            assert torch.isinf(scale[torch.isinf(x).any(-1)]).all()
+            assert (codes[torch.isinf(x).any(-1, keepdim=True) & ~bad] == 0).all()
+            assert (scale[bad.all(-1) & nan & ~endless] == 1).all()
+        assert torch.isfinite(scale[~some]).all() and (scale[~some] > 0).all()
