@@ -59,7 +59,7 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int D, int sms, long long keys) {
       if (s == 1 || us < best) {
         best = us;
         p.splits = s;
-        p.us = waves * (longest * real_us + 3.0) + s * part_us;
+        p.us = waves * (longest * real_us + 3.0) + s * (part_us + 0.1);   // (the merge of a row takes its parts in turn)
       }
     }
   }
@@ -95,13 +95,17 @@ struct MergeParams {
 };
 
 // One decode over all keys of each request takes two launches in place of four, and its reads of the shared keys
-// come from L2 but for the first; for one request they are no more than the split's.  It is taken where the estimates
-// say so.  Measured, one pass and split (us): B2 S5003 Hkv4 D1024 32 and 48, B2 S18858 Hkv1 D512 17 and 30, B3 S3305 Hkv8
-// D128 13.7 and 16.6, B4 S30111 Hkv4 D64 20 and 27.5, B16 S1010 Hkv4 D128 12.4 and 13.8, B8 S1024 Hkv8 D512 23 and 19.5,
-// B4 S8192 Hkv8 D256 36 and 25, B16 S3353 Hkv2 D512 29 and 21; of 134 such sizes the estimates take the slower way
-// for 10, eight of them by 9 % or less, B2 S16384 Hkv8 D512 by 16 %, B32 S950 Hkv8 D64 by 24 %.
-bool one_pass(int B, int Hkv, int D, double keys, const SharedPlan& split) {
-  return B == 1 || 9.0 + B * Hkv * keys * D * 4.0 / 10.6e6 <= 10.0 + split.us;
+// come from L2 but for the first: 10.6 TB/s with up to 8 heads a key head; more take one CTA an SM, 5.6 TB/s, and above
+// 16 heads every pass of 16 reads the keys again.  One request in one pass reads no more than the split.  It is taken where the
+// estimates say so.  Measured, one pass and split (us): B2 S5003 Hkv4 D1024 32 and 48, B2 S18858 Hkv1 D512 17 and 30, B3 S3305
+// Hkv8 D128 13.7 and 16.6, B4 S30111 Hkv4 D64 20 and 27.5, B16 S1010 Hkv4 D128 12.4 and 13.8, B8 S1024 Hkv8 D512 23 and 19.5,
+// B4 S8192 Hkv8 D256 36 and 25, B16 S3353 Hkv2 D512 29 and 21; of one key head with 128 heads, B1 S31552 D512 98 and 35,
+// B16 S54432 D192 1007 and 114.  Of 34916 sizes (1 to 4 key heads, groups of 1 to 128, B 1 to 32, 512 to 65536 shared keys) the
+// estimates take a way that is more than 10 % slower for 3 %, more than 25 % for 0.8 %, 1.7 times as slow at most.
+bool one_pass(int B, int Hkv, int group, int D, double keys, const SharedPlan& split) {
+  const int heads = 8 * decode_nt(group), passes = (group + heads - 1) / heads;
+  if (B == 1 && passes == 1) return true;          // (at most 4 % slower than the split in 4016 sizes)
+  return 9.0 + B * Hkv * passes * keys * D * 4.0 / (heads == 8 ? 10.6e6 : 5.6e6) <= 10.0 + split.us;
 }
 
 constexpr int MERGE_WARPS = 4;
@@ -239,7 +243,7 @@ ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v
   P.shared_table = shared_pages;
   P.shared_pages = pages;
   if (way == FFPA_VARIANT_SINGLE ||
-      (way == FFPA_VARIANT_AUTO && one_pass(B, Hkv, D, (double)pages * page_size, pl))) {
+      (way == FFPA_VARIANT_AUTO && one_pass(B, Hkv, Hq / Hkv, D, (double)pages * page_size, pl))) {
     P.o = static_cast<char*>(o);
     P.lse = lse;
     P.o_sb = o_str[0] * 2;
