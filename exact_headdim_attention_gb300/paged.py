@@ -295,8 +295,10 @@ def ffpa_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     seq_lens are those of ffpa_decode_paged, the shared keys included; the entries of the shared pages in
     block_table are not read, and a request of fewer keys sees that many.  D a multiple of 64, page_size
     of 8.  kernel: "single" decodes over all keys of each request in one pass (the shared pages are read
-    for every request: a few, or short ones), "split" reads the shared keys apart; None chooses by the
-    sizes and the number of shared_pages.  Other arguments and the result as for ffpa_decode_paged;
+    for every request: a few, or short ones), as exact as ffpa_decode_paged; "split" reads the shared keys
+    apart, and a softmax weight of one enters the sums as one 16-bit value, as in ffpa_fwd; None chooses by the
+    sizes and the number of shared_pages, so that a request's last bits depend on the batch that it is in.
+    Other arguments and the result as for ffpa_decode_paged;
     workspace: of decode_shared_workspace_bytes(...) bytes."""
     if stream is not None:
         need = decode_shared_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2])

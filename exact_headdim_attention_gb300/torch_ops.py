@@ -391,14 +391,14 @@ def _decode_paged_fp8_fake(q, k_cache, v_cache, k_scale, v_scale, block_table, s
 @torch.library.custom_op("ffpa::decode_shared", mutates_args=())
 def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, shared_pages: torch.Tensor,
                   shared_len: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, scale: Optional[float],
-                  enable_gqa: bool) -> tuple[torch.Tensor, torch.Tensor]:
+                  enable_gqa: bool, kernel: Optional[str] = None) -> tuple[torch.Tensor, torch.Tensor]:
     """O [B,Hq,D] and LSE [B,Hq] (fp32) of one new token per request behind shared pages."""
     return paged.ffpa_decode_shared(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale=scale,
-                                    enable_gqa=enable_gqa, return_lse=True)
+                                    enable_gqa=enable_gqa, return_lse=True, kernel=kernel)
 
 
 @decode_shared.register_fake
-def _decode_shared_fake(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale, enable_gqa):
+def _decode_shared_fake(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale, enable_gqa, kernel=None):
     return _decode_paged_fake(q, k_cache, v_cache, block_table, seq_lens, scale, enable_gqa)
 
 
@@ -443,10 +443,10 @@ def ffpa_attn_decode_fp8_func(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
 def ffpa_attn_decode_shared_func(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                  shared_pages: torch.Tensor, shared_len: torch.Tensor, block_table: torch.Tensor,
                                  seq_lens: torch.Tensor, scale: Optional[float] = None, enable_gqa: bool = False, *,
-                                 return_lse: bool = False):
+                                 return_lse: bool = False, kernel: Optional[str] = None):
     """Attention of one new token per request behind shared pages (see paged.ffpa_decode_shared)."""
     o, lse = torch.ops.ffpa.decode_shared(q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, scale,
-                                          bool(enable_gqa))
+                                          bool(enable_gqa), kernel)
     return (o, lse) if return_lse else o
 
 

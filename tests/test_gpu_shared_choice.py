@@ -34,3 +34,16 @@ def test_the_faster_way_is_taken(way, B, Hq, Hkv, D, shared):
     o = {w: pkg.ffpa_decode_shared(*args, enable_gqa=Hq != Hkv, kernel=w) for w in ("single", "split", None)}
     assert not torch.equal(o["single"], o["split"])
     assert torch.equal(o[None], o[way])
+
+
+@pytest.mark.parametrize("way", ["single", "split"])
+def test_a_traced_model_chooses_the_way(way):
+    """The operator takes the way that its caller names, traced too, whatever the sizes would take."""
+    args = call(4, 8, 2, 128, 512)
+    want = pkg.ffpa_decode_shared(*args, enable_gqa=True, kernel=way)
+    assert torch.equal(pkg.ffpa_attn_decode_shared_func(*args, enable_gqa=True, kernel=way), want)
+    step = torch.compile(lambda q: pkg.ffpa_attn_decode_shared_func(q * 1, *args[1:], enable_gqa=True, kernel=way),
+                         backend="eager", fullgraph=True)
+    assert torch.equal(step(args[0]), want)
+    with pytest.raises(ValueError):
+        pkg.ffpa_attn_decode_shared_func(*args, enable_gqa=True, kernel="both")
