@@ -577,8 +577,8 @@ __device__ __forceinline__ void write_columns(char* out, int64_t o_sh, int heads
 // One head's queries as fp16 operands of the first product with e4m3 keys, by a warp: of
 // 32 columns, lane 4 head + c of a matrix load gets columns 4 c .. 4 c + 3 of either half; the
 // first two of each are column pair c of one step of 16, the others of the next.  bf16 queries
-// come in units of a power of two that lifts the largest to 2^14 .. 2^15: exact from 2^-28 of it on
-// and off by 2^-40 of it below.
+// come in units of a power of two that lifts the largest of the row to 2^14 .. 2^15: exact from 2^-31 of it on
+// and off by 2^-39 of it below.
 template <bool F16>
 __device__ __forceinline__ void bring_queries(const char* q, bool there, int D, char* query_s, int step, int head, float* unit) {
   const int lane = threadIdx.x % 32;

@@ -645,8 +645,8 @@ ffpa_status ffpa_kv_append_fp8(const void* q, const void* k, const void* v, void
  * ffpa_decode_paged over such a cache: the attention of the values that the codes
  * stand for.  Scales are not negative; any size of them is taken (a weight times a
  * scale enters the sums to 2^-21 of itself (bf16: to 2^-11), or to 2^-40 of the largest; scales below
- * 2^-105 lose some of that).  q enters the scores exactly, or (bf16) to 2^-40 of
- * the largest of 128 of its columns.
+ * 2^-105 lose some of that).  q enters the scores exactly, or (bf16) to 2^-39 of
+ * the largest of its row's columns.
  * Arguments, checks and workspace otherwise as for ffpa_decode_paged (the workspace
  * sizes are the same).
  */
