@@ -309,6 +309,9 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
       page = page_of<KIND>(P, p.b, j, shared);
     }
   };
+  // L2 fetches 256 bytes at a time: where a head's row is shorter, the next head's comes with it and has to stay
+  // until it is asked for (loads that leave first, B32 Hq64 Hkv2 D64 of 8192 keys 63 -> 79 us, B8 Hkv8 D64 of 16666 64 -> 70).
+  const bool alone = P.Hkv == 1 || P.D * cache_bytes(KIND) >= 256;
   const uint64_t once = once_policy();
   look_up(at);
   int slot = 0, i = 0;
@@ -330,8 +333,10 @@ __device__ __forceinline__ void produce_boxes(const DecodeParams& P, int T, int 
     __syncwarp();
     if (mine) {
       const uint32_t dst = ring + slot * stage + to;
-      if (P.box_chunks == 1)
+      if (P.box_chunks == 1 && alone)
         tma_load_4d(dst, map, bar, chunk * 64, y, head, z, once);
+      else if (P.box_chunks == 1)
+        tma_load_4d(dst, map, bar, chunk * 64, y, head, z);
       else
         tma_load_5d(dst, map, bar, 0, y, 0, head, z, once);
     }
