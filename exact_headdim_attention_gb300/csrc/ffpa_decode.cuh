@@ -1097,7 +1097,8 @@ __global__ void __launch_bounds__(DEC_THREADS, decode_ctas(NT)) decode_kernel(co
 #pragma unroll
           for (int j = 0; j < 2 * KSTEPS; ++j) {
             // An output of bf16 is rounded to 2^-8 of itself; one fp16 value of a weight, off by 2^-11, adds 1 % to
-            // that error (B16 Hkv4 D1024 of 2000 keys 51 -> 50 us).
+            // that error.  With two (L2 flushed before each): B128 Hkv16 D128 of up to 2048 keys 138 -> 145 us, one key head
+            // and 16 heads of D256 53 -> 57.5, B1 D512 16.4 -> 17.2, B16 Hkv4 D1024 of 2000 58 -> 60, B32 Hkv8 D512 the same.
             if (TWO)
               split2<true>(x[j].x * lift, x[j].y * lift, pf[j >> 1][n][j & 1], pr[j >> 1][n][j & 1]);
             else

@@ -14,9 +14,10 @@
 //    SM are in flight, which the memory's latency takes (with loads into
 //    registers, one row at a time read and wrote 3.1 TB/s, four at a time 3.9).
 //  - e4m3: a row's lanes hold it in fp32 when its largest value is known (one
-//    more maximum over the lanes), so it is still read and written once.  Bound by issue slots
-//    (59 to 61 %) beside the memory: T16001 Hq16 Hkv4 D256, half the head rotated, 75 us, 4.8 TB/s; T5000 of 32 heads
-//    of D128 as they are 39.5 us, 5.2 TB/s.
+//    more maximum over the lanes), so it is still read and written once.  Bound by a row's chain
+//    (copy, products, maximum, division, codes), with too few rows on their way to cover it: issue slots are 59 to 61 % busy and
+//    the memory at 72 to 78 % of its rate.  T16001 Hq16 Hkv4 D256, half the head rotated, 75 us, 4.8 TB/s; T5000 of 32 heads
+//    of D128 as they are 39.5 us, 5.2 TB/s; T16384 of 8 and 8 heads D128 42 us, D320 (T8192) 73.
 #include "ffpa_rope.cuh"
 
 namespace ffpa {

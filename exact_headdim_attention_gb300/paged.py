@@ -298,8 +298,8 @@ def ffpa_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     for every request: a few, or short ones), as exact as ffpa_decode_paged; "split" reads the shared keys
     apart, and a softmax weight of one enters the sums as one 16-bit value, as in ffpa_fwd; None chooses by the
     sizes and the number of shared_pages, so that a request's last bits depend on the batch that it is in.
-    Other arguments and the result as for ffpa_decode_paged;
-    workspace: of decode_shared_workspace_bytes(...) bytes."""
+    Entries of shared_pages beyond shared_len cost some time, but are not read.  Other arguments and the result as for
+    ffpa_decode_paged; workspace: of decode_shared_workspace_bytes(...) bytes."""
     if stream is not None:
         need = decode_shared_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2])
         workspace = _on_stream(workspace, need, q, stream)

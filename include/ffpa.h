@@ -631,7 +631,8 @@ ffpa_status ffpa_kv_append(const void* q, const void* k, const void* v, void* q_
  * a NaN stays one; a row with an infinity has an infinite scale; as the norm makes a row with a NaN
  * all NaN, its scale is NaN too, and one with an infinity zeros but for a NaN there).  Each code is off by at
  * most 2^-4 of its value, or 2^-10 scales.  The rows are not rounded to 16 bits
- * before.  Arguments and checks otherwise as for ffpa_kv_append.
+ * before.  (The norm's factor cancels in y / a and enters the scale alone but in the smallest rows, so a
+ * value at the middle of two codes, within fp32's rounding, may become either.)  Arguments and checks otherwise as for ffpa_kv_append.
  */
 ffpa_status ffpa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
                                float* k_scale, float* v_scale, ffpa_dtype dt, int T, int Hq, int Hkv, int D,
@@ -707,7 +708,9 @@ ffpa_status ffpa_kv_read(const void* k_cache, const void* v_cache, const float* 
  * options->kernel: FFPA_VARIANT_AUTO chooses, by the sizes and n_shared, between reading the
  * shared keys apart from the requests' own and (where that is little) one pass over all keys of
  * each request; FFPA_VARIANT_SINGLE always takes the one pass (as exact as ffpa_decode_paged),
- * FFPA_VARIANT_SPLIT never; other values are FFPA_ERR_INVALID.  Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
+ * FFPA_VARIANT_SPLIT never; other values are FFPA_ERR_INVALID.  A call with more shared_pages than shared_len
+ * fills is planned for all of them: with 16384 keys' pages and none shared, B64 Hq32 Hkv8 D512 of 300 keys each takes
+ * 66 us in place of 56.  Other checks as for ffpa_decode_paged.  No allocation, no synchronisation.
  */
 size_t ffpa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D);
 ffpa_status ffpa_decode_shared(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
